@@ -24,6 +24,11 @@ Power-of-two (E8M0) scales, group 32 or 128 (scales are uint8 tensors):
 K-block-major scale variants (the layout of mode 'act_km'):
   quantize_act_kmajor, quantize_act_transposed_kmajor, quantize_act_dual_kmajor,
   quantize_mx_act_dual_kmajor
+Between the QKV and output projections (include/bfp8_attention.h; module attention):
+  rope_table(length, rot_dim, ...)     -> f32 [length][rot_dim/2][2]
+  rope(x, table, positions, ...)       -> x with its heads' pairs turned (or turned back)
+  attention_forward(q, k, v, ...)      -> (o bf16 [T][H][D], lse f32 [H][T])
+  attention_backward(dout, q, k, v, o, lse, ...) -> (dq, dk, dv)
 """
 
 import ctypes
@@ -53,6 +58,11 @@ __all__ = [
     "quantize_mx_weight",
     "quantize_mx_weight_batch",
     "gemm_mx",
+    "rope_table",
+    "rope",
+    "attention_forward",
+    "attention_backward",
+    "attention_workspace_bytes",
     "lib",
     "BFP8Error",
     "STATUS",
@@ -80,6 +90,26 @@ _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _int = ctypes.c_int
 
+
+class WeightJob(ctypes.Structure):
+    """bfp8_weight_job, and bfp8_mx_weight_job (the same layout; s points at
+    E8M0 bytes there)."""
+    _fields_ = [("w", _vp), ("rows", _i64), ("cols", _i64), ("ldw", _i64), ("q", _vp),
+                ("ldq", _i64), ("s", _vp)]
+
+
+class AttentionShape(ctypes.Structure):
+    """bfp8_attention_shape."""
+    _fields_ = [("batch", _i64), ("total_q", _i64), ("total_k", _i64), ("cu_q", _vp),
+                ("cu_k", _vp), ("k_lens", _vp), ("heads", _int), ("kv_heads", _int),
+                ("head_dim", _int), ("causal", _int), ("scale", ctypes.c_float)]
+
+
+class Heads(ctypes.Structure):
+    """bfp8_heads and bfp8_heads_out."""
+    _fields_ = [("data", _vp), ("row", _i64), ("head", _i64)]
+
+
 _SIGNATURES = {
     "bfp8_quantize_act": [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _vp],
     "bfp8_quantize_act_transposed": [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _vp],
@@ -105,24 +135,25 @@ _SIGNATURES = {
                      _i64, _vp, ctypes.c_size_t, _vp],
     "bfp8_gemm_static_scratch": [_int, _i64, _i64, _i64, _vp, _i64, _vp, _int, _vp, _i64, _vp,
                                  _int, _vp, _i64, _vp],
+    "bfp8_rope_table": [_vp, _i64, _int, ctypes.c_double, _int, ctypes.c_double, _i64, _vp],
+    "bfp8_rope": [_vp, _i64, _i64, _vp, _i64, _i64, _int, _i64, _i64, _int, _int, _int, _vp, _i64,
+                  _vp, _int, _vp],
+    "bfp8_attention_workspace_bytes": [ctypes.POINTER(AttentionShape), _int],
+    "bfp8_attention_forward": [ctypes.POINTER(AttentionShape), Heads, Heads, Heads, Heads, _vp,
+                               _vp, ctypes.c_size_t, _vp],
+    "bfp8_attention_backward": [ctypes.POINTER(AttentionShape), Heads, Heads, Heads, Heads, _vp,
+                                Heads, Heads, Heads, Heads, _vp, ctypes.c_size_t, _vp],
     "bfp8_status_str": [_int],
     "bfp8_abi_version": [],
 }
 _RESTYPES = {
     "bfp8_gemm_workspace_bytes": ctypes.c_size_t,
+    "bfp8_attention_workspace_bytes": ctypes.c_size_t,
     "bfp8_status_str": ctypes.c_char_p,
 }
 
 MAX_WEIGHT_JOBS = 16  # BFP8_MAX_WEIGHT_JOBS
 STATIC_SCRATCH_BYTES = 64 << 20  # BFP8_STATIC_SCRATCH_BYTES
-
-
-class WeightJob(ctypes.Structure):
-    """bfp8_weight_job, and bfp8_mx_weight_job (the same layout; s points at
-    E8M0 bytes there)."""
-    _fields_ = [("w", _vp), ("rows", _i64), ("cols", _i64), ("ldw", _i64), ("q", _vp),
-                ("ldq", _i64), ("s", _vp)]
-
 
 _lib = None
 
@@ -504,3 +535,7 @@ def gemm_mx(layout: str, qa, sa, qb, sb, mode_a: str = "act", mode_b: str = "blo
         qb.data_ptr(), qb.stride(0), sb.data_ptr(), MODES[mode_b], out.data_ptr(),
         out.stride(0), workspace.data_ptr() if ws_bytes else None, ws_bytes, _stream(qa)))
     return out
+
+
+from .attention import (attention_backward, attention_forward,  # noqa: E402
+                        attention_workspace_bytes, rope, rope_table)

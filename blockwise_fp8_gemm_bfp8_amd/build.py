@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libbfp8.so")
-SOURCES = ["api.cpp", "quantize.hip", "gemm.hip"]
+SOURCES = ["api.cpp", "api_attention.cpp", "quantize.hip", "gemm.hip", "rope.hip", "attention.hip",
+           "attention_bwd.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,303 @@
+// Internal declarations and device pieces of the attention kernels (not part
+// of the ABI; see include/bfp8_attention.h).
+#pragma once
+
+#include "bfp8_attention.h"
+#include "common.h"
+
+namespace bfp8 {
+
+// A tensor of heads as the kernels take it (strides in elements).
+struct Heads {
+  uint16_t* p;  // bf16 bits
+  int64_t row, head;
+};
+
+struct AttentionArgs {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const int32_t* k_lens;
+  int batch, total_q, total_k;
+  int heads, kv_heads, group;  // group = heads / kv_heads
+  int head_dim, causal;
+  float scale, scale_log2;     // scale_log2 = scale * log2(e)
+  Heads q, k, v, o, dout, dq, dk, dv;
+  float* lse;                  // [heads][total_q]
+  float* delta;                // [heads][total_q] (backward)
+};
+
+bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream);
+bfp8_status launch_attention_backward(const AttentionArgs& a, hipStream_t stream);
+size_t attention_forward_workspace(const AttentionArgs& a);
+
+bfp8_status launch_rope_table(float* table, int64_t positions, int rot_dim, double base,
+                              double factor, double original_length, int scaling,
+                              hipStream_t stream);
+struct RopeArgs {
+  const void* x;
+  void* y;
+  int64_t x_row, x_head, y_row, y_head;
+  int64_t tokens, heads;
+  int head_dim, rot_dim;
+  const float* table;
+  int64_t table_rows;
+  const int32_t* positions;
+  int inverse;
+};
+bfp8_status launch_rope(const RopeArgs& a, bfp8_in_dtype dt, bool interleaved, hipStream_t stream);
+
+namespace attn {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kNoData = 0x7FFFFFF0;  // a buffer offset past every extent: reads as zero
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// One sequence: rows [q0, q0 + qn) of the query tensors; rows [k0, k0 + ka)
+// of the key tensors, of which the first kn are used.  Every value is clamped
+// into the tensors, whatever the device arrays hold.
+struct Sequence {
+  int q0, qn, k0, ka, kn;
+};
+
+__device__ __forceinline__ void cu_range(const int32_t* cu, int batch, int total, int b, int& start,
+                                         int& n) {
+  if (cu == nullptr) {
+    n = total / batch;
+    start = b * n;
+  } else {
+    start = clampi(cu[b], 0, total);
+    n = clampi(cu[b + 1], start, total) - start;
+  }
+}
+
+__device__ __forceinline__ Sequence load_sequence(const AttentionArgs& a, int b) {
+  Sequence s;
+  cu_range(a.cu_q, a.batch, a.total_q, b, s.q0, s.qn);
+  cu_range(a.cu_k, a.batch, a.total_k, b, s.k0, s.ka);
+  s.kn = a.k_lens == nullptr ? s.ka : clampi(a.k_lens[b], 0, s.ka);
+  s.q0 = uniform(s.q0);
+  s.qn = uniform(s.qn);
+  s.k0 = uniform(s.k0);
+  s.ka = uniform(s.ka);
+  s.kn = uniform(s.kn);
+  return s;
+}
+
+// Sequence b and tile index within it of the t-th tile, where a sequence of
+// n rows (of the axis `cu` describes) has ceil(n * mult / unit) tiles; `tiles`
+// is that count.  Each wave finds it by itself: 64 sequences a step, their
+// tile counts summed by a scan over the lanes.  False past the last tile (the
+// grid is sized without knowing the lengths).
+__device__ __forceinline__ bool find_tile(const int32_t* cu, int batch, int total, int mult,
+                                          int unit, int t, int& b, int& tile, int& tiles) {
+  if (cu == nullptr) {
+    tiles = (total / batch * mult + unit - 1) / unit;
+    if (tiles == 0) return false;
+    b = t / tiles;
+    tile = t - b * tiles;
+    return b < batch;
+  }
+  const int lane = threadIdx.x & 63;
+  int base = 0;
+  for (int b0 = 0; b0 < batch; b0 += 64) {
+    int n = 0;
+    if (b0 + lane < batch) {
+      int start;
+      cu_range(cu, batch, total, b0 + lane, start, n);
+      n = (n * mult + unit - 1) / unit;
+    }
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int up = __shfl_up(sum, d);
+      if (lane >= d) sum += up;
+    }
+    const uint64_t past = __ballot(t < base + sum);
+    if (past != 0) {
+      const int l = uniform(__ffsll(static_cast<unsigned long long>(past)) - 1);
+      tiles = __builtin_amdgcn_readlane(n, l);
+      tile = t - base - (__builtin_amdgcn_readlane(sum, l) - tiles);
+      b = b0 + l;
+      return true;
+    }
+    base += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
+}
+
+// Raw buffer descriptor (wave-uniform): accesses at or past `bytes` read zero.
+__device__ __forceinline__ i32x4 buffer(const void* base, int bytes) {
+  const uint64_t addr = reinterpret_cast<uint64_t>(base);
+  i32x4 r;
+  r.x = uniform(static_cast<int>(addr & 0xFFFFFFFFu));
+  r.y = uniform(static_cast<int>((addr >> 32) & 0xFFFFu));
+  r.z = uniform(bytes);
+  r.w = 0x00020000;  // raw, 32-bit data
+  return r;
+}
+
+// Rows [row, row + rows) of head h of t, as a buffer whose end is the last
+// row's last value: a tile row past it reads zeros, whoever's rows lie there.
+// Row strides are at most 2^22 elements and tiles at most 256 rows, so offsets
+// inside a tile fit 31 bits; the tile's own address is 64 bits wide.
+__device__ __forceinline__ i32x4 head_rows(const Heads& t, int64_t row, int h, int rows, int dim) {
+  const int bytes = rows > 0 ? static_cast<int>(((rows - 1) * t.row + dim) * 2) : 0;
+  return buffer(t.p + row * t.row + h * t.head, bytes);
+}
+
+// 16 bytes per lane from a buffer to LDS, the 64 lanes side by side from LDS
+// address `lds`, without passing registers.  From inline asm, so that the
+// compiler does not wait for a copy before each read of the LDS; it has no
+// result registers, and a wait for vmcnt stands before the barrier that
+// publishes the tile.  The s_nop is the wait state after a write of M0.
+__device__ __forceinline__ void copy16(uint32_t lds, uint32_t off, i32x4 rsrc) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(off), "s"(rsrc)
+               : "memory");
+}
+__device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+}
+
+// LDS tiles hold rows of DP bf16 values (DP = 64 or 128) whose 16-byte chunks
+// are permuted within the row: chunk c of row r lies at c ^ swizzle(r).  The
+// same tile is read along rows (16 bytes of 32 consecutive rows: the rows'
+// bits 2, 3 and 0, 1 spread 16 rows over all chunks of the LDS's 256 bytes)
+// and down columns (8 bytes of 4 rows each, transposed by the read itself:
+// the rows' low bits move them to different 64-byte quarters).
+template <int DP>
+__device__ __forceinline__ int swizzle(int r) {
+  return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+}
+
+// A tile of ROWS rows: its LDS bytes and the copies that fill it by WAVES waves.
+template <int DP, int ROWS, int WAVES>
+struct Tile {
+  static constexpr int kBytes = ROWS * DP * 2;
+  static constexpr int kChunks = DP / 8;           // 16-byte chunks of a row
+  static constexpr int kRows1K = 64 / kChunks;     // rows of one wave-wide copy
+  static constexpr int kCopies = ROWS / kRows1K / WAVES;
+  static_assert(kCopies >= 1, "every wave copies");
+  uint32_t off[kCopies];
+
+  __device__ __forceinline__ void init(int wave, int lane, int64_t row_stride, int dim) {
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const int r = (wave * kCopies + i) * kRows1K + lane / kChunks;
+      const int c = (lane % kChunks) ^ swizzle<DP>(r);
+      off[i] = c * 8 < dim ? static_cast<uint32_t>(r * row_stride * 2 + c * 16) : kNoData;
+    }
+  }
+  __device__ __forceinline__ void copy(uint8_t* dst, int wave, const i32x4& rsrc) const {
+    const uint32_t base = uniform(lds_offset(dst) + wave * kCopies * 1024);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy16(base + i * 1024, off[i], rsrc);
+  }
+};
+
+// First operand of the 32x32x16 product from rows of a tile: lane l gives row
+// r0 + l % 32, values 16 ks + 8 (l / 32) .. + 7.
+template <int DP>
+__device__ __forceinline__ bf16x8 row_operand(const uint8_t* tile, int r0, int ks, int lane) {
+  const int r = r0 + (lane & 31);
+  const int c = (2 * ks + (lane >> 5)) ^ swizzle<DP>(r);
+  return *reinterpret_cast<const bf16x8*>(tile + r * (DP * 2) + c * 16);
+}
+
+// First operand of the 32x32x16 product from columns of a tile: lane l gives
+// column 32 ct + l % 32 of 8 rows: r0 + 4 (l / 32) .. + 3 and the same + 8,
+// which is the order in which the accumulator of a previous product holds
+// those 16 rows (see `narrow`).  Each ds_read_b64_tr_b16 takes 4 rows x 16
+// columns per 16 lanes (lane i of them pointing at row i / 4, columns
+// 4 (i % 4) .. + 3) and hands lane i column i.
+template <int DP>
+__device__ __forceinline__ bf16x8 column_operand(const uint8_t* tile, int r0, int ct, int lane) {
+  const int r = r0 + 4 * (lane >> 5) + ((lane >> 2) & 3);
+  const int byte = ct * 64 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+  const int c = byte >> 4, in = byte & 8;
+  const uint8_t* p = tile + r * (DP * 2) + ((c ^ swizzle<DP>(r)) * 16 + in);
+  const uint8_t* p8 = tile + (r + 8) * (DP * 2) + ((c ^ swizzle<DP>(r + 8)) * 16 + in);
+  typedef short i16x8 __attribute__((ext_vector_type(8)));
+  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
+  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p8));
+  const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+__device__ __forceinline__ f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// The accumulator of a 32x32 product holds in lane l column l % 32 of rows
+// 8 (i / 4) + 4 (l / 32) + i % 4, i = 0 .. 15.
+__device__ __forceinline__ int acc_row(int i, int lane) {
+  return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+}
+
+// Rows 16 u .. 16 u + 15 of a 32x32 accumulator as the second operand of the
+// next product, rounded to bf16 (nearest even): no lane exchange is needed,
+// because that operand's order of the 16 summed rows is free as long as the
+// first operand (column_operand) uses the same.
+__device__ __forceinline__ bf16x8 narrow(const f32x16& v, int u) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[8 * u + 2 * i], v[8 * u + 2 * i + 1]);
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+// Max / sum over the two lanes l, l ^ 32 (result in both).
+__device__ __forceinline__ float pair_max(float v) {
+  const u32x2 r = __builtin_bit_cast(
+      u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+  return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
+}
+__device__ __forceinline__ float pair_sum(float v) {
+  const u32x2 r = __builtin_bit_cast(
+      u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+  return __uint_as_float(r.x) + __uint_as_float(r.y);
+}
+
+// Store acc (columns: this lane's row of a tensor; rows: head dims) times mul
+// as bf16 to `dst`, head dims below `dim` only.
+template <int DP>
+__device__ __forceinline__ void store_row(uint16_t* dst, const f32x16 (&acc)[DP / 32], float mul,
+                                          int dim, int lane) {
+#pragma unroll
+  for (int ct = 0; ct < DP / 32; ++ct)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = ct * 32 + 8 * i + 4 * (lane >> 5);
+      u32x2 w;
+      w.x = pack_bf16x2(acc[ct][4 * i] * mul, acc[ct][4 * i + 1] * mul);
+      w.y = pack_bf16x2(acc[ct][4 * i + 2] * mul, acc[ct][4 * i + 3] * mul);
+      if (d < dim) *reinterpret_cast<u32x2*>(dst + d) = w;
+    }
+}
+
+// 8 values of one row (16 bytes), zero where the row or the column is outside.
+__device__ __forceinline__ bf16x8 load8(const uint16_t* row, int d, int dim, bool valid) {
+  u32x4 w = {0, 0, 0, 0};
+  if (valid && d < dim) w = *reinterpret_cast<const u32x4*>(row + d);
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+}  // namespace attn
+}  // namespace bfp8
