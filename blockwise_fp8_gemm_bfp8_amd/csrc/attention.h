@@ -23,7 +23,8 @@ struct AttentionArgs {
   float scale, scale_log2;     // scale_log2 = scale * log2(e)
   Heads q, k, v, o, dout, dq, dk, dv;
   float* lse;                  // [heads][total_q]
-  float* delta;                // [heads][total_q] (backward)
+  float* lse2;                 // [heads][total_q] each (backward): the dq kernel
+  float* delta;                // leaves L log2(e) (0 for L = -inf) and -sum dO O
 };
 
 bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
@@ -62,6 +63,8 @@ typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// classes of instructions for __builtin_amdgcn_sched_group_barrier
+constexpr int kSchedValu = 0x2, kSchedMma = 0x8, kSchedRead = 0x100;
 constexpr int kNoData = 0x7FFFFFF0;  // a buffer offset past every extent: reads as zero
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
@@ -98,21 +101,70 @@ __device__ __forceinline__ Sequence load_sequence(const AttentionArgs& a, int b)
   return s;
 }
 
-// Sequence b and tile index within it of the t-th tile, where a sequence of
-// n rows (of the axis `cu` describes) has ceil(n * mult / unit) tiles; `tiles`
-// is that count.  Each wave finds it by itself: 64 sequences a step, their
-// tile counts summed by a scan over the lanes.  False past the last tile (the
-// grid is sized without knowing the lengths).
+// Sum over the 64 lanes of a wave (data-parallel moves: row shifts, then two
+// broadcasts of a row's last lane into the rows after it).
+__device__ __forceinline__ int wave_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1, 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2, 3
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+// The t-th tile of all sequences, where a sequence of n rows (of the axis `cu`
+// describes) has ceil(n * mult / unit) of them: its sequence b, that
+// sequence's tile count and the tile's rank in it.  False past the last tile
+// (the grid is sized without knowing the lengths).  Each wave finds it by
+// itself.
+//
+// Up to 64 sequences, tiles come by descending rank, whatever their sequence:
+// with a causal mask a tile's rank is its work, and workgroups that start with
+// the most work leave the least waiting at the end (4 sequences of 4096, two
+// tiles to a CU: sequence after sequence the last CUs end 1.4 times later than
+// all would, evenly shared).  Of G(r) = sum of max(n_b - r, 0) tiles that
+// have rank r or more, t falls into the largest r with G(r) > t, found by
+// bisection over a wave-wide sum.  More sequences than lanes come one after
+// another.
 __device__ __forceinline__ bool find_tile(const int32_t* cu, int batch, int total, int mult,
-                                          int unit, int t, int& b, int& tile, int& tiles) {
+                                          int unit, int t, int& b, int& rank, int& tiles) {
   if (cu == nullptr) {
     tiles = (total / batch * mult + unit - 1) / unit;
-    if (tiles == 0) return false;
-    b = t / tiles;
-    tile = t - b * tiles;
-    return b < batch;
+    rank = tiles - 1 - t / batch;
+    b = t % batch;
+    return rank >= 0;
   }
   const int lane = threadIdx.x & 63;
+  if (batch <= 64) {
+    int n = 0;
+    if (lane < batch) {
+      int start;
+      cu_range(cu, batch, total, lane, start, n);
+      n = (n * mult + unit - 1) / unit;
+    }
+    if (wave_sum(n) <= t) return false;
+    int lo = 0, hi = 1;  // G(lo) > t; find hi with G(hi) <= t
+    while (wave_sum(max(n - hi, 0)) > t) {
+      lo = hi;
+      hi *= 2;
+    }
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (wave_sum(max(n - mid, 0)) > t) lo = mid;
+      else hi = mid;
+    }
+    rank = lo;
+    const int at = t - wave_sum(max(n - hi, 0));  // among the sequences that have this rank
+    const uint64_t having = __ballot(n > lo);
+    const int before = __builtin_amdgcn_mbcnt_hi(
+        static_cast<uint32_t>(having >> 32),
+        __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(having), 0));
+    const uint64_t it = __ballot(n > lo && before == at);
+    b = uniform(__ffsll(static_cast<unsigned long long>(it)) - 1);
+    tiles = __builtin_amdgcn_readlane(n, b);
+    return true;
+  }
   int base = 0;
   for (int b0 = 0; b0 < batch; b0 += 64) {
     int n = 0;
@@ -131,7 +183,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, int batch, int tota
     if (past != 0) {
       const int l = uniform(__ffsll(static_cast<unsigned long long>(past)) - 1);
       tiles = __builtin_amdgcn_readlane(n, l);
-      tile = t - base - (__builtin_amdgcn_readlane(sum, l) - tiles);
+      rank = __builtin_amdgcn_readlane(sum, l) - 1 - (t - base);
       b = b0 + l;
       return true;
     }
@@ -171,38 +223,50 @@ __device__ __forceinline__ void copy16(uint32_t lds, uint32_t off, i32x4 rsrc) {
                : "s"(lds), "v"(off), "s"(rsrc)
                : "memory");
 }
-__device__ __forceinline__ void wait_copies() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+__device__ __forceinline__ void copy4(uint32_t lds, uint32_t off, i32x4 rsrc) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(off), "s"(rsrc)
+               : "memory");
+}
+// Until at most LEFT of this wave's copies are under way (they end in order).
+template <int LEFT>
+__device__ __forceinline__ void wait_copies() {
+  static_assert(LEFT < 16, "the low four bits of vmcnt");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | LEFT);
+}
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
 }
 
-// LDS tiles hold rows of DP bf16 values (DP = 64 or 128) whose 16-byte chunks
-// are permuted within the row: chunk c of row r lies at c ^ swizzle(r).  The
-// same tile is read along rows (16 bytes of 32 consecutive rows: the rows'
-// bits 2, 3 and 0, 1 spread 16 rows over all chunks of the LDS's 256 bytes)
-// and down columns (8 bytes of 4 rows each, transposed by the read itself:
-// the rows' low bits move them to different 64-byte quarters).
-template <int DP>
-__device__ __forceinline__ int swizzle(int r) {
-  return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-}
+// LDS tiles hold DP columns (64 or 128) of bf16 as panels of 32 columns, each
+// panel ROWS rows of 64 bytes.  The four 16-byte chunks of a panel's row r are
+// permuted: chunk c lies at c ^ (r / 4 % 4).  The same tile is read along rows
+// (16 bytes of 32 consecutive rows: 16 rows of one chunk spread over all of
+// the LDS's 256 bytes) and down columns (8 bytes of 4 rows each, transposed by
+// the read itself: 8 whole rows, 512 bytes in a piece), both without bank
+// conflicts, and every operand of a tile is a constant offset from one of two
+// addresses per kind of read.
+__device__ __forceinline__ int swizzle(int r) { return (r >> 2) & 3; }
 
-// A tile of ROWS rows: its LDS bytes and the copies that fill it by WAVES waves.
+// A tile of ROWS rows: its LDS bytes and the copies that fill it by WAVES
+// waves, 16 rows of a panel a copy.
 template <int DP, int ROWS, int WAVES>
 struct Tile {
-  static constexpr int kBytes = ROWS * DP * 2;
-  static constexpr int kChunks = DP / 8;           // 16-byte chunks of a row
-  static constexpr int kRows1K = 64 / kChunks;     // rows of one wave-wide copy
-  static constexpr int kCopies = ROWS / kRows1K / WAVES;
+  static constexpr int kPanel = ROWS * 64;  // bytes
+  static constexpr int kBytes = kPanel * (DP / 32);
+  static constexpr int kCopies = kBytes / 1024 / WAVES;
   static_assert(kCopies >= 1, "every wave copies");
   uint32_t off[kCopies];
 
   __device__ __forceinline__ void init(int wave, int lane, int64_t row_stride, int dim) {
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
-      const int r = (wave * kCopies + i) * kRows1K + lane / kChunks;
-      const int c = (lane % kChunks) ^ swizzle<DP>(r);
+      const int at = wave * kCopies + i;
+      const int panel = at / (ROWS / 16);
+      const int r = at % (ROWS / 16) * 16 + (lane >> 2);
+      const int c = panel * 4 + ((lane & 3) ^ swizzle(r));
       off[i] = c * 8 < dim ? static_cast<uint32_t>(r * row_stride * 2 + c * 16) : kNoData;
     }
   }
@@ -211,36 +275,34 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) copy16(base + i * 1024, off[i], rsrc);
   }
+
+  // First operand of the 32x32x16 product from rows of a tile: lane l gives
+  // row r0 + l % 32, values 16 ks + 8 (l / 32) .. + 7.
+  static __device__ __forceinline__ bf16x8 rows(const uint8_t* tile, int r0, int ks, int lane) {
+    const int r = lane & 31;
+    const int c = (2 * (ks & 1) + (lane >> 5)) ^ swizzle(r);
+    return *reinterpret_cast<const bf16x8*>(tile + (ks >> 1) * kPanel + r0 * 64 + (r * 64 + c * 16));
+  }
+
+  // First operand of the 32x32x16 product from columns of a tile: lane l gives
+  // column 32 ct + l % 32 of 8 rows: r0 + 4 (l / 32) .. + 3 and the same + 8,
+  // which is the order in which the accumulator of a previous product holds
+  // those 16 rows (see `narrow`).  Each ds_read_b64_tr_b16 takes 4 rows x 16
+  // columns per 16 lanes (lane i of them pointing at row i / 4, columns
+  // 4 (i % 4) .. + 3) and hands lane i column i.
+  static __device__ __forceinline__ bf16x8 columns(const uint8_t* tile, int r0, int ct, int lane) {
+    typedef short i16x8 __attribute__((ext_vector_type(8)));
+    const int r = 4 * (lane >> 5) + ((lane >> 2) & 3);
+    const int c = ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1), in = (lane & 1) * 8;
+    const uint8_t* p = tile + ct * kPanel + r0 * 64;
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_i16x4*)(p + (r * 64 + (c ^ swizzle(r)) * 16 + in)));
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_i16x4*)(p + ((r + 8) * 64 + (c ^ swizzle(r + 8)) * 16 + in)));
+    const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, v);
+  }
 };
-
-// First operand of the 32x32x16 product from rows of a tile: lane l gives row
-// r0 + l % 32, values 16 ks + 8 (l / 32) .. + 7.
-template <int DP>
-__device__ __forceinline__ bf16x8 row_operand(const uint8_t* tile, int r0, int ks, int lane) {
-  const int r = r0 + (lane & 31);
-  const int c = (2 * ks + (lane >> 5)) ^ swizzle<DP>(r);
-  return *reinterpret_cast<const bf16x8*>(tile + r * (DP * 2) + c * 16);
-}
-
-// First operand of the 32x32x16 product from columns of a tile: lane l gives
-// column 32 ct + l % 32 of 8 rows: r0 + 4 (l / 32) .. + 3 and the same + 8,
-// which is the order in which the accumulator of a previous product holds
-// those 16 rows (see `narrow`).  Each ds_read_b64_tr_b16 takes 4 rows x 16
-// columns per 16 lanes (lane i of them pointing at row i / 4, columns
-// 4 (i % 4) .. + 3) and hands lane i column i.
-template <int DP>
-__device__ __forceinline__ bf16x8 column_operand(const uint8_t* tile, int r0, int ct, int lane) {
-  const int r = r0 + 4 * (lane >> 5) + ((lane >> 2) & 3);
-  const int byte = ct * 64 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-  const int c = byte >> 4, in = byte & 8;
-  const uint8_t* p = tile + r * (DP * 2) + ((c ^ swizzle<DP>(r)) * 16 + in);
-  const uint8_t* p8 = tile + (r + 8) * (DP * 2) + ((c ^ swizzle<DP>(r + 8)) * 16 + in);
-  typedef short i16x8 __attribute__((ext_vector_type(8)));
-  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
-  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p8));
-  const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  return __builtin_bit_cast(bf16x8, v);
-}
 
 __device__ __forceinline__ f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -255,7 +317,7 @@ __device__ __forceinline__ int acc_row(int i, int lane) {
 // Rows 16 u .. 16 u + 15 of a 32x32 accumulator as the second operand of the
 // next product, rounded to bf16 (nearest even): no lane exchange is needed,
 // because that operand's order of the 16 summed rows is free as long as the
-// first operand (column_operand) uses the same.
+// first operand (Tile::columns) uses the same.
 __device__ __forceinline__ bf16x8 narrow(const f32x16& v, int u) {
   u32x4 w;
 #pragma unroll

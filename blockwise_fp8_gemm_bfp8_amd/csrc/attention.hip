@@ -37,13 +37,12 @@ __global__ __launch_bounds__(512, 2) void attention_forward_kernel(AttentionArgs
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][KTile::kBytes];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int g = blockIdx.x % a.kv_heads;
-  int b, tile, tiles;
-  if (!find_tile(a.cu_q, a.batch, a.total_q, a.group, kRows, blockIdx.x / a.kv_heads, b, tile,
+  int b, rank, tiles;
+  if (!find_tile(a.cu_q, a.batch, a.total_q, a.group, kRows, blockIdx.x / a.kv_heads, b, rank,
                  tiles))
     return;
   const Sequence s = load_sequence(a, b);
-  // the last rows see the most keys: they start first
-  const int row0 = (tiles - 1 - tile) * kRows;
+  const int row0 = rank * kRows;  // the last rows see the most keys
   const int rows = s.qn * a.group;
   const int r = row0 + wave * 32 + (lane & 31);
   const bool valid = r < rows;
@@ -77,23 +76,37 @@ __global__ __launch_bounds__(512, 2) void attention_forward_kernel(AttentionArgs
   f32x16 o[DP / 32];
 #pragma unroll
   for (int ct = 0; ct < DP / 32; ++ct) o[ct] = f32x16{};
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l[2] = {0.0f, 0.0f};  // l: sums of even and odd values
   const int nj = block_lim < 0 ? 0 : block_lim / kKeys + 1;
   if (nj > 0) copy_tile(0);
   for (int j = 0; j < nj; ++j) {
-    wait_copies();
+    wait_copies<0>();
     __syncthreads();
     if (j + 1 < nj) copy_tile(j + 1);
     if (j * kKeys > wave_lim) continue;
     const uint8_t* K = lds[j & 1][0];
     const uint8_t* V = lds[j & 1][1];
-    f32x16 p[2];
+    constexpr int kDims = DP / 32;    // 32-column panels
+    constexpr int kSteps = DP / 16;   // products of one S^T square
+    // S^T: the K rows of 8 products are in flight ahead of the products, and
+    // the V columns of the first P V products follow them
+    f32x16 p[2] = {};
+    bf16x8 kf[2][kSteps], vf[2][kDims];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      p[t] = f32x16{};
+    for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-      for (int ks = 0; ks < DP / 16; ++ks)
-        p[t] = mma(row_operand<DP>(K, 32 * t, ks, lane), q[ks], p[t]);
+      for (int t = 0; t < 2; ++t) kf[t][ks] = KTile::rows(K, 32 * t, ks, lane);
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) p[t] = mma(kf[t][ks], q[ks], p[t]);
+#pragma unroll
+    for (int ct = 0; ct < kDims; ++ct) vf[0][ct] = KTile::columns(V, 0, ct, lane);
+    __builtin_amdgcn_sched_group_barrier(kSchedRead, 8, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * kSteps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
     }
     if (j * kKeys + kKeys - 1 > wave_free) {
 #pragma unroll
@@ -112,35 +125,47 @@ __global__ __launch_bounds__(512, 2) void attention_forward_kernel(AttentionArgs
       const float next = fmaxf(m, top);
       const float alpha = __builtin_amdgcn_exp2f(m - (next == -INFINITY ? 0.0f : next));
       m = next;
-      l *= alpha;
+      l[0] *= alpha;
+      l[1] *= alpha;
 #pragma unroll
-      for (int ct = 0; ct < DP / 32; ++ct)
+      for (int ct = 0; ct < kDims; ++ct)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[ct][e] *= alpha;
     }
+    // P and O^T, 16 keys at a time: the exponentials of the next 16 and the
+    // reads of their V columns go between the products of these
     const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int u = 0; u < 4; ++u) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        p[t][e] = __builtin_amdgcn_exp2f(fmaf(p[t][e], a.scale_log2, -base));
-        l += p[t][e];
+      for (int e = 8 * (u & 1); e < 8 * (u & 1) + 8; ++e) {
+        p[u >> 1][e] = __builtin_amdgcn_exp2f(fmaf(p[u >> 1][e], a.scale_log2, -base));
+        l[e & 1] += p[u >> 1][e];
+      }
+      const bf16x8 pu = narrow(p[u >> 1], u & 1);
+      if (u < 3) {
+#pragma unroll
+        for (int ct = 0; ct < kDims; ++ct)
+          vf[(u + 1) & 1][ct] = KTile::columns(V, 16 * (u + 1), ct, lane);
       }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bf16x8 pu = narrow(p[u >> 1], u & 1);
+      for (int ct = 0; ct < kDims; ++ct) o[ct] = mma(vf[u & 1][ct], pu, o[ct]);
+    }
+    __builtin_amdgcn_sched_group_barrier(kSchedValu, 28, 1);
 #pragma unroll
-      for (int ct = 0; ct < DP / 32; ++ct)
-        o[ct] = mma(column_operand<DP>(V, 16 * u, ct, lane), pu, o[ct]);
+    for (int i = 0; i < 4 * kDims; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedValu, 28 / kDims, 1);
     }
   }
-  l = pair_sum(l);
+  const float sum = pair_sum(l[0] + l[1]);
   if (!valid) return;
   uint16_t* orow = a.o.p + (int64_t)(s.q0 + i) * a.o.row + h * a.o.head;
-  store_row<DP>(orow, o, l > 0.0f ? 1.0f / l : 0.0f, a.head_dim, lane);
+  store_row<DP>(orow, o, sum > 0.0f ? 1.0f / sum : 0.0f, a.head_dim, lane);
   if (lane < 32)
     a.lse[(int64_t)h * a.total_q + s.q0 + i] =
-        l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+        sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
 }
 
 }  // namespace

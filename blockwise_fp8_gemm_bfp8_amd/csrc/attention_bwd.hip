@@ -29,12 +29,12 @@ __global__ __launch_bounds__(512, 2) void attention_dq_kernel(AttentionArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][KTile::kBytes];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int g = blockIdx.x % a.kv_heads;
-  int b, tile, tiles;
-  if (!find_tile(a.cu_q, a.batch, a.total_q, a.group, kRows, blockIdx.x / a.kv_heads, b, tile,
+  int b, rank, tiles;
+  if (!find_tile(a.cu_q, a.batch, a.total_q, a.group, kRows, blockIdx.x / a.kv_heads, b, rank,
                  tiles))
     return;
   const Sequence s = load_sequence(a, b);
-  const int row0 = (tiles - 1 - tile) * kRows;
+  const int row0 = rank * kRows;
   const int rows = s.qn * a.group;
   const int r = row0 + wave * 32 + (lane & 31);
   const bool valid = r < rows;
@@ -69,7 +69,10 @@ __global__ __launch_bounds__(512, 2) void attention_dq_kernel(AttentionArgs a) {
   if (valid) {
     const float lse = a.lse[(int64_t)h * a.total_q + t];
     lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
-    if (lane < 32) a.delta[(int64_t)h * a.total_q + t] = delta;
+    if (lane < 32) {  // for the dkdv kernel
+      a.lse2[(int64_t)h * a.total_q + t] = lse2;
+      a.delta[(int64_t)h * a.total_q + t] = -delta;
+    }
   }
 
   KTile kt, vt;
@@ -88,35 +91,70 @@ __global__ __launch_bounds__(512, 2) void attention_dq_kernel(AttentionArgs a) {
   const int nj = block_lim < 0 ? 0 : block_lim / kKeys + 1;
   if (nj > 0) copy_tile(0);
   for (int j = 0; j < nj; ++j) {
-    wait_copies();
+    wait_copies<0>();
     __syncthreads();
     if (j + 1 < nj) copy_tile(j + 1);
+    if (j * kKeys > wave_lim) continue;
     const uint8_t* K = lds[j & 1][0];
     const uint8_t* V = lds[j & 1][1];
+    constexpr int kDims = DP / 32;   // 32-column panels
+    constexpr int kSteps = DP / 16;  // products of one 32x32 square
+    bf16x8 kf[kSteps], vf[kSteps], kc[2][kDims];
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) kf[ks] = KTile::rows(K, 0, ks, lane);
 #pragma unroll
     for (int t2 = 0; t2 < 2; ++t2) {
       const int key0 = j * kKeys + 32 * t2;
-      if (key0 > wave_lim) break;
+      // S^T and dP^T; the V rows are read between the products of S^T, the K
+      // columns of dQ^T between those of dP^T
       f32x16 p = {}, dp = {};
 #pragma unroll
-      for (int ks = 0; ks < DP / 16; ++ks) p = mma(row_operand<DP>(K, 32 * t2, ks, lane), q[ks], p);
+      for (int ks = 0; ks < kSteps; ++ks) vf[ks] = KTile::rows(V, 32 * t2, ks, lane);
 #pragma unroll
-      for (int ks = 0; ks < DP / 16; ++ks)
-        dp = mma(row_operand<DP>(V, 32 * t2, ks, lane), d[ks], dp);
+      for (int ks = 0; ks < kSteps; ++ks) p = mma(kf[ks], q[ks], p);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int ct = 0; ct < kDims; ++ct)
+          kc[u][ct] = KTile::columns(K, 32 * t2 + 16 * u, ct, lane);
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) dp = mma(vf[ks], d[ks], dp);
+      if (t2 == 0) __builtin_amdgcn_sched_group_barrier(kSchedRead, kSteps, 0);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
+      }
       if (key0 + 31 > wave_free) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (key0 + acc_row(e, lane) > lim) p[e] = -INFINITY;
       }
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        p[e] = __builtin_amdgcn_exp2f(fmaf(p[e], a.scale_log2, -lse2)) * (dp[e] - delta);
+      // dQ^T, 16 keys at a time; the K rows of the next square are read meanwhile
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int e = 8 * u; e < 8 * u + 8; ++e)
+          p[e] = __builtin_amdgcn_exp2f(fmaf(p[e], a.scale_log2, -lse2)) * (dp[e] - delta);
         const bf16x8 ds = narrow(p, u);
 #pragma unroll
-        for (int ct = 0; ct < DP / 32; ++ct)
-          acc[ct] = mma(column_operand<DP>(K, 32 * t2 + 16 * u, ct, lane), ds, acc[ct]);
+        for (int ct = 0; ct < kDims; ++ct) acc[ct] = mma(kc[u][ct], ds, acc[ct]);
+      }
+      if (t2 == 0) {
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) kf[ks] = KTile::rows(K, 32, ks, lane);
+      }
+      __builtin_amdgcn_sched_group_barrier(kSchedValu, 36, 1);
+#pragma unroll
+      for (int i = 0; i < 2 * kDims; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 1);
+        __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 1);
+        __builtin_amdgcn_sched_group_barrier(kSchedValu, 36 / kDims, 1);
       }
     }
   }
@@ -127,34 +165,36 @@ __global__ __launch_bounds__(512, 2) void attention_dq_kernel(AttentionArgs a) {
 template <int DP>
 __global__ __launch_bounds__(512, 2) void attention_dkdv_kernel(AttentionArgs a) {
   typedef Tile<DP, kQueries, kWaves> QTile;
+  typedef Tile<DP, kRows, kWaves> VTile;
+  // two stages of Q rows, dO rows and their statistics, and the workgroup's V rows
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][QTile::kBytes];
-  __shared__ __attribute__((aligned(16))) float stats[2][2][kQueries];  // lse2, delta
+  __shared__ __attribute__((aligned(1024))) uint8_t vlds[VTile::kBytes];
+  __shared__ __attribute__((aligned(256))) float stats[2][2][kQueries];  // lse2, -delta
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int g = blockIdx.x % a.kv_heads;
-  int b, tile, tiles;
-  if (!find_tile(a.cu_k, a.batch, a.total_k, 1, kRows, blockIdx.x / a.kv_heads, b, tile, tiles))
+  int b, rank, tiles;
+  if (!find_tile(a.cu_k, a.batch, a.total_k, 1, kRows, blockIdx.x / a.kv_heads, b, rank, tiles))
     return;
   const Sequence s = load_sequence(a, b);
-  const int row0 = tile * kRows;  // the first keys are seen by the most queries
+  const int row0 = (tiles - 1 - rank) * kRows;  // the first keys are seen by the most queries
   const int key = row0 + wave * 32 + (lane & 31);
   const bool used = key < s.kn;
   const int64_t krow = s.k0 + min(key, s.ka - 1);
   const uint16_t* kp = a.k.p + krow * a.k.row + g * a.k.head;
-  const uint16_t* vp = a.v.p + krow * a.v.row + g * a.v.head;
-  bf16x8 k[DP / 16], v[DP / 16];
+  bf16x8 k[DP / 16];
 #pragma unroll
-  for (int ks = 0; ks < DP / 16; ++ks) {
+  for (int ks = 0; ks < DP / 16; ++ks)
     k[ks] = load8(kp, ks * 16 + 8 * (lane >> 5), a.head_dim, used);
-    v[ks] = load8(vp, ks * 16 + 8 * (lane >> 5), a.head_dim, used);
+  {
+    VTile vt;
+    vt.init(wave, lane, a.v.row, a.head_dim);
+    vt.copy(vlds, wave,
+            head_rows(a.v, (int64_t)s.k0 + row0, g, min(s.kn - row0, kRows), a.head_dim));
   }
-  // query i sees keys up to i + kn - qn: the workgroup's first query, and the
-  // first from which on the wave's keys are all seen
+  // query i sees keys up to i + kn - qn
   const int back = a.causal ? s.qn - s.kn : -s.kn;  // first query that sees key: key + back
-  const int first = max(row0 + back, 0) / kQueries;
-  const int nq = (s.qn + kQueries - 1) / kQueries;
-  const int per_head = row0 < s.kn ? max(nq - first, 0) : 0;
-  const int steps = per_head * a.group;
-  const int wave_first = row0 + wave * 32 + back;       // first query that sees the wave's first key
+  const int first = row0 < s.kn ? max(row0 + back, 0) / kQueries * kQueries : s.qn;
+  const int wave_first = row0 + wave * 32 + back;  // first query that sees the wave's first key
   // first query of no masking: the one that sees the wave's last key, or none
   // if some of its keys are past the used length and must vanish
   const bool all_used = row0 + wave * 32 + 31 < s.kn;
@@ -164,71 +204,102 @@ __global__ __launch_bounds__(512, 2) void attention_dkdv_kernel(AttentionArgs a)
   QTile qt, dt;
   qt.init(wave, lane, a.q.row, a.head_dim);
   dt.init(wave, lane, a.dout.row, a.head_dim);
-  float stat = 0.0f;
-  auto copy_tile = [&](int n) {
-    const int hh = n / per_head;
-    const int i0 = (first + n - hh * per_head) * kQueries;
+  // tile of queries i0 .. of the h-th head of the group into stage n
+  auto copy_tile = [&](int n, int hh, int i0) {
     const int h = g * a.group + hh;
     const int rows = min(s.qn - i0, kQueries);
-    qt.copy(lds[n & 1][0], wave, head_rows(a.q, (int64_t)s.q0 + i0, h, rows, a.head_dim));
-    dt.copy(lds[n & 1][1], wave, head_rows(a.dout, (int64_t)s.q0 + i0, h, rows, a.head_dim));
-    if (threadIdx.x < 2 * kQueries) {
-      const int i = threadIdx.x % kQueries;
-      const float* src = threadIdx.x < kQueries ? a.lse : a.delta;
-      float x = 0.0f;
-      if (i < rows) x = src[(int64_t)h * a.total_q + s.q0 + i0 + i];
-      if (threadIdx.x < kQueries) x = x == -INFINITY ? 0.0f : x * kLog2e;
-      stat = x;
+    qt.copy(lds[n][0], wave, head_rows(a.q, (int64_t)s.q0 + i0, h, rows, a.head_dim));
+    dt.copy(lds[n][1], wave, head_rows(a.dout, (int64_t)s.q0 + i0, h, rows, a.head_dim));
+    if (wave < 2) {
+      const float* src = wave == 0 ? a.lse2 : a.delta;
+      copy4(uniform(lds_offset(&stats[n][wave][0])), lane * 4,
+            buffer(src + (int64_t)h * a.total_q + s.q0 + i0, rows * 4));
     }
   };
 
   f32x16 dk[DP / 32], dv[DP / 32];
 #pragma unroll
   for (int ct = 0; ct < DP / 32; ++ct) dk[ct] = dv[ct] = f32x16{};
-  if (steps > 0) copy_tile(0);
-  for (int n = 0; n < steps; ++n) {
-    if (threadIdx.x < 2 * kQueries)
-      stats[n & 1][threadIdx.x / kQueries][threadIdx.x % kQueries] = stat;
-    wait_copies();
+  int hh = 0, i0 = first, n = 0;
+  const bool any = first < s.qn;
+  if (any) copy_tile(0, 0, first);
+  while (any) {
+    int next_h = hh, next_i = i0 + kQueries;
+    if (next_i >= s.qn) {
+      next_i = first;
+      ++next_h;
+    }
+    wait_copies<0>();
     __syncthreads();
-    if (n + 1 < steps) copy_tile(n + 1);
-    const int i0 = (first + n % per_head) * kQueries;
-    const uint8_t* Q = lds[n & 1][0];
-    const uint8_t* D = lds[n & 1][1];
+    if (next_h < a.group) copy_tile(n ^ 1, next_h, next_i);
+    const uint8_t* Q = lds[n][0];
+    const uint8_t* D = lds[n][1];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (i0 + 32 * t + 31 < wave_first) continue;
-      f32x16 p = {}, dp = {};
+      constexpr int kDims = DP / 32, kSteps = DP / 16;
+      // S and dP; dP starts from -delta
+      f32x16 p = {}, dp;
 #pragma unroll
-      for (int ks = 0; ks < DP / 16; ++ks) p = mma(row_operand<DP>(Q, 32 * t, ks, lane), k[ks], p);
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int ks = 0; ks < DP / 16; ++ks)
-        dp = mma(row_operand<DP>(D, 32 * t, ks, lane), v[ks], dp);
-      const bool masked = i0 + 32 * t < wave_free;
+        for (int e = 0; e < 4; ++e)
+          dp[4 * c + e] = stats[n][1][32 * t + 8 * c + 4 * (lane >> 5) + e];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int r = 32 * t + 8 * c + 4 * (lane >> 5);
-        const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&stats[n & 1][0][r]);
-        const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[n & 1][1][r]);
+      for (int ks = 0; ks < kSteps; ++ks) p = mma(QTile::rows(Q, 32 * t, ks, lane), k[ks], p);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = __builtin_amdgcn_exp2f(fmaf(p[4 * c + e], a.scale_log2, -lse2[e]));
-          if (masked && i0 + r + e < from) x = 0.0f;
-          p[4 * c + e] = x;
-          dp[4 * c + e] = x * (dp[4 * c + e] - delta[e]);
-        }
+      for (int ks = 0; ks < kSteps; ++ks)
+        dp = mma(QTile::rows(D, 32 * t, ks, lane), VTile::rows(vlds, wave * 32, ks, lane), dp);
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 4, 0);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+      }
+      f32x16 lse2;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          lse2[4 * c + e] = stats[n][0][32 * t + 8 * c + 4 * (lane >> 5) + e];
+      if (i0 + 32 * t < wave_free) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (i0 + 32 * t + acc_row(e, lane) < from) p[e] = -INFINITY;
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        p[e] = __builtin_amdgcn_exp2f(fmaf(p[e], a.scale_log2, -lse2[e]));
+        dp[e] *= p[e];
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const bf16x8 pu = narrow(p, u), du = narrow(dp, u);
 #pragma unroll
-        for (int ct = 0; ct < DP / 32; ++ct) {
-          dv[ct] = mma(column_operand<DP>(D, 32 * t + 16 * u, ct, lane), pu, dv[ct]);
-          dk[ct] = mma(column_operand<DP>(Q, 32 * t + 16 * u, ct, lane), du, dk[ct]);
-        }
+        for (int ct = 0; ct < kDims; ++ct)
+          dv[ct] = mma(QTile::columns(D, 32 * t + 16 * u, ct, lane), pu, dv[ct]);
+#pragma unroll
+        for (int ct = 0; ct < kDims; ++ct)
+          dk[ct] = mma(QTile::columns(Q, 32 * t + 16 * u, ct, lane), du, dk[ct]);
+      }
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 8, 1);
+#pragma unroll
+      for (int i = 0; i < 4 * kDims; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 1);
+        __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 1);
       }
     }
+    if (next_h == a.group) break;
+    hh = next_h;
+    i0 = next_i;
+    n ^= 1;
   }
+  wait_copies<0>();  // no copy may land after the workgroup has given up its LDS
   if (key >= s.ka) return;
   store_row<DP>(a.dv.p + krow * a.dv.row + g * a.dv.head, dv, 1.0f, a.head_dim, lane);
   store_row<DP>(a.dk.p + krow * a.dk.row + g * a.dk.head, dk, a.scale, a.head_dim, lane);
