@@ -193,8 +193,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, int batch, int tota
 }
 
 // Raw buffer descriptor (wave-uniform): accesses at or past `bytes` read zero.
-__device__ __forceinline__ i32x4 buffer(const void* base, int bytes) {
-  const uint64_t addr = reinterpret_cast<uint64_t>(base);
+__device__ __forceinline__ i32x4 buffer(uint64_t addr, int bytes) {
   i32x4 r;
   r.x = uniform(static_cast<int>(addr & 0xFFFFFFFFu));
   r.y = uniform(static_cast<int>((addr >> 32) & 0xFFFFu));
@@ -203,14 +202,24 @@ __device__ __forceinline__ i32x4 buffer(const void* base, int bytes) {
   return r;
 }
 
-// Rows [row, row + rows) of head h of t, as a buffer whose end is the last
-// row's last value: a tile row past it reads zeros, whoever's rows lie there.
-// Row strides are at most 2^22 elements and tiles at most 256 rows, so offsets
-// inside a tile fit 31 bits; the tile's own address is 64 bits wide.
-__device__ __forceinline__ i32x4 head_rows(const Heads& t, int64_t row, int h, int rows, int dim) {
-  const int bytes = rows > 0 ? static_cast<int>(((rows - 1) * t.row + dim) * 2) : 0;
-  return buffer(t.p + row * t.row + h * t.head, bytes);
-}
+// A walk over the rows of one head of a tensor (all of it wave-uniform): the
+// rows at its place as a buffer whose end is the last row's last value, so a
+// tile row past it reads zeros, whoever's rows lie there.  Row strides are at
+// most 2^22 elements and tiles at most 128 rows, so offsets inside a tile and
+// steps of the walk fit 31 bits; the place itself is a 64-bit address.
+struct Walk {
+  uint64_t at;
+  int row_bytes, dim_bytes;
+
+  __device__ __forceinline__ Walk(const Heads& t, int64_t row, int h, int dim)
+      : at(reinterpret_cast<uint64_t>(t.p + row * t.row + h * t.head)),
+        row_bytes(static_cast<int>(t.row) * 2),
+        dim_bytes(dim * 2) {}
+  __device__ __forceinline__ i32x4 rows(int n) const {
+    return buffer(at, n > 0 ? (n - 1) * row_bytes + dim_bytes : 0);
+  }
+  __device__ __forceinline__ void step(int n) { at += static_cast<int64_t>(n * row_bytes); }
+};
 
 // 16 bytes per lane from a buffer to LDS, the 64 lanes side by side from LDS
 // address `lds`, without passing registers.  From inline asm, so that the

@@ -66,11 +66,13 @@ __global__ __launch_bounds__(512, 2) void attention_forward_kernel(AttentionArgs
   KTile kt, vt;
   kt.init(wave, lane, a.k.row, a.head_dim);
   vt.init(wave, lane, a.v.row, a.head_dim);
-  auto copy_tile = [&](int j) {
+  Walk kw(a.k, s.k0, g, a.head_dim), vw(a.v, s.k0, g, a.head_dim);
+  auto copy_tile = [&](int j) {  // tiles in their order
     const int n = min(s.kn - j * kKeys, kKeys);
-    const int64_t row = (int64_t)s.k0 + j * kKeys;
-    kt.copy(lds[j & 1][0], wave, head_rows(a.k, row, g, n, a.head_dim));
-    vt.copy(lds[j & 1][1], wave, head_rows(a.v, row, g, n, a.head_dim));
+    kt.copy(lds[j & 1][0], wave, kw.rows(n));
+    vt.copy(lds[j & 1][1], wave, vw.rows(n));
+    kw.step(kKeys);
+    vw.step(kKeys);
   };
 
   f32x16 o[DP / 32];

@@ -21,7 +21,9 @@ using namespace attn;
 constexpr int kWaves = 8;
 constexpr int kRows = 32 * kWaves;
 constexpr int kKeys = 64;     // keys of a dq tile
-constexpr int kQueries = 64;  // queries of a dkdv tile
+constexpr int kKeyWaves = 4;  // waves over the keys of a dkdv workgroup; two halves of them
+constexpr int kKeyRows = 32 * kKeyWaves;
+static_assert(kWaves == 2 * kKeyWaves, "two halves");
 
 template <int DP>
 __global__ __launch_bounds__(512, 2) void attention_dq_kernel(AttentionArgs a) {
@@ -78,11 +80,13 @@ __global__ __launch_bounds__(512, 2) void attention_dq_kernel(AttentionArgs a) {
   KTile kt, vt;
   kt.init(wave, lane, a.k.row, a.head_dim);
   vt.init(wave, lane, a.v.row, a.head_dim);
-  auto copy_tile = [&](int j) {
+  Walk kw(a.k, s.k0, g, a.head_dim), vw(a.v, s.k0, g, a.head_dim);
+  auto copy_tile = [&](int j) {  // tiles in their order
     const int n = min(s.kn - j * kKeys, kKeys);
-    const int64_t row = (int64_t)s.k0 + j * kKeys;
-    kt.copy(lds[j & 1][0], wave, head_rows(a.k, row, g, n, a.head_dim));
-    vt.copy(lds[j & 1][1], wave, head_rows(a.v, row, g, n, a.head_dim));
+    kt.copy(lds[j & 1][0], wave, kw.rows(n));
+    vt.copy(lds[j & 1][1], wave, vw.rows(n));
+    kw.step(kKeys);
+    vw.step(kKeys);
   };
 
   f32x16 acc[DP / 32];
@@ -164,145 +168,186 @@ __global__ __launch_bounds__(512, 2) void attention_dq_kernel(AttentionArgs a) {
 
 template <int DP>
 __global__ __launch_bounds__(512, 2) void attention_dkdv_kernel(AttentionArgs a) {
-  typedef Tile<DP, kQueries, kWaves> QTile;
-  typedef Tile<DP, kRows, kWaves> VTile;
-  // two stages of Q rows, dO rows and their statistics, and the workgroup's V rows
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][QTile::kBytes];
+  typedef Tile<DP, 32, kKeyWaves> QTile;
+  typedef Tile<DP, kKeyRows, kWaves> VTile;
+  constexpr int kDims = DP / 32;   // 32-column panels
+  constexpr int kSteps = DP / 16;  // products of one 32x32 square
+  // two stages of each half's Q rows, dO rows and their lse2 and -delta; the V rows
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][2][QTile::kBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t vlds[VTile::kBytes];
-  __shared__ __attribute__((aligned(256))) float stats[2][2][kQueries];  // lse2, -delta
+  __shared__ __attribute__((aligned(256))) float stats[2][2][2][64];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int half = wave / kKeyWaves, kw = wave % kKeyWaves;
   const int g = blockIdx.x % a.kv_heads;
   int b, rank, tiles;
-  if (!find_tile(a.cu_k, a.batch, a.total_k, 1, kRows, blockIdx.x / a.kv_heads, b, rank, tiles))
+  if (!find_tile(a.cu_k, a.batch, a.total_k, 1, kKeyRows, blockIdx.x / a.kv_heads, b, rank, tiles))
     return;
   const Sequence s = load_sequence(a, b);
-  const int row0 = (tiles - 1 - rank) * kRows;  // the first keys are seen by the most queries
-  const int key = row0 + wave * 32 + (lane & 31);
+  const int row0 = (tiles - 1 - rank) * kKeyRows;  // the first keys are seen by the most queries
+  const int key0 = row0 + kw * 32;                 // the wave's first key
+  const int key = key0 + (lane & 31);
   const bool used = key < s.kn;
   const int64_t krow = s.k0 + min(key, s.ka - 1);
-  const uint16_t* kp = a.k.p + krow * a.k.row + g * a.k.head;
-  bf16x8 k[DP / 16];
-#pragma unroll
-  for (int ks = 0; ks < DP / 16; ++ks)
-    k[ks] = load8(kp, ks * 16 + 8 * (lane >> 5), a.head_dim, used);
   {
     VTile vt;
     vt.init(wave, lane, a.v.row, a.head_dim);
-    vt.copy(vlds, wave,
-            head_rows(a.v, (int64_t)s.k0 + row0, g, min(s.kn - row0, kRows), a.head_dim));
+    const Walk vw(a.v, (int64_t)s.k0 + row0, g, a.head_dim);
+    vt.copy(vlds, wave, vw.rows(min(s.kn - row0, kKeyRows)));
   }
-  // query i sees keys up to i + kn - qn
-  const int back = a.causal ? s.qn - s.kn : -s.kn;  // first query that sees key: key + back
-  const int first = row0 < s.kn ? max(row0 + back, 0) / kQueries * kQueries : s.qn;
-  const int wave_first = row0 + wave * 32 + back;  // first query that sees the wave's first key
+  // query i sees keys up to i + kn - qn: key j is first seen by query j + back
+  const int back = a.causal ? s.qn - s.kn : -s.kn;
+  const int first = row0 < s.kn ? max(row0 + back, 0) & ~31 : s.qn;
+  const int per_head = first < s.qn ? (s.qn - first + 31) / 32 : 0;
+  const int total = per_head * a.group;  // squares of queries, head after head
+  const int wave_first = key0 + back;
   // first query of no masking: the one that sees the wave's last key, or none
   // if some of its keys are past the used length and must vanish
-  const bool all_used = row0 + wave * 32 + 31 < s.kn;
-  const int wave_free = all_used ? row0 + wave * 32 + 31 + back : 0x7FFFFFFF;
+  const int wave_free = key0 + 31 < s.kn ? key0 + 31 + back : 0x7FFFFFFF;
   const int from = used ? key + back : 0x7FFFFFFF;  // first query that sees this lane's key
 
+  // this half's queries: i0 .. i0 + 31 of the group's hh-th head, n-th of all
   QTile qt, dt;
-  qt.init(wave, lane, a.q.row, a.head_dim);
-  dt.init(wave, lane, a.dout.row, a.head_dim);
-  // tile of queries i0 .. of the h-th head of the group into stage n
-  auto copy_tile = [&](int n, int hh, int i0) {
-    const int h = g * a.group + hh;
-    const int rows = min(s.qn - i0, kQueries);
-    qt.copy(lds[n][0], wave, head_rows(a.q, (int64_t)s.q0 + i0, h, rows, a.head_dim));
-    dt.copy(lds[n][1], wave, head_rows(a.dout, (int64_t)s.q0 + i0, h, rows, a.head_dim));
-    if (wave < 2) {
-      const float* src = wave == 0 ? a.lse2 : a.delta;
-      copy4(uniform(lds_offset(&stats[n][wave][0])), lane * 4,
-            buffer(src + (int64_t)h * a.total_q + s.q0 + i0, rows * 4));
-    }
-  };
-
-  f32x16 dk[DP / 32], dv[DP / 32];
+  qt.init(kw, lane, a.q.row, a.head_dim);
+  dt.init(kw, lane, a.dout.row, a.head_dim);
+  Walk qw(a.q, (int64_t)s.q0 + first, g * a.group, a.head_dim);
+  Walk dw(a.dout, (int64_t)s.q0 + first, g * a.group, a.head_dim);
+  const int64_t q_next = a.q.head * 2 - static_cast<int64_t>(per_head) * 32 * qw.row_bytes;
+  const int64_t d_next = a.dout.head * 2 - static_cast<int64_t>(per_head) * 32 * dw.row_bytes;
+  const int64_t stat_next = (static_cast<int64_t>(a.total_q) - per_head * 32) * 4;
+  uint64_t stat_at = reinterpret_cast<uint64_t>(
+      (kw == 0 ? a.lse2 : a.delta) + static_cast<int64_t>(g) * a.group * a.total_q + s.q0 + first);
+  int left = s.qn - first;  // rows from the walks' place to the end of the sequence
+  auto pass = [&](int n) {  // the walks go on by n squares of 32 rows
+    qw.step(32 * n);
+    dw.step(32 * n);
+    stat_at += 32 * 4 * n;
+    left -= 32 * n;
 #pragma unroll
-  for (int ct = 0; ct < DP / 32; ++ct) dk[ct] = dv[ct] = f32x16{};
-  int hh = 0, i0 = first, n = 0;
-  const bool any = first < s.qn;
-  if (any) copy_tile(0, 0, first);
-  while (any) {
-    int next_h = hh, next_i = i0 + kQueries;
-    if (next_i >= s.qn) {
-      next_i = first;
-      ++next_h;
-    }
+    for (int twice = 0; twice < 2; ++twice)
+      if (left <= 0) {  // into the next head
+        qw.at += q_next;
+        dw.at += d_next;
+        stat_at += stat_next;
+        left += per_head * 32;
+      }
+  };
+  if (half == 1 && total > 0) pass(1);
+  int copied = half;
+  auto copy_square = [&](int stage) {
+    const int rows = copied < total ? min(left, 32) : 0;
+    qt.copy(lds[stage][half][0], kw, qw.rows(rows));
+    dt.copy(lds[stage][half][1], kw, dw.rows(rows));
+    if (kw < 2)
+      copy4(uniform(lds_offset(&stats[stage][half][kw][0])), lane * 4, buffer(stat_at, rows * 4));
+    copied += 2;  // the halves take squares in turn
+    pass(2);
+  };
+  if (total > 0) copy_square(0);
+  const uint16_t* kp = a.k.p + krow * a.k.row + g * a.k.head;
+  bf16x8 k[kSteps];
+#pragma unroll
+  for (int ks = 0; ks < kSteps; ++ks)
+    k[ks] = load8(kp, ks * 16 + 8 * (lane >> 5), a.head_dim, used);
+
+  f32x16 dk[kDims], dv[kDims];
+#pragma unroll
+  for (int ct = 0; ct < kDims; ++ct) dk[ct] = dv[ct] = f32x16{};
+  int at = per_head == 1 ? 0 : half;  // this half's square of its head
+  for (int n = 0; n < total; n += 2) {
+    const int stage = (n >> 1) & 1;
     wait_copies<0>();
     __syncthreads();
-    if (next_h < a.group) copy_tile(n ^ 1, next_h, next_i);
-    const uint8_t* Q = lds[n][0];
-    const uint8_t* D = lds[n][1];
+    if (n + 2 < total) copy_square(stage ^ 1);
+    const int i0 = first + at * 32;
+    at += 2;
+    if (at >= per_head) at -= per_head;
+    if (at >= per_head) at -= per_head;
+    if (n + half >= total || i0 + 31 < wave_first) continue;
+    const uint8_t* Q = lds[stage][half][0];
+    const uint8_t* D = lds[stage][half][1];
+    const float* lses = stats[stage][half][0] + 4 * (lane >> 5);
+    const float* deltas = stats[stage][half][1] + 4 * (lane >> 5);
+    // S and dP; dP starts from -delta
+    f32x16 p = {}, dp;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (i0 + 32 * t + 31 < wave_first) continue;
-      constexpr int kDims = DP / 32, kSteps = DP / 16;
-      // S and dP; dP starts from -delta
-      f32x16 p = {}, dp;
+    for (int e = 0; e < 16; ++e) dp[e] = deltas[8 * (e >> 2) + (e & 3)];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+    for (int ks = 0; ks < kSteps; ++ks) p = mma(QTile::rows(Q, 0, ks, lane), k[ks], p);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          dp[4 * c + e] = stats[n][1][32 * t + 8 * c + 4 * (lane >> 5) + e];
+    for (int ks = 0; ks < kSteps; ++ks)
+      dp = mma(QTile::rows(D, 0, ks, lane), VTile::rows(vlds, kw * 32, ks, lane), dp);
+    __builtin_amdgcn_sched_group_barrier(kSchedRead, 4 + 4, 0);  // 4 of -delta
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) p = mma(QTile::rows(Q, 32 * t, ks, lane), k[ks], p);
+    for (int i = 0; i < kSteps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks)
-        dp = mma(QTile::rows(D, 32 * t, ks, lane), VTile::rows(vlds, wave * 32, ks, lane), dp);
-      __builtin_amdgcn_sched_group_barrier(kSchedRead, 4, 0);
+    for (int i = 0; i < kSteps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+    }
+    f32x16 lse2;
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
-      }
+    for (int e = 0; e < 16; ++e) lse2[e] = lses[8 * (e >> 2) + (e & 3)];
+    if (i0 < wave_free) {
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
-      }
-      f32x16 lse2;
+      for (int e = 0; e < 16; ++e)
+        if (i0 + acc_row(e, lane) < from) p[e] = -INFINITY;
+    }
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+    for (int e = 0; e < 16; ++e) {
+      p[e] = __builtin_amdgcn_exp2f(fmaf(p[e], a.scale_log2, -lse2[e]));
+      dp[e] *= p[e];
+    }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          lse2[4 * c + e] = stats[n][0][32 * t + 8 * c + 4 * (lane >> 5) + e];
-      if (i0 + 32 * t < wave_free) {
+    for (int u = 0; u < 2; ++u) {
+      const bf16x8 pu = narrow(p, u), du = narrow(dp, u);
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (i0 + 32 * t + acc_row(e, lane) < from) p[e] = -INFINITY;
-      }
+      for (int ct = 0; ct < kDims; ++ct)
+        dv[ct] = mma(QTile::columns(D, 16 * u, ct, lane), pu, dv[ct]);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(fmaf(p[e], a.scale_log2, -lse2[e]));
-        dp[e] *= p[e];
-      }
+      for (int ct = 0; ct < kDims; ++ct)
+        dk[ct] = mma(QTile::columns(Q, 16 * u, ct, lane), du, dk[ct]);
+    }
+    __builtin_amdgcn_sched_group_barrier(kSchedRead, 8, 1);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bf16x8 pu = narrow(p, u), du = narrow(dp, u);
+    for (int i = 0; i < 4 * kDims; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 1);
+    }
+  }
+  // The halves' sums: the first half takes dV, the second dK, 32 columns at a
+  // time through the LDS that the tiles no longer need (nothing is under way)
+  wait_copies<0>();
+  f32x4* mine = reinterpret_cast<f32x4*>(&lds[0][0][0][0]) + ((half * kKeyWaves + kw) * 4) * 64 + lane;
+  const f32x4* other =
+      reinterpret_cast<f32x4*>(&lds[0][0][0][0]) + (((half ^ 1) * kKeyWaves + kw) * 4) * 64 + lane;
 #pragma unroll
-        for (int ct = 0; ct < kDims; ++ct)
-          dv[ct] = mma(QTile::columns(D, 32 * t + 16 * u, ct, lane), pu, dv[ct]);
+  for (int ct = 0; ct < kDims; ++ct) {
+    __syncthreads();
 #pragma unroll
-        for (int ct = 0; ct < kDims; ++ct)
-          dk[ct] = mma(QTile::columns(Q, 32 * t + 16 * u, ct, lane), du, dk[ct]);
-      }
-      __builtin_amdgcn_sched_group_barrier(kSchedRead, 8, 1);
+    for (int c = 0; c < 4; ++c) {
+      const f32x16& give = half == 0 ? dk[ct] : dv[ct];
+      mine[c * 64] = f32x4{give[4 * c], give[4 * c + 1], give[4 * c + 2], give[4 * c + 3]};
+    }
+    __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4 * kDims; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 1);
-        __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 1);
+    for (int c = 0; c < 4; ++c) {
+      const f32x4 add = other[c * 64];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (half == 0) dv[ct][4 * c + e] += add[e];
+        else dk[ct][4 * c + e] += add[e];
       }
     }
-    if (next_h == a.group) break;
-    hh = next_h;
-    i0 = next_i;
-    n ^= 1;
   }
-  wait_copies<0>();  // no copy may land after the workgroup has given up its LDS
   if (key >= s.ka) return;
-  store_row<DP>(a.dv.p + krow * a.dv.row + g * a.dv.head, dv, 1.0f, a.head_dim, lane);
-  store_row<DP>(a.dk.p + krow * a.dk.row + g * a.dk.head, dk, a.scale, a.head_dim, lane);
+  if (half == 0)
+    store_row<DP>(a.dv.p + krow * a.dv.row + g * a.dv.head, dv, 1.0f, a.head_dim, lane);
+  else
+    store_row<DP>(a.dk.p + krow * a.dk.row + g * a.dk.head, dk, a.scale, a.head_dim, lane);
 }
 
 template <int DP>
@@ -317,16 +362,17 @@ bfp8_status launch_backward(const AttentionArgs& a, int64_t q_blocks, int64_t k_
   return st;
 }
 
-int64_t tile_bound(const int32_t* cu, int64_t batch, int64_t total, int64_t mult) {
-  if (cu == nullptr) return batch * ((total / batch * mult + kRows - 1) / kRows);
-  return (total * mult + batch * (kRows - 1)) / kRows;
+// An upper bound on the tiles of all sequences, whose lengths are on the device.
+int64_t tile_bound(const int32_t* cu, int64_t batch, int64_t total, int64_t mult, int64_t unit) {
+  if (cu == nullptr) return batch * ((total / batch * mult + unit - 1) / unit);
+  return (total * mult + batch * (unit - 1)) / unit;
 }
 
 }  // namespace
 
 bfp8_status launch_attention_backward(const AttentionArgs& a, hipStream_t stream) {
-  const int64_t q_blocks = tile_bound(a.cu_q, a.batch, a.total_q, a.group) * a.kv_heads;
-  const int64_t k_blocks = tile_bound(a.cu_k, a.batch, a.total_k, 1) * a.kv_heads;
+  const int64_t q_blocks = tile_bound(a.cu_q, a.batch, a.total_q, a.group, kRows) * a.kv_heads;
+  const int64_t k_blocks = tile_bound(a.cu_k, a.batch, a.total_k, 1, kKeyRows) * a.kv_heads;
   if (q_blocks >= (int64_t(1) << 31) || k_blocks >= (int64_t(1) << 31)) return BFP8_ERR_SHAPE;
   return a.head_dim <= 64 ? launch_backward<64>(a, q_blocks, k_blocks, stream)
                           : launch_backward<128>(a, q_blocks, k_blocks, stream);
