@@ -241,9 +241,11 @@ __device__ __forceinline__ void copy4(uint32_t lds, uint32_t off, i32x4 rsrc) {
 // Until at most LEFT of this wave's copies are under way (they end in order).
 template <int LEFT>
 __device__ __forceinline__ void wait_copies() {
-  static_assert(LEFT < 16, "the low four bits of vmcnt");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | LEFT);
+  static_assert(LEFT < 64, "vmcnt has six bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (LEFT & 15) | (LEFT >> 4) << 14);
 }
+// Until this wave's LDS reads have returned.
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));

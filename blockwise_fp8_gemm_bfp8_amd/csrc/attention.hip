@@ -170,11 +170,329 @@ __global__ __launch_bounds__(512, 2) void attention_forward_kernel(AttentionArgs
         sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
 }
 
+// ---- few query rows ---------------------------------------------------------
+//
+// Generation: one or a few queries of each sequence over its cached keys.  The
+// work is reading K and V once, so what counts is that every CU streams, all
+// the time and equally long.  The work is a line of tiles of 32 keys: sequence
+// after sequence, kv head after kv head (and 32 rows after 32 rows, should a
+// head have more), key tile after key tile.  Each wave, a workgroup of its own,
+// takes an equal stretch of the line through two LDS stages, without barriers.
+// Where a stretch ends inside a segment (one kv head's 32 rows), its float32
+// results go to the workspace, and a second kernel joins a segment's parts in
+// their order.
+constexpr int kStreams = 1280;  // as many 32 KiB workgroups as 256 CUs of 160 KiB hold
+constexpr int kMinShare = 3;    // line units of a stretch at least
+// A segment counts for so many tiles more than it has, for the latency of its
+// first loads; they come first.
+constexpr int kSegmentCost = 1;
+
+// The results of a stretch that covers a part of a segment: part 2 w is of the
+// segment that stretch w began in, part 2 w + 1 of the one it ended in.
+struct Parts {
+  float* o;    // [2 kStreams][32][head_dim], each over its own maximum
+  float2* ml;  // [2 kStreams][32]: maximum (in powers of two) and sum
+};
+
+// A place on the line of tiles.
+struct Place {
+  int b;         // sequence
+  int segment;   // in it: kv head, then 32 rows
+  int unit;      // in the segment: kSegmentCost, then its key tiles
+  int units, segments;  // of the sequence's segments
+};
+
+__device__ __forceinline__ void line_units(const AttentionArgs& a, int b, int& units,
+                                           int& segments) {
+  int q0, qn, k0, kn;
+  cu_range(a.cu_q, a.batch, a.total_q, b, q0, qn);
+  cu_range(a.cu_k, a.batch, a.total_k, b, k0, kn);
+  if (a.k_lens != nullptr) kn = clampi(a.k_lens[b], 0, kn);
+  units = kSegmentCost + max((kn + 31) / 32, 1);  // rows without keys have a result, too
+  segments = (qn * a.group + 31) / 32 * a.kv_heads;
+}
+
+// Length of the line and the place of unit number `share(length)` * n; false
+// past its end.  Each wave by itself, 64 sequences at a time.
+template <typename Share>
+__device__ __forceinline__ bool find_place(const AttentionArgs& a, int n, Share share, int& length,
+                                           int& at, Place& p) {
+  const int lane = threadIdx.x & 63;
+  length = 0;
+  int units = 0, segments = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    units = segments = 0;
+    if (b0 + lane < a.batch) line_units(a, b0 + lane, units, segments);
+    length += wave_sum(units * segments);
+  }
+  at = n * share(length);
+  if (at >= length) return false;
+  int base = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    if (a.batch > 64) {
+      units = segments = 0;
+      if (b0 + lane < a.batch) line_units(a, b0 + lane, units, segments);
+    }
+    int sum = units * segments;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int up = __shfl_up(sum, d);
+      if (lane >= d) sum += up;
+    }
+    const uint64_t past = __ballot(at < base + sum);
+    if (past != 0) {
+      const int l = uniform(__ffsll(static_cast<unsigned long long>(past)) - 1);
+      p.b = b0 + l;
+      p.units = __builtin_amdgcn_readlane(units, l);
+      p.segments = __builtin_amdgcn_readlane(segments, l);
+      const int in = at - base - (__builtin_amdgcn_readlane(sum, l) - p.units * p.segments);
+      p.segment = in / p.units;
+      p.unit = in - p.segment * p.units;
+      return true;
+    }
+    base += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
+}
+
+__device__ __forceinline__ int stream_share(int length) {
+  return max((length + kStreams - 1) / kStreams, kMinShare);
+}
+
+template <int DP>
+__global__ __launch_bounds__(64, 1) void attention_stream_kernel(AttentionArgs a, Parts parts) {
+  typedef Tile<DP, 32, 1> KTile;
+  constexpr int kDims = DP / 32, kSteps = DP / 16;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][KTile::kBytes];
+  const int lane = threadIdx.x;
+  int length, at;
+  Place p;
+  if (!find_place(a, blockIdx.x, stream_share, length, at, p)) return;
+  int remaining = min(stream_share(length), length - at);
+
+  KTile kt, vt;
+  kt.init(0, lane, a.k.row, a.head_dim);
+  vt.init(0, lane, a.v.row, a.head_dim);
+  Sequence s = load_sequence(a, p.b);
+  while (true) {
+    const int end = min(p.unit + remaining, p.units);
+    remaining -= end - p.unit;
+    const int t0 = max(p.unit - kSegmentCost, 0), t1 = max(end - kSegmentCost, 0);
+    if (t0 < t1) {  // this stretch has tiles of the segment
+      const int row_tiles = p.segments / a.kv_heads;
+      const int g = p.segment / row_tiles;
+      const int row0 = (p.segment - g * row_tiles) * 32;
+      const int rows = s.qn * a.group;
+      const int shift = a.causal ? s.kn - s.qn : s.kn;
+      const int r = row0 + (lane & 31);
+      const bool valid = r < rows;
+      const int i = min(r, rows - 1) / a.group;
+      const int h = g * a.group + r % a.group;
+      const int lim = min(i + shift, s.kn - 1);
+      const int free = min(row0 / a.group + shift, s.kn - 1);  // seen by every row
+      Walk kw(a.k, (int64_t)s.k0 + t0 * 32, g, a.head_dim);
+      Walk vw(a.v, (int64_t)s.k0 + t0 * 32, g, a.head_dim);
+      int left = min(t1 * 32, s.kn) - t0 * 32;  // keys from the walks' place on
+      auto copy_tile = [&](int stage) {         // past the end: zeros, counted as the others
+        kt.copy(lds[stage][0], 0, kw.rows(min(left, 32)));
+        vt.copy(lds[stage][1], 0, vw.rows(min(left, 32)));
+        kw.step(32);
+        vw.step(32);
+        left -= 32;
+      };
+      const uint16_t* qrow = a.q.p + (int64_t)(s.q0 + i) * a.q.row + h * a.q.head;
+      bf16x8 q[kSteps];
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+        q[ks] = load8(qrow, ks * 16 + 8 * (lane >> 5), a.head_dim, valid);
+      copy_tile(0);
+      copy_tile(1);
+      f32x16 o[kDims];
+#pragma unroll
+      for (int ct = 0; ct < kDims; ++ct) o[ct] = f32x16{};
+      float m = -INFINITY, l = 0.0f;
+      int stage = 0;
+      for (int t = t0; t < t1; ++t) {
+        wait_copies<2 * KTile::kCopies>();
+        const uint8_t* K = lds[stage][0];
+        const uint8_t* V = lds[stage][1];
+        f32x16 x = {};
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) x = mma(KTile::rows(K, 0, ks, lane), q[ks], x);
+        if (t * 32 + 31 > free) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (t * 32 + acc_row(e, lane) > lim) x[e] = -INFINITY;
+        }
+        float top = x[0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
+        top = pair_max(top) * a.scale_log2;
+        if (__any(top > m + kSlack)) {
+          const float next = fmaxf(m, top);
+          const float alpha = __builtin_amdgcn_exp2f(m - (next == -INFINITY ? 0.0f : next));
+          m = next;
+          l *= alpha;
+#pragma unroll
+          for (int ct = 0; ct < kDims; ++ct)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[ct][e] *= alpha;
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale_log2, -base));
+          l += x[e];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const bf16x8 xu = narrow(x, u);
+#pragma unroll
+          for (int ct = 0; ct < kDims; ++ct)
+            o[ct] = mma(KTile::columns(V, 16 * u, ct, lane), xu, o[ct]);
+        }
+        wait_lds();  // the stage has been read
+        copy_tile(stage);
+        stage ^= 1;
+      }
+      wait_copies<0>();
+      l = pair_sum(l);
+      if (valid) {
+        if (t0 == 0 && end == p.units) {
+          uint16_t* orow = a.o.p + (int64_t)(s.q0 + i) * a.o.row + h * a.o.head;
+          store_row<DP>(orow, o, l > 0.0f ? 1.0f / l : 0.0f, a.head_dim, lane);
+          if (lane < 32)
+            a.lse[(int64_t)h * a.total_q + s.q0 + i] =
+                l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+        } else {
+          const int64_t part = (2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * 32 + (lane & 31);
+          float* to = parts.o + part * a.head_dim;
+#pragma unroll
+          for (int ct = 0; ct < kDims; ++ct)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int d = ct * 32 + 8 * c + 4 * (lane >> 5);
+              if (d < a.head_dim)
+                *reinterpret_cast<f32x4*>(to + d) = f32x4{o[ct][4 * c], o[ct][4 * c + 1],
+                                                          o[ct][4 * c + 2], o[ct][4 * c + 3]};
+            }
+          if (lane < 32) parts.ml[part] = make_float2(m, l);
+        }
+      }
+    }
+    if (remaining == 0) return;
+    p.unit = 0;
+    if (++p.segment == p.segments) {  // on to the next sequence that has rows
+      p.segment = 0;
+      do {
+        ++p.b;  // there is one: units remain
+        line_units(a, p.b, p.units, p.segments);
+        p.units = uniform(p.units);
+        p.segments = uniform(p.segments);
+      } while (p.segments == 0);
+      s = load_sequence(a, p.b);
+    }
+  }
+}
+
+// Joins the parts of one segment in their order.  Workgroup n looks at the
+// boundary between stretches n and n + 1: where it lies among the tiles of a
+// segment and is the first that does, it joins that segment.  8 rows at a
+// time; where there are fewer, several groups of threads share a row's parts.
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Parts parts) {
+  __shared__ f32x4 other_o[256];
+  __shared__ float2 other_ml[256];
+  int length, at;
+  Place p;
+  const int n = blockIdx.x;
+  if (!find_place(a, n + 1, stream_share, length, at, p)) return;
+  const int share = stream_share(length);
+  // a boundary at or before the first tile leaves the stretch before it no part
+  const int first_tile = at - p.unit + kSegmentCost;  // on the line
+  if (p.unit <= kSegmentCost || first_tile / share != n) return;
+  const int last = (at - p.unit + p.units - 1) / share;  // stretch in which the segment ends
+  const Sequence s = load_sequence(a, p.b);
+  const int row_tiles = p.segments / a.kv_heads;
+  const int g = p.segment / row_tiles;
+  const int row0 = (p.segment - g * row_tiles) * 32;
+  const int rows = min(s.qn * a.group - row0, 32);
+  const int per_row = a.head_dim / 4;
+  const int slots = 256 / per_row;            // at least 8
+  const int shared = max(slots / rows, 1);    // slots of one row
+  const int at_once = slots / shared;         // rows
+  const int slot = threadIdx.x / per_row;
+  const int d = (threadIdx.x - slot * per_row) * 4;
+  const int sub = slot / at_once;
+  for (int r0 = 0; r0 < rows; r0 += at_once) {
+    const int r = r0 + slot - sub * at_once;
+    float top = -INFINITY, sum = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto add = [&](float2 x, f32x4 v) {
+      const float next = fmaxf(top, x.x);
+      const float base = next == -INFINITY ? 0.0f : next;
+      const float keep = __builtin_amdgcn_exp2f(top - base);
+      const float mul = __builtin_amdgcn_exp2f(x.x - base);
+      top = next;
+      sum = sum * keep + x.y * mul;
+      o = o * keep + v * mul;
+    };
+    if (sub < shared && r < rows) {
+#pragma unroll 4
+      for (int w = n + sub; w <= last; w += shared) {
+        const int64_t part = (2 * w + (w == n ? 1 : 0)) * 32 + r;
+        add(parts.ml[part], *reinterpret_cast<const f32x4*>(parts.o + part * a.head_dim + d));
+      }
+    }
+    __syncthreads();
+    other_o[threadIdx.x] = o;
+    other_ml[threadIdx.x] = make_float2(top, sum);
+    __syncthreads();
+    if (sub != 0 || r >= rows) continue;
+    for (int k = 1; k < shared; ++k) {
+      const int from = threadIdx.x + k * at_once * per_row;
+      add(other_ml[from], other_o[from]);
+    }
+    const int i = (row0 + r) / a.group, h = g * a.group + (row0 + r) % a.group;
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    u32x2 w;
+    w.x = pack_bf16x2(o[0] * inv, o[1] * inv);
+    w.y = pack_bf16x2(o[2] * inv, o[3] * inv);
+    *reinterpret_cast<u32x2*>(a.o.p + (int64_t)(s.q0 + i) * a.o.row + h * a.o.head + d) = w;
+    if (d == 0)
+      a.lse[(int64_t)h * a.total_q + s.q0 + i] =
+          sum > 0.0f ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+// Few rows: the heads of a group give no more than one 32-row operand a
+// sequence on average.  (The line's units are counted in 32 bits.)
+bool few_rows(const AttentionArgs& a) {
+  const int64_t row_tiles = (int64_t)a.total_q * a.group / 32 + a.batch;
+  const int64_t key_tiles = (int64_t)a.total_k / 32 + (1 + kSegmentCost) * a.batch;
+  return a.total_q > 0 && (int64_t)a.total_q * a.group <= (int64_t)32 * a.batch &&
+         row_tiles * key_tiles * a.kv_heads < (int64_t(1) << 31);
+}
+
 }  // namespace
 
-size_t attention_forward_workspace(const AttentionArgs&) { return 0; }
+size_t attention_forward_workspace(const AttentionArgs& a) {
+  if (!few_rows(a)) return 0;
+  return static_cast<size_t>(2 * kStreams) * 32 * (a.head_dim + 2) * sizeof(float);
+}
 
-bfp8_status launch_attention_forward(const AttentionArgs& a, void*, size_t, hipStream_t stream) {
+bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream) {
+  if (few_rows(a) && workspace != nullptr && workspace_bytes >= attention_forward_workspace(a)) {
+    Parts parts;
+    parts.o = static_cast<float*>(workspace);
+    parts.ml = reinterpret_cast<float2*>(parts.o + 2 * kStreams * 32 * a.head_dim);
+    const bfp8_status st =
+        a.head_dim <= 64
+            ? launch(attention_stream_kernel<64>, dim3(kStreams), dim3(64), stream, a, parts)
+            : launch(attention_stream_kernel<128>, dim3(kStreams), dim3(64), stream, a, parts);
+    if (st != BFP8_OK) return st;
+    return launch(attention_join_kernel, dim3(kStreams - 1), dim3(256), stream, a, parts);
+  }
   // an upper bound on the tiles of all sequences: the lengths are on the device
   int64_t tiles;
   if (a.cu_q == nullptr)
