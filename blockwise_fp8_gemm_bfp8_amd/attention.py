@@ -17,37 +17,51 @@ ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
-def _check_heads(t: torch.Tensor, name: str, dtypes, device=None):
+# The calls below are short (a decode step's kernels take a few microseconds),
+# so the marshalling is kept short, too: each tensor's sizes and strides are
+# fetched once, and the current stream's handle without building a Stream.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device: int):
+    if _raw_stream is not None:
+        return _raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _heads(t: torch.Tensor, name: str, dtypes, device: int = None, shape=None):
+    """Check a tensor of heads; returns its device, shape and bfp8_heads.
+    The strides of axes with one entry do not matter and take the values of a
+    dense tensor."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != 3:
+    at = t.get_device()
+    if device is not None and at != device:
+        raise ValueError(f"{name} must be on device {device}, got {at}")
+    size = t.shape
+    if len(size) != 3:
         raise ValueError(f"{name} must be 3-D [tokens][heads][head_dim]")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.numel() and t.stride(2) != 1:
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(size)}")
+    T, H, D = size
+    row, head, one = t.stride()
+    if one != 1 and D > 1 and T and H:
         raise ValueError(f"{name} must have unit stride along its last axis")
+    if H <= 1:
+        head = D
+    if T <= 1:
+        row = max(H * head, D)
+    return at, size, Heads(t.data_ptr(), row, head)
 
 
-def _strides(t: torch.Tensor):
-    """(row, head) strides; those of axes with one entry do not matter and
-    take the values of a dense tensor."""
-    T, H, D = t.shape
-    head = t.stride(1) if H > 1 else D
-    return (t.stride(0) if T > 1 else max(H * head, D)), head
-
-
-def _heads(t: torch.Tensor) -> Heads:
-    row, head = _strides(t)
-    return Heads(t.data_ptr(), row, head)
-
-
-def _check_i32(t, name: str, n: int, device):
+def _check_i32(t, name: str, n: int, device: int):
     if t is None:
         return
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a dense 1-D int32 tensor on {device}")
+    if (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()
+            or not t.is_cuda or t.get_device() != device):
+        raise ValueError(f"{name} must be a dense 1-D int32 tensor on device {device}")
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
 
@@ -87,88 +101,82 @@ def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor = None,
     ``out=x`` works in place.  See bfp8_rope."""
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
-    _check_heads(x, "x", tuple(DTYPES))
+    device, size, xh = _heads(x, "x", DTYPES)
     if (table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32
-            or not table.is_contiguous() or table.device != x.device):
-        raise ValueError(f"table must be a dense float32 [length][rot_dim/2][2] on {x.device}")
-    T, H, D = x.shape
-    _check_i32(positions, "positions", T, x.device)
+            or not table.is_contiguous() or not table.is_cuda or table.get_device() != device):
+        raise ValueError(f"table must be a dense float32 [length][rot_dim/2][2] on device {device}")
+    T, H, D = size
+    _check_i32(positions, "positions", T, device)
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    else:
-        _check_heads(out, "out", (x.dtype,), x.device)
-        if out.shape != x.shape:
-            raise ValueError("out must have the shape of x")
-    xr, xh = _strides(x)
-    yr, yh = _strides(out)
+        out = x.new_empty(size)
+    _, _, yh = _heads(out, "out", (x.dtype,), device, size)
+    length, half, _ = table.shape
     _check("bfp8_rope", lib().bfp8_rope(
-        x.data_ptr(), xr, xh, out.data_ptr(), yr, yh, DTYPES[x.dtype], T, H, D,
-        2 * table.shape[1], ROPE_LAYOUTS[layout], table.data_ptr(), table.shape[0],
-        _pointer(positions), int(inverse), _stream(x)))
+        xh.data, xh.row, xh.head, yh.data, yh.row, yh.head, DTYPES[x.dtype], T, H, D, 2 * half,
+        ROPE_LAYOUTS[layout], table.data_ptr(), length, _pointer(positions), int(inverse),
+        _stream_of(device)))
     return out
 
 
 # ---- attention --------------------------------------------------------------
 
 _BF16 = (torch.bfloat16,)
+_INVALID = ctypes.c_size_t(-1).value  # bfp8_attention_workspace_bytes of an invalid shape
 
 
-def _shape(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale) -> AttentionShape:
-    _check_heads(q, "q", _BF16)
-    _check_heads(k, "k", _BF16, q.device)
-    _check_heads(v, "v", _BF16, q.device)
-    Tq, H, D = q.shape
-    Tk, KV, Dk = k.shape
-    if v.shape != k.shape:
-        raise ValueError(f"k and v must have one shape, got {tuple(k.shape)} and {tuple(v.shape)}")
+def _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale):
+    """Check the inputs; returns (device, bfp8_attention_shape, q, k, v as
+    bfp8_heads)."""
+    device, qs, qh = _heads(q, "q", _BF16)
+    _, ks, kh = _heads(k, "k", _BF16, device)
+    _, _, vh = _heads(v, "v", _BF16, device, ks)
+    Tq, H, D = qs
+    Tk, KV, Dk = ks
     if Dk != D:
         raise ValueError(f"q and k must have one head size, got {D} and {Dk}")
     if batch is None:
-        given = [t.numel() - 1 for t in (cu_q, cu_k) if t is not None]
-        given += [k_lens.numel()] if k_lens is not None else []
-        batch = given[0] if given else 1
-    _check_i32(cu_q, "cu_q", batch + 1, q.device)
-    _check_i32(cu_k, "cu_k", batch + 1, q.device)
-    _check_i32(k_lens, "k_lens", batch, q.device)
+        batch = (cu_q.numel() - 1 if cu_q is not None else cu_k.numel() - 1 if cu_k is not None
+                 else k_lens.numel() if k_lens is not None else 1)
+    _check_i32(cu_q, "cu_q", batch + 1, device)
+    _check_i32(cu_k, "cu_k", batch + 1, device)
+    _check_i32(k_lens, "k_lens", batch, device)
     if scale is None:
         scale = 1.0 / math.sqrt(D) if D else 1.0
-    return AttentionShape(batch, Tq, Tk, _pointer(cu_q), _pointer(cu_k), _pointer(k_lens), H, KV, D,
-                          int(causal), scale)
+    shape = AttentionShape(batch, Tq, Tk, _pointer(cu_q), _pointer(cu_k), _pointer(k_lens), H, KV,
+                           D, int(causal), scale)
+    return device, shape, qh, kh, vh
 
 
 def attention_workspace_bytes(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = None,
                               causal: bool = True, scale: float = None,
                               backward: bool = False) -> int:
     """Workspace bytes of attention_forward, or of attention_backward."""
-    s = _shape(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
-    n = int(lib().bfp8_attention_workspace_bytes(ctypes.byref(s), int(backward)))
-    if n == ctypes.c_size_t(-1).value:
+    _, s, *_ = _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
+    n = lib().bfp8_attention_workspace_bytes(ctypes.byref(s), int(backward))
+    if n == _INVALID:
         raise ValueError("invalid attention shape")
     return n
 
 
-def _workspace(shape, backward, given, device):
-    n = int(lib().bfp8_attention_workspace_bytes(ctypes.byref(shape), int(backward)))
-    if n == ctypes.c_size_t(-1).value:
-        n = 0  # the call itself reports what is wrong with the shape
-    if n and given is None:
-        given = torch.empty((n,), dtype=torch.uint8, device=device)
-    return given, (given.numel() * given.element_size() if given is not None else 0)
+def _workspace(shape, backward, given, like):
+    """(tensor or None, bytes)"""
+    if given is None:
+        n = lib().bfp8_attention_workspace_bytes(ctypes.byref(shape), backward)
+        if n == 0 or n == _INVALID:  # the call itself reports what is wrong with a shape
+            return None, 0
+        given = like.new_empty((n,), dtype=torch.uint8)
+        return given, n
+    return given, given.numel() * given.element_size()
 
 
-def _output(out, name, like, device):
-    if out is None:
-        return torch.empty(like.shape, dtype=torch.bfloat16, device=device)
-    _check_heads(out, name, _BF16, device)
-    if out.shape != like.shape:
-        raise ValueError(f"{name} must have the shape {tuple(like.shape)}")
-    return out
+def _output(out, like):
+    return like.new_empty(like.shape) if out is None else out
 
 
-def _check_lse(lse, heads, tokens, device):
+def _check_lse(lse, heads, tokens, device: int):
     if (lse.shape != (heads, tokens) or lse.dtype != torch.float32 or not lse.is_contiguous()
-            or lse.device != device):
-        raise ValueError(f"lse must be a dense float32 [{heads}][{tokens}] on {device}")
+            or not lse.is_cuda or lse.get_device() != device):
+        raise ValueError(f"lse must be a dense float32 [{heads}][{tokens}] on device {device}")
 
 
 def attention_forward(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = None,
@@ -183,16 +191,17 @@ def attention_forward(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = N
     causal      query i of n sees keys 0 .. i + m - n of m.
     scale       default 1/sqrt(D).
     A workspace is allocated when the library asks for one and none is given."""
-    s = _shape(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
-    out = _output(out, "out", q, q.device)
+    device, s, qh, kh, vh = _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
+    out = _output(out, q)
+    _, _, oh = _heads(out, "out", _BF16, device, q.shape)
     if lse is None:
-        lse = torch.empty((s.heads, s.total_q), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((s.heads, s.total_q), dtype=torch.float32)
     else:
-        _check_lse(lse, s.heads, s.total_q, q.device)
-    workspace, nbytes = _workspace(s, False, workspace, q.device)
+        _check_lse(lse, s.heads, s.total_q, device)
+    workspace, nbytes = _workspace(s, 0, workspace, q)
     _check("bfp8_attention_forward", lib().bfp8_attention_forward(
-        ctypes.byref(s), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(),
-        _pointer(workspace), nbytes, _stream(q)))
+        ctypes.byref(s), qh, kh, vh, oh, lse.data_ptr(), _pointer(workspace), nbytes,
+        _stream_of(device)))
     return out, lse
 
 
@@ -203,18 +212,16 @@ def attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, k_lens=Non
     """Gradients (dq, dk, dv) of attention_forward for the gradient `dout` of
     its `out`, given the `lse` it returned and the same sequences, mask and
     scale; see bfp8_attention_backward."""
-    s = _shape(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
-    for t, name in ((out, "out"), (dout, "dout")):
-        _check_heads(t, name, _BF16, q.device)
-        if t.shape != q.shape:
-            raise ValueError(f"{name} must have the shape of q")
-    _check_lse(lse, s.heads, s.total_q, q.device)
-    dq = _output(dq, "dq", q, q.device)
-    dk = _output(dk, "dk", k, q.device)
-    dv = _output(dv, "dv", v, q.device)
-    workspace, nbytes = _workspace(s, True, workspace, q.device)
+    device, s, qh, kh, vh = _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
+    _, _, oh = _heads(out, "out", _BF16, device, q.shape)
+    _, _, doh = _heads(dout, "dout", _BF16, device, q.shape)
+    _check_lse(lse, s.heads, s.total_q, device)
+    dq, dk, dv = _output(dq, q), _output(dk, k), _output(dv, v)
+    _, _, dqh = _heads(dq, "dq", _BF16, device, q.shape)
+    _, _, dkh = _heads(dk, "dk", _BF16, device, k.shape)
+    _, _, dvh = _heads(dv, "dv", _BF16, device, k.shape)
+    workspace, nbytes = _workspace(s, 1, workspace, q)
     _check("bfp8_attention_backward", lib().bfp8_attention_backward(
-        ctypes.byref(s), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(),
-        _heads(dout), _heads(dq), _heads(dk), _heads(dv), _pointer(workspace), nbytes,
-        _stream(q)))
+        ctypes.byref(s), qh, kh, vh, oh, lse.data_ptr(), doh, dqh, dkh, dvh, _pointer(workspace),
+        nbytes, _stream_of(device)))
     return dq, dk, dv

@@ -23,8 +23,8 @@ struct AttentionArgs {
   float scale, scale_log2;     // scale_log2 = scale * log2(e)
   Heads q, k, v, o, dout, dq, dk, dv;
   float* lse;                  // [heads][total_q]
-  float* lse2;                 // [heads][total_q] each (backward): the dq kernel
-  float* delta;                // leaves L log2(e) (0 for L = -inf) and -sum dO O
+  float* lse2;                 // [heads][total_q] each (backward): L log2(e), or 0
+  float* delta;                // for L = -inf, and -sum dO O
 };
 
 bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
@@ -88,17 +88,22 @@ __device__ __forceinline__ void cu_range(const int32_t* cu, int batch, int total
   }
 }
 
-__device__ __forceinline__ Sequence load_sequence(const AttentionArgs& a, int b) {
+// Sequence b, which may differ from lane to lane.
+__device__ __forceinline__ Sequence lane_sequence(const AttentionArgs& a, int b) {
   Sequence s;
   cu_range(a.cu_q, a.batch, a.total_q, b, s.q0, s.qn);
   cu_range(a.cu_k, a.batch, a.total_k, b, s.k0, s.ka);
   s.kn = a.k_lens == nullptr ? s.ka : clampi(a.k_lens[b], 0, s.ka);
-  s.q0 = uniform(s.q0);
-  s.qn = uniform(s.qn);
-  s.k0 = uniform(s.k0);
-  s.ka = uniform(s.ka);
-  s.kn = uniform(s.kn);
   return s;
+}
+// The sequence that lane l holds, in scalar registers.
+__device__ __forceinline__ Sequence from_lane(const Sequence& s, int l) {
+  return Sequence{__builtin_amdgcn_readlane(s.q0, l), __builtin_amdgcn_readlane(s.qn, l),
+                  __builtin_amdgcn_readlane(s.k0, l), __builtin_amdgcn_readlane(s.ka, l),
+                  __builtin_amdgcn_readlane(s.kn, l)};
+}
+__device__ __forceinline__ Sequence load_sequence(const AttentionArgs& a, int b) {
+  return from_lane(lane_sequence(a, b), 0);
 }
 
 // Sum over the 64 lanes of a wave (data-parallel moves: row shifts, then two
@@ -113,11 +118,11 @@ __device__ __forceinline__ int wave_sum(int v) {
   return __builtin_amdgcn_readlane(v, 63);
 }
 
-// The t-th tile of all sequences, where a sequence of n rows (of the axis `cu`
-// describes) has ceil(n * mult / unit) of them: its sequence b, that
-// sequence's tile count and the tile's rank in it.  False past the last tile
-// (the grid is sized without knowing the lengths).  Each wave finds it by
-// itself.
+// The t-th tile of all sequences, where a sequence of n rows (of q, or of k
+// with KEYS) has ceil(n * mult / unit) of them: its sequence, that sequence's
+// tile count and the tile's rank in it.  False past the last tile (the grid is
+// sized without knowing the lengths).  Each wave finds it by itself, after one
+// round of loads: each lane loads all of a sequence.
 //
 // Up to 64 sequences, tiles come by descending rank, whatever their sequence:
 // with a causal mask a tile's rank is its work, and workgroups that start with
@@ -127,22 +132,14 @@ __device__ __forceinline__ int wave_sum(int v) {
 // have rank r or more, t falls into the largest r with G(r) > t, found by
 // bisection over a wave-wide sum.  More sequences than lanes come one after
 // another.
-__device__ __forceinline__ bool find_tile(const int32_t* cu, int batch, int total, int mult,
-                                          int unit, int t, int& b, int& rank, int& tiles) {
-  if (cu == nullptr) {
-    tiles = (total / batch * mult + unit - 1) / unit;
-    rank = tiles - 1 - t / batch;
-    b = t % batch;
-    return rank >= 0;
-  }
+template <bool KEYS>
+__device__ __forceinline__ bool find_tile(const AttentionArgs& a, int mult, int unit, int t,
+                                          Sequence& s, int& rank, int& tiles) {
   const int lane = threadIdx.x & 63;
-  if (batch <= 64) {
+  if (a.batch <= 64) {
+    const Sequence mine = lane_sequence(a, min(lane, a.batch - 1));
     int n = 0;
-    if (lane < batch) {
-      int start;
-      cu_range(cu, batch, total, lane, start, n);
-      n = (n * mult + unit - 1) / unit;
-    }
+    if (lane < a.batch) n = ((KEYS ? mine.ka : mine.qn) * mult + unit - 1) / unit;
     if (wave_sum(n) <= t) return false;
     int lo = 0, hi = 1;  // G(lo) > t; find hi with G(hi) <= t
     while (wave_sum(max(n - hi, 0)) > t) {
@@ -161,18 +158,16 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, int batch, int tota
         static_cast<uint32_t>(having >> 32),
         __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(having), 0));
     const uint64_t it = __ballot(n > lo && before == at);
-    b = uniform(__ffsll(static_cast<unsigned long long>(it)) - 1);
-    tiles = __builtin_amdgcn_readlane(n, b);
+    const int l = uniform(__ffsll(static_cast<unsigned long long>(it)) - 1);
+    tiles = __builtin_amdgcn_readlane(n, l);
+    s = from_lane(mine, l);
     return true;
   }
   int base = 0;
-  for (int b0 = 0; b0 < batch; b0 += 64) {
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    const Sequence mine = lane_sequence(a, min(b0 + lane, a.batch - 1));
     int n = 0;
-    if (b0 + lane < batch) {
-      int start;
-      cu_range(cu, batch, total, b0 + lane, start, n);
-      n = (n * mult + unit - 1) / unit;
-    }
+    if (b0 + lane < a.batch) n = ((KEYS ? mine.ka : mine.qn) * mult + unit - 1) / unit;
     int sum = n;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -184,7 +179,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, int batch, int tota
       const int l = uniform(__ffsll(static_cast<unsigned long long>(past)) - 1);
       tiles = __builtin_amdgcn_readlane(n, l);
       rank = __builtin_amdgcn_readlane(sum, l) - 1 - (t - base);
-      b = b0 + l;
+      s = from_lane(mine, l);
       return true;
     }
     base += __builtin_amdgcn_readlane(sum, 63);
@@ -349,19 +344,29 @@ __device__ __forceinline__ float pair_sum(float v) {
 }
 
 // Store acc (columns: this lane's row of a tensor; rows: head dims) times mul
-// as bf16 to `dst`, head dims below `dim` only.
+// as bf16 to `dst`, head dims below `dim` only.  Lanes l and l + 32 hold 4 and
+// 4 of 8 neighbouring dims of one row; of two such runs each takes one whole,
+// so that every store is 16 bytes.
 template <int DP>
 __device__ __forceinline__ void store_row(uint16_t* dst, const f32x16 (&acc)[DP / 32], float mul,
                                           int dim, int lane) {
 #pragma unroll
   for (int ct = 0; ct < DP / 32; ++ct)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = ct * 32 + 8 * i + 4 * (lane >> 5);
-      u32x2 w;
-      w.x = pack_bf16x2(acc[ct][4 * i] * mul, acc[ct][4 * i + 1] * mul);
-      w.y = pack_bf16x2(acc[ct][4 * i + 2] * mul, acc[ct][4 * i + 3] * mul);
-      if (d < dim) *reinterpret_cast<u32x2*>(dst + d) = w;
+    for (int i = 0; i < 4; i += 2) {
+      uint32_t w[2][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          w[k][e] = pack_bf16x2(acc[ct][4 * (i + k) + 2 * e] * mul,
+                                acc[ct][4 * (i + k) + 2 * e + 1] * mul);
+      const u32x2 x = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false));
+      const u32x2 y = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false));
+      const int d = ct * 32 + 8 * (i + (lane >> 5));
+      if (d < dim) *reinterpret_cast<u32x4*>(dst + d) = u32x4{x.x, y.x, x.y, y.y};
     }
 }
 

@@ -24,6 +24,7 @@ using namespace attn;
 constexpr int kWaves = 8;
 constexpr int kRows = 32 * kWaves;  // rows of a workgroup
 constexpr int kKeys = 64;           // keys of a tile
+constexpr int kStages = 3;          // tiles in LDS: one being read, two under way
 
 // The rows are scaled back to the running maximum only when it has grown by
 // more than this many powers of two: probabilities stay below 2^8 (float32
@@ -32,16 +33,14 @@ constexpr int kKeys = 64;           // keys of a tile
 constexpr float kSlack = 8.0f;
 
 template <int DP>
-__global__ __launch_bounds__(512, 2) void attention_forward_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(AttentionArgs a) {
   typedef Tile<DP, kKeys, kWaves> KTile;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][KTile::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages][2][KTile::kBytes];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int g = blockIdx.x % a.kv_heads;
-  int b, rank, tiles;
-  if (!find_tile(a.cu_q, a.batch, a.total_q, a.group, kRows, blockIdx.x / a.kv_heads, b, rank,
-                 tiles))
-    return;
-  const Sequence s = load_sequence(a, b);
+  Sequence s;
+  int rank, tiles;
+  if (!find_tile<false>(a, a.group, kRows, blockIdx.x / a.kv_heads, s, rank, tiles)) return;
   const int row0 = rank * kRows;  // the last rows see the most keys
   const int rows = s.qn * a.group;
   const int r = row0 + wave * 32 + (lane & 31);
@@ -57,37 +56,46 @@ __global__ __launch_bounds__(512, 2) void attention_forward_kernel(AttentionArgs
       wave_first < rows ? min((min(wave_first + 32, rows) - 1) / a.group + shift, s.kn - 1) : -1;
   const int wave_free = min(wave_first / a.group + shift, s.kn - 1);  // seen by every row
 
+  KTile kt, vt;
+  kt.init(wave, lane, a.k.row, a.head_dim);
+  vt.init(wave, lane, a.v.row, a.head_dim);
+  Walk kw(a.k, s.k0, g, a.head_dim), vw(a.v, s.k0, g, a.head_dim);
+  int left = s.kn, ahead = 0;  // keys from the walks' place on; stage of the next copies
+  auto copy_tile = [&]() {     // tiles in their order; past the end zeros, counted as the others
+    const int n = min(left, kKeys);
+    kt.copy(lds[ahead][0], wave, kw.rows(n));
+    vt.copy(lds[ahead][1], wave, vw.rows(n));
+    kw.step(kKeys);
+    vw.step(kKeys);
+    left -= kKeys;
+    ahead = ahead == kStages - 1 ? 0 : ahead + 1;
+  };
+  const int nj = block_lim < 0 ? 0 : block_lim / kKeys + 1;
+  if (nj > 0) {
+#pragma unroll
+    for (int n = 0; n < kStages - 1; ++n) copy_tile();
+  }
   const uint16_t* qrow = a.q.p + (int64_t)(s.q0 + i) * a.q.row + h * a.q.head;
   bf16x8 q[DP / 16];
 #pragma unroll
   for (int ks = 0; ks < DP / 16; ++ks)
     q[ks] = load8(qrow, ks * 16 + 8 * (lane >> 5), a.head_dim, valid);
 
-  KTile kt, vt;
-  kt.init(wave, lane, a.k.row, a.head_dim);
-  vt.init(wave, lane, a.v.row, a.head_dim);
-  Walk kw(a.k, s.k0, g, a.head_dim), vw(a.v, s.k0, g, a.head_dim);
-  auto copy_tile = [&](int j) {  // tiles in their order
-    const int n = min(s.kn - j * kKeys, kKeys);
-    kt.copy(lds[j & 1][0], wave, kw.rows(n));
-    vt.copy(lds[j & 1][1], wave, vw.rows(n));
-    kw.step(kKeys);
-    vw.step(kKeys);
-  };
+  wait_copies<0>();  // and the loads of q
 
   f32x16 o[DP / 32];
 #pragma unroll
   for (int ct = 0; ct < DP / 32; ++ct) o[ct] = f32x16{};
   float m = -INFINITY, l[2] = {0.0f, 0.0f};  // l: sums of even and odd values
-  const int nj = block_lim < 0 ? 0 : block_lim / kKeys + 1;
-  if (nj > 0) copy_tile(0);
+  int stage = 0;
   for (int j = 0; j < nj; ++j) {
-    wait_copies<0>();
+    wait_copies<2 * (kStages - 2) * KTile::kCopies>();  // later tiles' may still be under way
     __syncthreads();
-    if (j + 1 < nj) copy_tile(j + 1);
+    copy_tile();
+    const uint8_t* K = lds[stage][0];
+    const uint8_t* V = lds[stage][1];
+    stage = stage == kStages - 1 ? 0 : stage + 1;
     if (j * kKeys > wave_lim) continue;
-    const uint8_t* K = lds[j & 1][0];
-    const uint8_t* V = lds[j & 1][1];
     constexpr int kDims = DP / 32;    // 32-column panels
     constexpr int kSteps = DP / 16;   // products of one S^T square
     // S^T: the K rows of 8 products are in flight ahead of the products, and
@@ -161,6 +169,7 @@ __global__ __launch_bounds__(512, 2) void attention_forward_kernel(AttentionArgs
       __builtin_amdgcn_sched_group_barrier(kSchedValu, 28 / kDims, 1);
     }
   }
+  wait_copies<0>();  // no copy may land after the workgroup has given up its LDS
   const float sum = pair_sum(l[0] + l[1]);
   if (!valid) return;
   uint16_t* orow = a.o.p + (int64_t)(s.q0 + i) * a.o.row + h * a.o.head;
@@ -503,8 +512,8 @@ bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
   if (blocks == 0) return BFP8_OK;
   if (blocks >= (int64_t(1) << 31)) return BFP8_ERR_SHAPE;
   const dim3 grid(static_cast<unsigned>(blocks));
-  if (a.head_dim <= 64) return launch(attention_forward_kernel<64>, grid, dim3(512), stream, a);
-  return launch(attention_forward_kernel<128>, grid, dim3(512), stream, a);
+  if (a.head_dim <= 64) return launch(attention_forward_kernel<64>, grid, dim3(64 * kWaves), stream, a);
+  return launch(attention_forward_kernel<128>, grid, dim3(64 * kWaves), stream, a);
 }
 
 }  // namespace bfp8

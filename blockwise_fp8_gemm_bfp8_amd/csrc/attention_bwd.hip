@@ -21,21 +21,49 @@ using namespace attn;
 constexpr int kWaves = 8;
 constexpr int kRows = 32 * kWaves;
 constexpr int kKeys = 64;     // keys of a dq tile
+constexpr int kStages = 3;    // tiles in LDS: one being read, two under way
 constexpr int kKeyWaves = 4;  // waves over the keys of a dkdv workgroup; two halves of them
 constexpr int kKeyRows = 32 * kKeyWaves;
 static_assert(kWaves == 2 * kKeyWaves, "two halves");
 
+// lse2 and -delta of every row of every head, for the kernel below: 16 lanes a
+// row, 8 values a lane.  Memory-bound: O and dO once.
+__global__ __launch_bounds__(256) void attention_stats_kernel(AttentionArgs a) {
+  const int64_t at = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;  // row, then head
+  const int d = threadIdx.x % 16 * 8;
+  const int64_t t = at / a.heads;
+  const int h = static_cast<int>(at - t * a.heads);
+  if (t >= a.total_q) return;
+  const bf16x8 o = load8(a.o.p + t * a.o.row + h * a.o.head, d, a.head_dim, true);
+  const bf16x8 dout = load8(a.dout.p + t * a.dout.row + h * a.dout.head, d, a.head_dim, true);
+  float sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    sum = fmaf(static_cast<float>(dout[e]), static_cast<float>(o[e]), sum);
+#pragma unroll
+  for (int x = 1; x < 16; x *= 2) sum += __shfl_xor(sum, x);
+  if (d == 0) {
+    const int64_t row = h * (int64_t)a.total_q + t;
+    const float lse = a.lse[row];
+    a.lse2[row] = lse == -INFINITY ? 0.0f : lse * kLog2e;
+    a.delta[row] = -sum;
+  }
+}
+
 template <int DP>
-__global__ __launch_bounds__(512, 2) void attention_dq_kernel(AttentionArgs a) {
+struct DqShared {
+  uint8_t tiles[kStages][2][Tile<DP, kKeys, kWaves>::kBytes];  // K and V rows
+};
+
+template <int DP>
+__device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& shared, int n,
+                                        int g) {
   typedef Tile<DP, kKeys, kWaves> KTile;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][KTile::kBytes];
+  auto& lds = shared.tiles;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int g = blockIdx.x % a.kv_heads;
-  int b, rank, tiles;
-  if (!find_tile(a.cu_q, a.batch, a.total_q, a.group, kRows, blockIdx.x / a.kv_heads, b, rank,
-                 tiles))
-    return;
-  const Sequence s = load_sequence(a, b);
+  Sequence s;
+  int rank, tiles;
+  if (!find_tile<false>(a, a.group, kRows, n, s, rank, tiles)) return;
   const int row0 = rank * kRows;
   const int rows = s.qn * a.group;
   const int r = row0 + wave * 32 + (lane & 31);
@@ -50,57 +78,54 @@ __global__ __launch_bounds__(512, 2) void attention_dq_kernel(AttentionArgs a) {
       wave_first < rows ? min((min(wave_first + 32, rows) - 1) / a.group + shift, s.kn - 1) : -1;
   const int wave_free = min(wave_first / a.group + shift, s.kn - 1);
 
+  KTile kt, vt;
+  kt.init(wave, lane, a.k.row, a.head_dim);
+  vt.init(wave, lane, a.v.row, a.head_dim);
+  Walk kw(a.k, s.k0, g, a.head_dim), vw(a.v, s.k0, g, a.head_dim);
+  int left = s.kn, ahead = 0;  // keys from the walks' place on; stage of the next copies
+  auto copy_tile = [&]() {     // tiles in their order; past the end zeros, counted as the others
+    const int n = min(left, kKeys);
+    kt.copy(lds[ahead][0], wave, kw.rows(n));
+    vt.copy(lds[ahead][1], wave, vw.rows(n));
+    kw.step(kKeys);
+    vw.step(kKeys);
+    left -= kKeys;
+    ahead = ahead == kStages - 1 ? 0 : ahead + 1;
+  };
+  const int nj = block_lim < 0 ? 0 : block_lim / kKeys + 1;
+  if (nj > 0) {
+#pragma unroll
+    for (int n = 0; n < kStages - 1; ++n) copy_tile();
+  }
   const int64_t t = s.q0 + i;
   const uint16_t* qrow = a.q.p + t * a.q.row + h * a.q.head;
   const uint16_t* drow = a.dout.p + t * a.dout.row + h * a.dout.head;
-  const uint16_t* orow = a.o.p + t * a.o.row + h * a.o.head;
   bf16x8 q[DP / 16], d[DP / 16];
-  float delta = 0.0f;
 #pragma unroll
   for (int ks = 0; ks < DP / 16; ++ks) {
     const int c = ks * 16 + 8 * (lane >> 5);
     q[ks] = load8(qrow, c, a.head_dim, valid);
     d[ks] = load8(drow, c, a.head_dim, valid);
-    const bf16x8 o = load8(orow, c, a.head_dim, valid);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      delta = fmaf(static_cast<float>(d[ks][e]), static_cast<float>(o[e]), delta);
   }
-  delta = pair_sum(delta);
-  float lse2 = 0.0f;
+  float lse2 = 0.0f, delta = 0.0f;
   if (valid) {
-    const float lse = a.lse[(int64_t)h * a.total_q + t];
-    lse2 = lse == -INFINITY ? 0.0f : lse * kLog2e;
-    if (lane < 32) {  // for the dkdv kernel
-      a.lse2[(int64_t)h * a.total_q + t] = lse2;
-      a.delta[(int64_t)h * a.total_q + t] = -delta;
-    }
+    lse2 = a.lse2[(int64_t)h * a.total_q + t];
+    delta = -a.delta[(int64_t)h * a.total_q + t];
   }
-
-  KTile kt, vt;
-  kt.init(wave, lane, a.k.row, a.head_dim);
-  vt.init(wave, lane, a.v.row, a.head_dim);
-  Walk kw(a.k, s.k0, g, a.head_dim), vw(a.v, s.k0, g, a.head_dim);
-  auto copy_tile = [&](int j) {  // tiles in their order
-    const int n = min(s.kn - j * kKeys, kKeys);
-    kt.copy(lds[j & 1][0], wave, kw.rows(n));
-    vt.copy(lds[j & 1][1], wave, vw.rows(n));
-    kw.step(kKeys);
-    vw.step(kKeys);
-  };
+  wait_copies<0>();  // and the loads above
 
   f32x16 acc[DP / 32];
 #pragma unroll
   for (int ct = 0; ct < DP / 32; ++ct) acc[ct] = f32x16{};
-  const int nj = block_lim < 0 ? 0 : block_lim / kKeys + 1;
-  if (nj > 0) copy_tile(0);
+  int stage = 0;
   for (int j = 0; j < nj; ++j) {
-    wait_copies<0>();
+    wait_copies<2 * (kStages - 2) * KTile::kCopies>();  // later tiles' may still be under way
     __syncthreads();
-    if (j + 1 < nj) copy_tile(j + 1);
+    copy_tile();
+    const uint8_t* K = lds[stage][0];
+    const uint8_t* V = lds[stage][1];
+    stage = stage == kStages - 1 ? 0 : stage + 1;
     if (j * kKeys > wave_lim) continue;
-    const uint8_t* K = lds[j & 1][0];
-    const uint8_t* V = lds[j & 1][1];
     constexpr int kDims = DP / 32;   // 32-column panels
     constexpr int kSteps = DP / 16;  // products of one 32x32 square
     bf16x8 kf[kSteps], vf[kSteps], kc[2][kDims];
@@ -162,27 +187,35 @@ __global__ __launch_bounds__(512, 2) void attention_dq_kernel(AttentionArgs a) {
       }
     }
   }
+  wait_copies<0>();  // no copy may land after the workgroup has given up its LDS
   if (!valid) return;
   store_row<DP>(a.dq.p + t * a.dq.row + h * a.dq.head, acc, a.scale, a.head_dim, lane);
 }
 
 template <int DP>
-__global__ __launch_bounds__(512, 2) void attention_dkdv_kernel(AttentionArgs a) {
+struct DkdvShared {
   typedef Tile<DP, 32, kKeyWaves> QTile;
   typedef Tile<DP, kKeyRows, kWaves> VTile;
+  uint8_t tiles[kStages][2][2][QTile::kBytes];  // of each half: Q rows, dO rows
+  uint8_t v[VTile::kBytes];                     // the workgroup's V rows
+  float stats[kStages][2][2][64];               // of each half: lse2, -delta
+};
+
+template <int DP>
+__device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>& shared, int n0,
+                                          int g) {
+  typedef typename DkdvShared<DP>::QTile QTile;
+  typedef typename DkdvShared<DP>::VTile VTile;
   constexpr int kDims = DP / 32;   // 32-column panels
   constexpr int kSteps = DP / 16;  // products of one 32x32 square
-  // two stages of each half's Q rows, dO rows and their lse2 and -delta; the V rows
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][2][QTile::kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t vlds[VTile::kBytes];
-  __shared__ __attribute__((aligned(256))) float stats[2][2][2][64];
+  auto& lds = shared.tiles;
+  auto& vlds = shared.v;
+  auto& stats = shared.stats;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int half = wave / kKeyWaves, kw = wave % kKeyWaves;
-  const int g = blockIdx.x % a.kv_heads;
-  int b, rank, tiles;
-  if (!find_tile(a.cu_k, a.batch, a.total_k, 1, kKeyRows, blockIdx.x / a.kv_heads, b, rank, tiles))
-    return;
-  const Sequence s = load_sequence(a, b);
+  Sequence s;
+  int rank, tiles;
+  if (!find_tile<true>(a, 1, kKeyRows, n0, s, rank, tiles)) return;
   const int row0 = (tiles - 1 - rank) * kKeyRows;  // the first keys are seen by the most queries
   const int key0 = row0 + kw * 32;                 // the wave's first key
   const int key = key0 + (lane & 31);
@@ -233,31 +266,41 @@ __global__ __launch_bounds__(512, 2) void attention_dkdv_kernel(AttentionArgs a)
   };
   if (half == 1 && total > 0) pass(1);
   int copied = half;
-  auto copy_square = [&](int stage) {
+  int ahead = 0;  // stage of the next copies
+  auto copy_square = [&]() {  // past the last: zeros, counted as the others
     const int rows = copied < total ? min(left, 32) : 0;
-    qt.copy(lds[stage][half][0], kw, qw.rows(rows));
-    dt.copy(lds[stage][half][1], kw, dw.rows(rows));
+    qt.copy(lds[ahead][half][0], kw, qw.rows(rows));
+    dt.copy(lds[ahead][half][1], kw, dw.rows(rows));
     if (kw < 2)
-      copy4(uniform(lds_offset(&stats[stage][half][kw][0])), lane * 4, buffer(stat_at, rows * 4));
+      copy4(uniform(lds_offset(&stats[ahead][half][kw][0])), lane * 4, buffer(stat_at, rows * 4));
+    ahead = ahead == kStages - 1 ? 0 : ahead + 1;
     copied += 2;  // the halves take squares in turn
     pass(2);
   };
-  if (total > 0) copy_square(0);
+  if (total > 0) {
+    copy_square();
+    copy_square();
+  }
   const uint16_t* kp = a.k.p + krow * a.k.row + g * a.k.head;
   bf16x8 k[kSteps];
 #pragma unroll
   for (int ks = 0; ks < kSteps; ++ks)
     k[ks] = load8(kp, ks * 16 + 8 * (lane >> 5), a.head_dim, used);
+  wait_copies<0>();  // and the loads of k
 
   f32x16 dk[kDims], dv[kDims];
 #pragma unroll
   for (int ct = 0; ct < kDims; ++ct) dk[ct] = dv[ct] = f32x16{};
   int at = per_head == 1 ? 0 : half;  // this half's square of its head
+  int next = 0;
   for (int n = 0; n < total; n += 2) {
-    const int stage = (n >> 1) & 1;
-    wait_copies<0>();
+    // the next square's copies may still be under way
+    if (kw < 2) wait_copies<2 * QTile::kCopies + 1>();
+    else wait_copies<2 * QTile::kCopies>();
     __syncthreads();
-    if (n + 2 < total) copy_square(stage ^ 1);
+    copy_square();
+    const int stage = next;
+    next = next == kStages - 1 ? 0 : next + 1;
     const int i0 = first + at * 32;
     at += 2;
     if (at >= per_head) at -= per_head;
@@ -350,16 +393,25 @@ __global__ __launch_bounds__(512, 2) void attention_dkdv_kernel(AttentionArgs a)
     store_row<DP>(a.dk.p + krow * a.dk.row + g * a.dk.head, dk, a.scale, a.head_dim, lane);
 }
 
+// Both kinds of tiles in one launch, so that neither waits for the other's
+// last workgroups: of every total places, q_tiles are dq tiles, evenly spread
+// (each kind's come by descending work).  The kv head changes fastest, which
+// puts all tiles of a head on one XCD where the heads are a multiple of 8.
 template <int DP>
-bfp8_status launch_backward(const AttentionArgs& a, int64_t q_blocks, int64_t k_blocks,
-                            hipStream_t stream) {
-  bfp8_status st = BFP8_OK;
-  if (q_blocks > 0)
-    st = launch(attention_dq_kernel<DP>, dim3(static_cast<unsigned>(q_blocks)), dim3(512), stream, a);
-  if (st == BFP8_OK && k_blocks > 0)
-    st = launch(attention_dkdv_kernel<DP>, dim3(static_cast<unsigned>(k_blocks)), dim3(512), stream,
-                a);
-  return st;
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_backward_kernel(AttentionArgs a,
+                                                                           unsigned q_tiles,
+                                                                           unsigned total) {
+  union Shared {
+    DqShared<DP> dq;
+    DkdvShared<DP> dkdv;
+  };
+  __shared__ __attribute__((aligned(1024))) Shared shared;
+  const int g = blockIdx.x % a.kv_heads;
+  const unsigned place = blockIdx.x / a.kv_heads;
+  if (place < total - q_tiles)
+    dkdv_tile<DP>(a, shared.dkdv, place, g);
+  else
+    dq_tile<DP>(a, shared.dq, place - (total - q_tiles), g);
 }
 
 // An upper bound on the tiles of all sequences, whose lengths are on the device.
@@ -371,11 +423,22 @@ int64_t tile_bound(const int32_t* cu, int64_t batch, int64_t total, int64_t mult
 }  // namespace
 
 bfp8_status launch_attention_backward(const AttentionArgs& a, hipStream_t stream) {
-  const int64_t q_blocks = tile_bound(a.cu_q, a.batch, a.total_q, a.group, kRows) * a.kv_heads;
-  const int64_t k_blocks = tile_bound(a.cu_k, a.batch, a.total_k, 1, kKeyRows) * a.kv_heads;
-  if (q_blocks >= (int64_t(1) << 31) || k_blocks >= (int64_t(1) << 31)) return BFP8_ERR_SHAPE;
-  return a.head_dim <= 64 ? launch_backward<64>(a, q_blocks, k_blocks, stream)
-                          : launch_backward<128>(a, q_blocks, k_blocks, stream);
+  const int64_t q_tiles = tile_bound(a.cu_q, a.batch, a.total_q, a.group, kRows);
+  const int64_t total = q_tiles + tile_bound(a.cu_k, a.batch, a.total_k, 1, kKeyRows);
+  const int64_t blocks = total * a.kv_heads;
+  const int64_t stat_blocks = ((int64_t)a.total_q * a.heads + 15) / 16;
+  if (blocks >= (int64_t(1) << 31) || stat_blocks >= (int64_t(1) << 31)) return BFP8_ERR_SHAPE;
+  if (stat_blocks > 0) {
+    const bfp8_status st = launch(attention_stats_kernel, dim3(static_cast<unsigned>(stat_blocks)),
+                                  dim3(256), stream, a);
+    if (st != BFP8_OK) return st;
+  }
+  if (blocks == 0) return BFP8_OK;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  return a.head_dim <= 64
+             ? launch(attention_backward_kernel<64>, grid, dim3(64 * kWaves), stream, a, q_tiles, total)
+             : launch(attention_backward_kernel<128>, grid, dim3(64 * kWaves), stream, a, q_tiles,
+                      total);
 }
 
 }  // namespace bfp8
