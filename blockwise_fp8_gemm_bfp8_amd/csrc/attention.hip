@@ -14,6 +14,8 @@
 // (query, head of the group) pair: the heads that share keys share their
 // tiles, and few queries fill more of a tile.  Each wave owns 32 rows; tiles
 // of 64 keys pass through two LDS stages, filled by LDS-DMA one tile ahead.
+#include <algorithm>
+
 #include "attention.h"
 
 namespace bfp8 {
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
 // Where a stretch ends inside a segment (one kv head's 32 rows), its float32
 // results go to the workspace, and a second kernel joins a segment's parts in
 // their order.
-constexpr int kStreams = 1280;  // as many 32 KiB workgroups as 256 CUs of 160 KiB hold
+constexpr int kStreams = 1024;  // one on each SIMD (its registers leave no room for two)
 constexpr int kMinShare = 3;    // line units of a stretch at least
 // A segment counts for so many tiles more than it has, for the latency of its
 // first loads; they come first.
@@ -205,20 +207,17 @@ struct Parts {
 
 // A place on the line of tiles.
 struct Place {
-  int b;         // sequence
-  int segment;   // in it: kv head, then 32 rows
-  int unit;      // in the segment: kSegmentCost, then its key tiles
+  Sequence s;
+  int b;                // its index
+  int segment;          // in it: kv head, then 32 rows
+  int unit;             // in the segment: kSegmentCost, then its key tiles
   int units, segments;  // of the sequence's segments
 };
 
-__device__ __forceinline__ void line_units(const AttentionArgs& a, int b, int& units,
+__device__ __forceinline__ void line_units(const AttentionArgs& a, const Sequence& s, int& units,
                                            int& segments) {
-  int q0, qn, k0, kn;
-  cu_range(a.cu_q, a.batch, a.total_q, b, q0, qn);
-  cu_range(a.cu_k, a.batch, a.total_k, b, k0, kn);
-  if (a.k_lens != nullptr) kn = clampi(a.k_lens[b], 0, kn);
-  units = kSegmentCost + max((kn + 31) / 32, 1);  // rows without keys have a result, too
-  segments = (qn * a.group + 31) / 32 * a.kv_heads;
+  units = kSegmentCost + max((s.kn + 31) / 32, 1);  // rows without keys have a result, too
+  segments = (s.qn * a.group + 31) / 32 * a.kv_heads;
 }
 
 // Length of the line and the place of unit number `share(length)` * n; false
@@ -228,20 +227,22 @@ __device__ __forceinline__ bool find_place(const AttentionArgs& a, int n, Share 
                                            int& at, Place& p) {
   const int lane = threadIdx.x & 63;
   length = 0;
+  Sequence mine;
   int units = 0, segments = 0;
+  auto load = [&](int b0) {
+    mine = lane_sequence(a, min(b0 + lane, a.batch - 1));
+    line_units(a, mine, units, segments);
+    if (b0 + lane >= a.batch) segments = 0;
+  };
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    units = segments = 0;
-    if (b0 + lane < a.batch) line_units(a, b0 + lane, units, segments);
+    load(b0);
     length += wave_sum(units * segments);
   }
   at = n * share(length);
   if (at >= length) return false;
   int base = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    if (a.batch > 64) {
-      units = segments = 0;
-      if (b0 + lane < a.batch) line_units(a, b0 + lane, units, segments);
-    }
+    if (a.batch > 64) load(b0);
     int sum = units * segments;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -251,6 +252,7 @@ __device__ __forceinline__ bool find_place(const AttentionArgs& a, int n, Share 
     const uint64_t past = __ballot(at < base + sum);
     if (past != 0) {
       const int l = uniform(__ffsll(static_cast<unsigned long long>(past)) - 1);
+      p.s = from_lane(mine, l);
       p.b = b0 + l;
       p.units = __builtin_amdgcn_readlane(units, l);
       p.segments = __builtin_amdgcn_readlane(segments, l);
@@ -282,8 +284,8 @@ __global__ __launch_bounds__(64, 1) void attention_stream_kernel(AttentionArgs a
   KTile kt, vt;
   kt.init(0, lane, a.k.row, a.head_dim);
   vt.init(0, lane, a.v.row, a.head_dim);
-  Sequence s = load_sequence(a, p.b);
   while (true) {
+    const Sequence s = p.s;
     const int end = min(p.unit + remaining, p.units);
     remaining -= end - p.unit;
     const int t0 = max(p.unit - kSegmentCost, 0), t1 = max(end - kSegmentCost, 0);
@@ -394,23 +396,21 @@ __global__ __launch_bounds__(64, 1) void attention_stream_kernel(AttentionArgs a
     if (++p.segment == p.segments) {  // on to the next sequence that has rows
       p.segment = 0;
       do {
-        ++p.b;  // there is one: units remain
-        line_units(a, p.b, p.units, p.segments);
-        p.units = uniform(p.units);
-        p.segments = uniform(p.segments);
+        p.s = load_sequence(a, ++p.b);  // there is one: units remain
+        line_units(a, p.s, p.units, p.segments);
       } while (p.segments == 0);
-      s = load_sequence(a, p.b);
     }
   }
 }
 
 // Joins the parts of one segment in their order.  Workgroup n looks at the
 // boundary between stretches n and n + 1: where it lies among the tiles of a
-// segment and is the first that does, it joins that segment.  8 rows at a
+// segment and is the first that does, it joins that segment.  16 rows at a
 // time; where there are fewer, several groups of threads share a row's parts.
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Parts parts) {
-  __shared__ f32x4 other_o[256];
-  __shared__ float2 other_ml[256];
+constexpr int kJoinThreads = 512;
+__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionArgs a, Parts parts) {
+  __shared__ f32x4 other_o[kJoinThreads];
+  __shared__ float2 other_ml[kJoinThreads];
   int length, at;
   Place p;
   const int n = blockIdx.x;
@@ -420,13 +420,13 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
   const int first_tile = at - p.unit + kSegmentCost;  // on the line
   if (p.unit <= kSegmentCost || first_tile / share != n) return;
   const int last = (at - p.unit + p.units - 1) / share;  // stretch in which the segment ends
-  const Sequence s = load_sequence(a, p.b);
+  const Sequence s = p.s;
   const int row_tiles = p.segments / a.kv_heads;
   const int g = p.segment / row_tiles;
   const int row0 = (p.segment - g * row_tiles) * 32;
   const int rows = min(s.qn * a.group - row0, 32);
   const int per_row = a.head_dim / 4;
-  const int slots = 256 / per_row;            // at least 8
+  const int slots = kJoinThreads / per_row;   // at least 16
   const int shared = max(slots / rows, 1);    // slots of one row
   const int at_once = slots / shared;         // rows
   const int slot = threadIdx.x / per_row;
@@ -446,7 +446,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
       o = o * keep + v * mul;
     };
     if (sub < shared && r < rows) {
-#pragma unroll 4
+#pragma unroll 8
       for (int w = n + sub; w <= last; w += shared) {
         const int64_t part = (2 * w + (w == n ? 1 : 0)) * 32 + r;
         add(parts.ml[part], *reinterpret_cast<const f32x4*>(parts.o + part * a.head_dim + d));
@@ -473,25 +473,37 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pa
   }
 }
 
-// Few rows: the heads of a group give no more than one 32-row operand a
-// sequence on average.  (The line's units are counted in 32 bits.)
-bool few_rows(const AttentionArgs& a) {
-  const int64_t row_tiles = (int64_t)a.total_q * a.group / 32 + a.batch;
-  const int64_t key_tiles = (int64_t)a.total_k / 32 + (1 + kSegmentCost) * a.batch;
-  return a.total_q > 0 && (int64_t)a.total_q * a.group <= (int64_t)32 * a.batch &&
-         row_tiles * key_tiles * a.kv_heads < (int64_t(1) << 31);
+// Whether the keys are streamed.  The other kernel's time is its longest
+// workgroup's, about 1 us for 64 keys whatever its rows, until its workgroups
+// fill the CUs; this one's is all 32 x 32 squares over 1024 waves, and the
+// join.  So it pays while few rows (R, 32-row tiles over all kv heads) meet
+// many keys (K, tiles of an average sequence's room).  Measured with heads of
+// 128 in us, the other kernel / this one: R 8: K 16 12 / 15, K 32 19 / 14, K
+// 128 62 / 17; R 64: K 64 35 / 34, K 128 92 / 43; R 128: K 32 21 / 26, K 128
+// 64 / 55; R 256: K 64 47 / 55, K 128 93 / 97, K 512 350 / 298; R 512: K 128
+// 94 / 153.
+bool streams_keys(const AttentionArgs& a) {
+  if (a.total_q == 0) return false;
+  const int64_t row_tiles =
+      std::max<int64_t>(a.batch, ((int64_t)a.total_q * a.group + 31) / 32) * a.kv_heads;
+  const int64_t key_tiles = (int64_t)a.total_k / a.batch / 32;
+  // the line's units, counted in 32 bits: any split of total_q over the sequences
+  const int64_t most_rows = (int64_t)a.total_q * a.group / 32 + a.batch;
+  const int64_t most_keys = (int64_t)a.total_k / 32 + (1 + kSegmentCost) * a.batch;
+  return key_tiles >= 32 && row_tiles <= std::min<int64_t>(key_tiles, 256) &&
+         most_rows * a.kv_heads * most_keys < (int64_t(1) << 31);
 }
 
 }  // namespace
 
 size_t attention_forward_workspace(const AttentionArgs& a) {
-  if (!few_rows(a)) return 0;
+  if (!streams_keys(a)) return 0;
   return static_cast<size_t>(2 * kStreams) * 32 * (a.head_dim + 2) * sizeof(float);
 }
 
 bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
                                      size_t workspace_bytes, hipStream_t stream) {
-  if (few_rows(a) && workspace != nullptr && workspace_bytes >= attention_forward_workspace(a)) {
+  if (streams_keys(a) && workspace != nullptr && workspace_bytes >= attention_forward_workspace(a)) {
     Parts parts;
     parts.o = static_cast<float*>(workspace);
     parts.ml = reinterpret_cast<float2*>(parts.o + 2 * kStreams * 32 * a.head_dim);
@@ -500,7 +512,7 @@ bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
             ? launch(attention_stream_kernel<64>, dim3(kStreams), dim3(64), stream, a, parts)
             : launch(attention_stream_kernel<128>, dim3(kStreams), dim3(64), stream, a, parts);
     if (st != BFP8_OK) return st;
-    return launch(attention_join_kernel, dim3(kStreams - 1), dim3(256), stream, a, parts);
+    return launch(attention_join_kernel, dim3(kStreams - 1), dim3(kJoinThreads), stream, a, parts);
   }
   // an upper bound on the tiles of all sequences: the lengths are on the device
   int64_t tiles;
