@@ -54,7 +54,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -248,13 +247,19 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 
 // LDS tiles hold DP columns (64 or 128) of bf16 as panels of 32 columns, each
 // panel ROWS rows of 64 bytes.  The four 16-byte chunks of a panel's row r are
-// permuted: chunk c lies at c ^ (r / 4 % 4).  The same tile is read along rows
-// (16 bytes of 32 consecutive rows: 16 rows of one chunk spread over all of
-// the LDS's 256 bytes) and down columns (8 bytes of 4 rows each, transposed by
-// the read itself: 8 whole rows, 512 bytes in a piece), both without bank
-// conflicts, and every operand of a tile is a constant offset from one of two
-// addresses per kind of read.
-__device__ __forceinline__ int swizzle(int r) { return (r >> 2) & 3; }
+// permuted: chunk c lies at c ^ swizzle(r).  The same tile is read along rows
+// (16 bytes of 16 rows from each quarter of the lanes) and down columns (8
+// bytes of 4 rows each, transposed by the read itself), both without bank
+// conflicts, and every operand of a tile is a constant offset from one address
+// (rows) or two (columns).  The LDS serves 16-byte reads 16 lanes at a time,
+// lanes 0-3, 12-15, 20-23 and 24-27 together, and 8-byte reads 32 lanes at a
+// time; 4 rows cover its 256 bytes, so the permutations of the 4-row groups
+// (0, 2, 3, 1) are such that these lanes meet four different chunks of either
+// kind.  (With 0, 2, 1, 3 a third of the LDS's time went to conflicts.)
+__device__ __forceinline__ int swizzle(int r) {
+  const int b0 = (r >> 2) & 1, b1 = (r >> 3) & 1;
+  return (b0 ^ b1) * 2 + b1;
+}
 
 // A tile of ROWS rows: its LDS bytes and the copies that fill it by WAVES
 // waves, 16 rows of a panel a copy.
@@ -282,92 +287,93 @@ struct Tile {
     for (int i = 0; i < kCopies; ++i) copy16(base + i * 1024, off[i], rsrc);
   }
 
-  // First operand of the 32x32x16 product from rows of a tile: lane l gives
-  // row r0 + l % 32, values 16 ks + 8 (l / 32) .. + 7.
+  // First operand of the 16x16x32 product from rows of a tile: lane l gives
+  // row r0 + l % 16, values 32 ks + 8 (l / 16) .. + 7.  r0 % 16 == 0.
   static __device__ __forceinline__ bf16x8 rows(const uint8_t* tile, int r0, int ks, int lane) {
-    const int r = lane & 31;
-    const int c = (2 * (ks & 1) + (lane >> 5)) ^ swizzle(r);
-    return *reinterpret_cast<const bf16x8*>(tile + (ks >> 1) * kPanel + r0 * 64 + (r * 64 + c * 16));
+    const int r = lane & 15;
+    const int c = (lane >> 4) ^ swizzle(r);
+    return *reinterpret_cast<const bf16x8*>(tile + ks * kPanel + r0 * 64 + (r * 64 + c * 16));
   }
 
-  // First operand of the 32x32x16 product from columns of a tile: lane l gives
-  // column 32 ct + l % 32 of 8 rows: r0 + 4 (l / 32) .. + 3 and the same + 8,
-  // which is the order in which the accumulator of a previous product holds
-  // those 16 rows (see `narrow`).  Each ds_read_b64_tr_b16 takes 4 rows x 16
+  // First operand of the 16x16x32 product from columns of a tile: lane l gives
+  // column 16 ct + l % 16 of 8 rows: r0 + 4 (l / 16) .. + 3 and the same + 16,
+  // which is the order in which two accumulators of a previous product hold
+  // those 32 rows (see `narrow`).  Each ds_read_b64_tr_b16 takes 4 rows x 16
   // columns per 16 lanes (lane i of them pointing at row i / 4, columns
-  // 4 (i % 4) .. + 3) and hands lane i column i.
+  // 4 (i % 4) .. + 3) and hands lane i column i.  r0 % 16 == 0.
   static __device__ __forceinline__ bf16x8 columns(const uint8_t* tile, int r0, int ct, int lane) {
     typedef short i16x8 __attribute__((ext_vector_type(8)));
-    const int r = 4 * (lane >> 5) + ((lane >> 2) & 3);
-    const int c = ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1), in = (lane & 1) * 8;
-    const uint8_t* p = tile + ct * kPanel + r0 * 64;
-    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_i16x4*)(p + (r * 64 + (c ^ swizzle(r)) * 16 + in)));
-    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_i16x4*)(p + ((r + 8) * 64 + (c ^ swizzle(r + 8)) * 16 + in)));
+    const int r = 4 * (lane >> 4) + ((lane >> 2) & 3);
+    const int c = 2 * (ct & 1) + ((lane >> 1) & 1);
+    const uint8_t* p = tile + (ct >> 1) * kPanel + r0 * 64 +
+                       (r * 64 + (c ^ swizzle(r)) * 16 + (lane & 1) * 8);
+    const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p));
+    const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + 16 * 64));
     const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(bf16x8, v);
   }
 };
 
-__device__ __forceinline__ f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+// 16x16x32 rather than 32x32x16: the card's power, not the instruction's rate,
+// bounds these kernels, and on random values the smaller shape does more for
+// it: 2090 TFLOP/s against 1840 with nothing else running (2450 each on zeros).
+__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// The accumulator of a 32x32 product holds in lane l column l % 32 of rows
-// 8 (i / 4) + 4 (l / 32) + i % 4, i = 0 .. 15.
-__device__ __forceinline__ int acc_row(int i, int lane) {
-  return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-}
+// The accumulator of a 16x16 product holds in lane l column l % 16 of rows
+// 4 (l / 16) + i, i = 0 .. 3.
+__device__ __forceinline__ int acc_row(int i, int lane) { return 4 * (lane >> 4) + i; }
 
-// Rows 16 u .. 16 u + 15 of a 32x32 accumulator as the second operand of the
+// Two accumulators, of rows 0 .. 15 and 16 .. 31, as the second operand of the
 // next product, rounded to bf16 (nearest even): no lane exchange is needed,
-// because that operand's order of the 16 summed rows is free as long as the
+// because that operand's order of the 32 summed rows is free as long as the
 // first operand (Tile::columns) uses the same.
-__device__ __forceinline__ bf16x8 narrow(const f32x16& v, int u) {
-  u32x4 w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[8 * u + 2 * i], v[8 * u + 2 * i + 1]);
-  return __builtin_bit_cast(bf16x8, w);
+__device__ __forceinline__ bf16x8 narrow(const f32x4& v, const f32x4& w) {
+  const u32x4 r = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(w[0], w[1]),
+                   pack_bf16x2(w[2], w[3])};
+  return __builtin_bit_cast(bf16x8, r);
 }
 
-// Max / sum over the two lanes l, l ^ 32 (result in both).
-__device__ __forceinline__ float pair_max(float v) {
-  const u32x2 r = __builtin_bit_cast(
-      u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+// Max / sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48 (result in all).
+__device__ __forceinline__ u32x2 swap16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a, b, false, false));
+}
+__device__ __forceinline__ u32x2 swap32(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(a, b, false, false));
+}
+__device__ __forceinline__ float column_max(float v) {
+  u32x2 r = swap16(__float_as_uint(v), __float_as_uint(v));
+  v = fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
+  r = swap32(__float_as_uint(v), __float_as_uint(v));
   return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
 }
-__device__ __forceinline__ float pair_sum(float v) {
-  const u32x2 r = __builtin_bit_cast(
-      u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+__device__ __forceinline__ float column_sum(float v) {
+  u32x2 r = swap16(__float_as_uint(v), __float_as_uint(v));
+  v = __uint_as_float(r.x) + __uint_as_float(r.y);
+  r = swap32(__float_as_uint(v), __float_as_uint(v));
   return __uint_as_float(r.x) + __uint_as_float(r.y);
 }
 
 // Store acc (columns: this lane's row of a tensor; rows: head dims) times mul
-// as bf16 to `dst`, head dims below `dim` only.  Lanes l and l + 32 hold 4 and
-// 4 of 8 neighbouring dims of one row; of two such runs each takes one whole,
-// so that every store is 16 bytes.
+// as bf16 to `dst`, head dims below `dim` only.  A lane holds 4 of 16 dims, its
+// neighbours l ^ 16 4 next to them; of two such runs each takes one whole, so
+// that every store is 16 bytes.
 template <int DP>
-__device__ __forceinline__ void store_row(uint16_t* dst, const f32x16 (&acc)[DP / 32], float mul,
+__device__ __forceinline__ void store_row(uint16_t* dst, const f32x4 (&acc)[DP / 16], float mul,
                                           int dim, int lane) {
 #pragma unroll
-  for (int ct = 0; ct < DP / 32; ++ct)
+  for (int ct = 0; ct < DP / 16; ct += 2) {
+    uint32_t w[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      uint32_t w[2][2];
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          w[k][e] = pack_bf16x2(acc[ct][4 * (i + k) + 2 * e] * mul,
-                                acc[ct][4 * (i + k) + 2 * e + 1] * mul);
-      const u32x2 x = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false));
-      const u32x2 y = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false));
-      const int d = ct * 32 + 8 * (i + (lane >> 5));
-      if (d < dim) *reinterpret_cast<u32x4*>(dst + d) = u32x4{x.x, y.x, x.y, y.y};
-    }
+      for (int e = 0; e < 2; ++e)
+        w[k][e] = pack_bf16x2(acc[ct + k][2 * e] * mul, acc[ct + k][2 * e + 1] * mul);
+    const u32x2 x = swap16(w[0][0], w[1][0]), y = swap16(w[0][1], w[1][1]);
+    const int d = (ct + ((lane >> 4) & 1)) * 16 + (lane >> 5) * 8;
+    if (d < dim) *reinterpret_cast<u32x4*>(dst + d) = u32x4{x.x, y.x, x.y, y.y};
+  }
 }
 
 // 8 values of one row (16 bytes), zero where the row or the column is outside.

@@ -37,6 +37,8 @@ constexpr float kSlack = 8.0f;
 template <int DP>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(AttentionArgs a) {
   typedef Tile<DP, kKeys, kWaves> KTile;
+  constexpr int kDims = DP / 16;   // 16-column results
+  constexpr int kSteps = DP / 32;  // products of one 16x16 square
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages][2][KTile::kBytes];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int g = blockIdx.x % a.kv_heads;
@@ -45,13 +47,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
   if (!find_tile<false>(a, a.group, kRows, blockIdx.x / a.kv_heads, s, rank, tiles)) return;
   const int row0 = rank * kRows;  // the last rows see the most keys
   const int rows = s.qn * a.group;
-  const int r = row0 + wave * 32 + (lane & 31);
-  const bool valid = r < rows;
-  const int i = min(r, rows - 1) / a.group;  // query
-  const int h = g * a.group + r % a.group;
-  // last visible key of a row, of the workgroup's last and of the wave's first and last
+  // last visible key of the workgroup's last row and of the wave's first and last
   const int shift = a.causal ? s.kn - s.qn : s.kn;
-  const int lim = min(i + shift, s.kn - 1);
   const int block_lim = min((min(row0 + kRows, rows) - 1) / a.group + shift, s.kn - 1);
   const int wave_first = row0 + wave * 32;
   const int wave_lim =
@@ -77,18 +74,28 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
 #pragma unroll
     for (int n = 0; n < kStages - 1; ++n) copy_tile();
   }
-  const uint16_t* qrow = a.q.p + (int64_t)(s.q0 + i) * a.q.row + h * a.q.head;
-  bf16x8 q[DP / 16];
+  // two sets of 16 rows: a lane's row, its query, head and last visible key
+  int64_t t[2];
+  int h[2], lim[2];
+  bool valid[2];
+  bf16x8 q[2][kSteps];
 #pragma unroll
-  for (int ks = 0; ks < DP / 16; ++ks)
-    q[ks] = load8(qrow, ks * 16 + 8 * (lane >> 5), a.head_dim, valid);
-
+  for (int n = 0; n < 2; ++n) {
+    const int r = wave_first + 16 * n + (lane & 15);
+    valid[n] = r < rows;
+    const int i = min(r, rows - 1) / a.group;
+    h[n] = g * a.group + r % a.group;
+    lim[n] = min(i + shift, s.kn - 1);
+    t[n] = s.q0 + i;
+    const uint16_t* qrow = a.q.p + t[n] * a.q.row + h[n] * a.q.head;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks)
+      q[n][ks] = load8(qrow, ks * 32 + 8 * (lane >> 4), a.head_dim, valid[n]);
+  }
   wait_copies<0>();  // and the loads of q
 
-  f32x16 o[DP / 32];
-#pragma unroll
-  for (int ct = 0; ct < DP / 32; ++ct) o[ct] = f32x16{};
-  float m = -INFINITY, l[2] = {0.0f, 0.0f};  // l: sums of even and odd values
+  f32x4 o[2][kDims] = {};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {};
   int stage = 0;
   for (int j = 0; j < nj; ++j) {
     wait_copies<2 * (kStages - 2) * KTile::kCopies>();  // later tiles' may still be under way
@@ -98,87 +105,103 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
     const uint8_t* V = lds[stage][1];
     stage = stage == kStages - 1 ? 0 : stage + 1;
     if (j * kKeys > wave_lim) continue;
-    constexpr int kDims = DP / 32;    // 32-column panels
-    constexpr int kSteps = DP / 16;   // products of one S^T square
-    // S^T: the K rows of 8 products are in flight ahead of the products, and
-    // the V columns of the first P V products follow them
-    f32x16 p[2] = {};
-    bf16x8 kf[2][kSteps], vf[2][kDims];
+    // S^T: the K rows of 8 reads are in flight ahead of the products, and the
+    // V columns of the first P V products follow them
+    f32x4 p[4][2] = {};
+    bf16x8 kf[kSteps][4], vf[2][kDims];
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) kf[t][ks] = KTile::rows(K, 32 * t, ks, lane);
+      for (int k = 0; k < 4; ++k) kf[ks][k] = KTile::rows(K, 16 * k, ks, lane);
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) p[t] = mma(kf[t][ks], q[ks], p[t]);
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) p[k][n] = mma(kf[ks][k], q[n][ks], p[k][n]);
 #pragma unroll
     for (int ct = 0; ct < kDims; ++ct) vf[0][ct] = KTile::columns(V, 0, ct, lane);
     __builtin_amdgcn_sched_group_barrier(kSchedRead, 8, 0);
 #pragma unroll
-    for (int i = 0; i < 2 * kSteps; ++i) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+    for (int i = 0; i < 4 * kSteps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 2, 0);
       __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
     }
     if (j * kKeys + kKeys - 1 > wave_free) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (j * kKeys + 32 * t + acc_row(e, lane) > lim) p[t][e] = -INFINITY;
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j * kKeys + 16 * k + acc_row(e, lane) > lim[n]) p[k][n][e] = -INFINITY;
     }
-    float top = p[0][0];
+    float top[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int n = 0; n < 2; ++n) {
+      top[n] = p[0][n][0];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, p[t][e]);
-    top = pair_max(top) * a.scale_log2;
-    if (__any(top > m + kSlack)) {
-      const float next = fmaxf(m, top);
-      const float alpha = __builtin_amdgcn_exp2f(m - (next == -INFINITY ? 0.0f : next));
-      m = next;
-      l[0] *= alpha;
-      l[1] *= alpha;
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[n] = fmaxf(top[n], p[k][n][e]);
+      top[n] = column_max(top[n]) * a.scale_log2;
+    }
+    if (__any(top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float next = fmaxf(m[n], top[n]);
+        const float alpha = __builtin_amdgcn_exp2f(m[n] - (next == -INFINITY ? 0.0f : next));
+        m[n] = next;
+        l[n] *= alpha;
+#pragma unroll
+        for (int ct = 0; ct < kDims; ++ct) o[n][ct] *= alpha;
+      }
+    }
+    // P and O^T, 32 keys at a time: the exponentials of the second 32 and the
+    // reads of their V columns go between the products of the first
+    const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      bf16x8 pu[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int k = 2 * u; k < 2 * u + 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[k][n][e] = __builtin_amdgcn_exp2f(fmaf(p[k][n][e], a.scale_log2, -base[n]));
+            l[n] += p[k][n][e];
+          }
+        pu[n] = narrow(p[2 * u][n], p[2 * u + 1][n]);
+      }
+      if (u == 0) {
+#pragma unroll
+        for (int ct = 0; ct < kDims; ++ct) vf[1][ct] = KTile::columns(V, 32, ct, lane);
+      }
 #pragma unroll
       for (int ct = 0; ct < kDims; ++ct)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[ct][e] *= alpha;
+        for (int n = 0; n < 2; ++n) o[n][ct] = mma(vf[u][ct], pu[n], o[n][ct]);
     }
-    // P and O^T, 16 keys at a time: the exponentials of the next 16 and the
-    // reads of their V columns go between the products of these
-    const float base = m == -INFINITY ? 0.0f : m;
+    __builtin_amdgcn_sched_group_barrier(kSchedValu, 56, 1);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-#pragma unroll
-      for (int e = 8 * (u & 1); e < 8 * (u & 1) + 8; ++e) {
-        p[u >> 1][e] = __builtin_amdgcn_exp2f(fmaf(p[u >> 1][e], a.scale_log2, -base));
-        l[e & 1] += p[u >> 1][e];
-      }
-      const bf16x8 pu = narrow(p[u >> 1], u & 1);
-      if (u < 3) {
-#pragma unroll
-        for (int ct = 0; ct < kDims; ++ct)
-          vf[(u + 1) & 1][ct] = KTile::columns(V, 16 * (u + 1), ct, lane);
-      }
-#pragma unroll
-      for (int ct = 0; ct < kDims; ++ct) o[ct] = mma(vf[u & 1][ct], pu, o[ct]);
-    }
-    __builtin_amdgcn_sched_group_barrier(kSchedValu, 28, 1);
-#pragma unroll
-    for (int i = 0; i < 4 * kDims; ++i) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 1);
+    for (int i = 0; i < 2 * kDims; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 2, 1);
       __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 1);
-      __builtin_amdgcn_sched_group_barrier(kSchedValu, 28 / kDims, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedValu, 56 / kDims, 1);
     }
   }
   wait_copies<0>();  // no copy may land after the workgroup has given up its LDS
-  const float sum = pair_sum(l[0] + l[1]);
-  if (!valid) return;
-  uint16_t* orow = a.o.p + (int64_t)(s.q0 + i) * a.o.row + h * a.o.head;
-  store_row<DP>(orow, o, sum > 0.0f ? 1.0f / sum : 0.0f, a.head_dim, lane);
-  if (lane < 32)
-    a.lse[(int64_t)h * a.total_q + s.q0 + i] =
-        sum > 0.0f ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const float sum = column_sum(l[n]);
+    if (!valid[n]) continue;
+    uint16_t* orow = a.o.p + t[n] * a.o.row + h[n] * a.o.head;
+    store_row<DP>(orow, o[n], sum > 0.0f ? 1.0f / sum : 0.0f, a.head_dim, lane);
+    if (lane < 16)
+      a.lse[(int64_t)h[n] * a.total_q + t[n]] =
+          sum > 0.0f ? (m[n] + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+  }
 }
 
 // ---- few query rows ---------------------------------------------------------
@@ -273,7 +296,7 @@ __device__ __forceinline__ int stream_share(int length) {
 template <int DP>
 __global__ __launch_bounds__(64, 1) void attention_stream_kernel(AttentionArgs a, Parts parts) {
   typedef Tile<DP, 32, 1> KTile;
-  constexpr int kDims = DP / 32, kSteps = DP / 16;
+  constexpr int kDims = DP / 16, kSteps = DP / 32;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][KTile::kBytes];
   const int lane = threadIdx.x;
   int length, at;
@@ -295,11 +318,6 @@ __global__ __launch_bounds__(64, 1) void attention_stream_kernel(AttentionArgs a
       const int row0 = (p.segment - g * row_tiles) * 32;
       const int rows = s.qn * a.group;
       const int shift = a.causal ? s.kn - s.qn : s.kn;
-      const int r = row0 + (lane & 31);
-      const bool valid = r < rows;
-      const int i = min(r, rows - 1) / a.group;
-      const int h = g * a.group + r % a.group;
-      const int lim = min(i + shift, s.kn - 1);
       const int free = min(row0 / a.group + shift, s.kn - 1);  // seen by every row
       Walk kw(a.k, (int64_t)s.k0 + t0 * 32, g, a.head_dim);
       Walk vw(a.v, (int64_t)s.k0 + t0 * 32, g, a.head_dim);
@@ -311,83 +329,114 @@ __global__ __launch_bounds__(64, 1) void attention_stream_kernel(AttentionArgs a
         vw.step(32);
         left -= 32;
       };
-      const uint16_t* qrow = a.q.p + (int64_t)(s.q0 + i) * a.q.row + h * a.q.head;
-      bf16x8 q[kSteps];
+      int64_t at[2];  // two sets of 16 rows
+      int h[2], lim[2];
+      bool valid[2];
+      bf16x8 q[2][kSteps];
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks)
-        q[ks] = load8(qrow, ks * 16 + 8 * (lane >> 5), a.head_dim, valid);
+      for (int n = 0; n < 2; ++n) {
+        const int r = row0 + 16 * n + (lane & 15);
+        valid[n] = r < rows;
+        const int i = min(r, rows - 1) / a.group;
+        h[n] = g * a.group + r % a.group;
+        lim[n] = min(i + shift, s.kn - 1);
+        at[n] = s.q0 + i;
+        const uint16_t* qrow = a.q.p + at[n] * a.q.row + h[n] * a.q.head;
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks)
+          q[n][ks] = load8(qrow, ks * 32 + 8 * (lane >> 4), a.head_dim, valid[n]);
+      }
       copy_tile(0);
       copy_tile(1);
-      f32x16 o[kDims];
-#pragma unroll
-      for (int ct = 0; ct < kDims; ++ct) o[ct] = f32x16{};
-      float m = -INFINITY, l = 0.0f;
+      f32x4 o[2][kDims] = {};
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {};
       int stage = 0;
       for (int t = t0; t < t1; ++t) {
         wait_copies<2 * KTile::kCopies>();
         const uint8_t* K = lds[stage][0];
         const uint8_t* V = lds[stage][1];
-        f32x16 x = {};
+        f32x4 x[2][2] = {};
 #pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) x = mma(KTile::rows(K, 0, ks, lane), q[ks], x);
+        for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bf16x8 kf = KTile::rows(K, 16 * k, ks, lane);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) x[k][n] = mma(kf, q[n][ks], x[k][n]);
+          }
         if (t * 32 + 31 > free) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (t * 32 + acc_row(e, lane) > lim) x[e] = -INFINITY;
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (t * 32 + 16 * k + acc_row(e, lane) > lim[n]) x[k][n][e] = -INFINITY;
         }
-        float top = x[0];
+        float top[2];
 #pragma unroll
-        for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
-        top = pair_max(top) * a.scale_log2;
-        if (__any(top > m + kSlack)) {
-          const float next = fmaxf(m, top);
-          const float alpha = __builtin_amdgcn_exp2f(m - (next == -INFINITY ? 0.0f : next));
-          m = next;
-          l *= alpha;
+        for (int n = 0; n < 2; ++n) {
+          top[n] = x[0][n][0];
 #pragma unroll
-          for (int ct = 0; ct < kDims; ++ct)
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[ct][e] *= alpha;
+            for (int e = 0; e < 4; ++e) top[n] = fmaxf(top[n], x[k][n][e]);
+          top[n] = column_max(top[n]) * a.scale_log2;
         }
-        const float base = m == -INFINITY ? 0.0f : m;
+        if (__any(top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], a.scale_log2, -base));
-          l += x[e];
+          for (int n = 0; n < 2; ++n) {
+            const float next = fmaxf(m[n], top[n]);
+            const float alpha = __builtin_amdgcn_exp2f(m[n] - (next == -INFINITY ? 0.0f : next));
+            m[n] = next;
+            l[n] *= alpha;
+#pragma unroll
+            for (int ct = 0; ct < kDims; ++ct) o[n][ct] *= alpha;
+          }
+        }
+        bf16x8 xu[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float base = m[n] == -INFINITY ? 0.0f : m[n];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[k][n][e] = __builtin_amdgcn_exp2f(fmaf(x[k][n][e], a.scale_log2, -base));
+              l[n] += x[k][n][e];
+            }
+          xu[n] = narrow(x[0][n], x[1][n]);
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const bf16x8 xu = narrow(x, u);
+        for (int ct = 0; ct < kDims; ++ct) {
+          const bf16x8 vf = KTile::columns(V, 0, ct, lane);
 #pragma unroll
-          for (int ct = 0; ct < kDims; ++ct)
-            o[ct] = mma(KTile::columns(V, 16 * u, ct, lane), xu, o[ct]);
+          for (int n = 0; n < 2; ++n) o[n][ct] = mma(vf, xu[n], o[n][ct]);
         }
         wait_lds();  // the stage has been read
         copy_tile(stage);
         stage ^= 1;
       }
       wait_copies<0>();
-      l = pair_sum(l);
-      if (valid) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float sum = column_sum(l[n]);
+        if (!valid[n]) continue;
         if (t0 == 0 && end == p.units) {
-          uint16_t* orow = a.o.p + (int64_t)(s.q0 + i) * a.o.row + h * a.o.head;
-          store_row<DP>(orow, o, l > 0.0f ? 1.0f / l : 0.0f, a.head_dim, lane);
-          if (lane < 32)
-            a.lse[(int64_t)h * a.total_q + s.q0 + i] =
-                l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+          uint16_t* orow = a.o.p + at[n] * a.o.row + h[n] * a.o.head;
+          store_row<DP>(orow, o[n], sum > 0.0f ? 1.0f / sum : 0.0f, a.head_dim, lane);
+          if (lane < 16)
+            a.lse[(int64_t)h[n] * a.total_q + at[n]] =
+                sum > 0.0f ? (m[n] + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
         } else {
-          const int64_t part = (2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * 32 + (lane & 31);
+          const int64_t part = (2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * 32 + 16 * n + (lane & 15);
           float* to = parts.o + part * a.head_dim;
 #pragma unroll
-          for (int ct = 0; ct < kDims; ++ct)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int d = ct * 32 + 8 * c + 4 * (lane >> 5);
-              if (d < a.head_dim)
-                *reinterpret_cast<f32x4*>(to + d) = f32x4{o[ct][4 * c], o[ct][4 * c + 1],
-                                                          o[ct][4 * c + 2], o[ct][4 * c + 3]};
-            }
-          if (lane < 32) parts.ml[part] = make_float2(m, l);
+          for (int ct = 0; ct < kDims; ++ct) {
+            const int d = ct * 16 + 4 * (lane >> 4);
+            if (d < a.head_dim) *reinterpret_cast<f32x4*>(to + d) = o[n][ct];
+          }
+          if (lane < 16) parts.ml[part] = make_float2(m[n], sum);
         }
       }
     }

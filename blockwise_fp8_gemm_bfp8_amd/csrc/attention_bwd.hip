@@ -59,24 +59,22 @@ template <int DP>
 __device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& shared, int n,
                                         int g) {
   typedef Tile<DP, kKeys, kWaves> KTile;
+  constexpr int kDims = DP / 16;   // 16-column results
+  constexpr int kSteps = DP / 32;  // products of one 16x16 square
   auto& lds = shared.tiles;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   Sequence s;
   int rank, tiles;
   if (!find_tile<false>(a, a.group, kRows, n, s, rank, tiles)) return;
-  const int row0 = rank * kRows;
+  const int row0 = rank * kRows;  // the last rows see the most keys
   const int rows = s.qn * a.group;
-  const int r = row0 + wave * 32 + (lane & 31);
-  const bool valid = r < rows;
-  const int i = min(r, rows - 1) / a.group;
-  const int h = g * a.group + r % a.group;
+  // last visible key of the workgroup's last row and of the wave's first and last
   const int shift = a.causal ? s.kn - s.qn : s.kn;
-  const int lim = min(i + shift, s.kn - 1);
   const int block_lim = min((min(row0 + kRows, rows) - 1) / a.group + shift, s.kn - 1);
   const int wave_first = row0 + wave * 32;
   const int wave_lim =
       wave_first < rows ? min((min(wave_first + 32, rows) - 1) / a.group + shift, s.kn - 1) : -1;
-  const int wave_free = min(wave_first / a.group + shift, s.kn - 1);
+  const int wave_free = min(wave_first / a.group + shift, s.kn - 1);  // seen by every row
 
   KTile kt, vt;
   kt.init(wave, lane, a.k.row, a.head_dim);
@@ -97,26 +95,37 @@ __device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& sh
 #pragma unroll
     for (int n = 0; n < kStages - 1; ++n) copy_tile();
   }
-  const int64_t t = s.q0 + i;
-  const uint16_t* qrow = a.q.p + t * a.q.row + h * a.q.head;
-  const uint16_t* drow = a.dout.p + t * a.dout.row + h * a.dout.head;
-  bf16x8 q[DP / 16], d[DP / 16];
+  // two sets of 16 rows: a lane's row, its query, head and last visible key
+  int64_t at[2];
+  int h[2], lim[2];
+  bool valid[2];
+  float lse2[2], delta[2];
+  bf16x8 q[2][kSteps], d[2][kSteps];
 #pragma unroll
-  for (int ks = 0; ks < DP / 16; ++ks) {
-    const int c = ks * 16 + 8 * (lane >> 5);
-    q[ks] = load8(qrow, c, a.head_dim, valid);
-    d[ks] = load8(drow, c, a.head_dim, valid);
-  }
-  float lse2 = 0.0f, delta = 0.0f;
-  if (valid) {
-    lse2 = a.lse2[(int64_t)h * a.total_q + t];
-    delta = -a.delta[(int64_t)h * a.total_q + t];
+  for (int n = 0; n < 2; ++n) {
+    const int r = wave_first + 16 * n + (lane & 15);
+    valid[n] = r < rows;
+    const int i = min(r, rows - 1) / a.group;
+    h[n] = g * a.group + r % a.group;
+    lim[n] = min(i + shift, s.kn - 1);
+    at[n] = s.q0 + i;
+    const uint16_t* qrow = a.q.p + at[n] * a.q.row + h[n] * a.q.head;
+    const uint16_t* drow = a.dout.p + at[n] * a.dout.row + h[n] * a.dout.head;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) {
+      const int c = ks * 32 + 8 * (lane >> 4);
+      q[n][ks] = load8(qrow, c, a.head_dim, valid[n]);
+      d[n][ks] = load8(drow, c, a.head_dim, valid[n]);
+    }
+    lse2[n] = delta[n] = 0.0f;
+    if (valid[n]) {
+      lse2[n] = a.lse2[(int64_t)h[n] * a.total_q + at[n]];
+      delta[n] = -a.delta[(int64_t)h[n] * a.total_q + at[n]];
+    }
   }
   wait_copies<0>();  // and the loads above
 
-  f32x16 acc[DP / 32];
-#pragma unroll
-  for (int ct = 0; ct < DP / 32; ++ct) acc[ct] = f32x16{};
+  f32x4 acc[2][kDims] = {};
   int stage = 0;
   for (int j = 0; j < nj; ++j) {
     wait_copies<2 * (kStages - 2) * KTile::kCopies>();  // later tiles' may still be under way
@@ -126,70 +135,92 @@ __device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& sh
     const uint8_t* V = lds[stage][1];
     stage = stage == kStages - 1 ? 0 : stage + 1;
     if (j * kKeys > wave_lim) continue;
-    constexpr int kDims = DP / 32;   // 32-column panels
-    constexpr int kSteps = DP / 16;  // products of one 32x32 square
-    bf16x8 kf[kSteps], vf[kSteps], kc[2][kDims];
+    bf16x8 kf[kSteps][2], vf[kSteps][2], kc[kDims];
 #pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) kf[ks] = KTile::rows(K, 0, ks, lane);
+    for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-    for (int t2 = 0; t2 < 2; ++t2) {
-      const int key0 = j * kKeys + 32 * t2;
-      // S^T and dP^T; the V rows are read between the products of S^T, the K
-      // columns of dQ^T between those of dP^T
-      f32x16 p = {}, dp = {};
+      for (int k = 0; k < 2; ++k) kf[ks][k] = KTile::rows(K, 16 * k, ks, lane);
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) vf[ks] = KTile::rows(V, 32 * t2, ks, lane);
+    for (int half = 0; half < 2; ++half) {
+      const int key0 = j * kKeys + 32 * half;
+      // S^T and dP^T of 32 keys; the V rows are read between the products of
+      // S^T, the K columns of dQ^T between those of dP^T
+      f32x4 p[2][2] = {}, dp[2][2] = {};
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) p = mma(kf[ks], q[ks], p);
+      for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int k = 0; k < 2; ++k) vf[ks][k] = KTile::rows(V, 32 * half + 16 * k, ks, lane);
 #pragma unroll
-        for (int ct = 0; ct < kDims; ++ct)
-          kc[u][ct] = KTile::columns(K, 32 * t2 + 16 * u, ct, lane);
+      for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) dp = mma(vf[ks], d[ks], dp);
-      if (t2 == 0) __builtin_amdgcn_sched_group_barrier(kSchedRead, kSteps, 0);
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+          for (int n = 0; n < 2; ++n) p[k][n] = mma(kf[ks][k], q[n][ks], p[k][n]);
+#pragma unroll
+      for (int ct = 0; ct < kDims; ++ct) kc[ct] = KTile::columns(K, 32 * half, ct, lane);
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) dp[k][n] = mma(vf[ks][k], d[n][ks], dp[k][n]);
+      if (half == 0) __builtin_amdgcn_sched_group_barrier(kSchedRead, 2 * kSteps, 0);
+#pragma unroll
+      for (int i = 0; i < 2 * kSteps; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMma, 2, 0);
         __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
       }
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+      for (int i = 0; i < 2 * kSteps; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMma, 2, 0);
         __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
       }
       if (key0 + 31 > wave_free) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (key0 + acc_row(e, lane) > lim) p[e] = -INFINITY;
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + 16 * k + acc_row(e, lane) > lim[n]) p[k][n][e] = -INFINITY;
       }
-      // dQ^T, 16 keys at a time; the K rows of the next square are read meanwhile
+      // dQ^T; the K rows of the next 32 keys are read meanwhile
+      bf16x8 ds[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int n = 0; n < 2; ++n) {
 #pragma unroll
-        for (int e = 8 * u; e < 8 * u + 8; ++e)
-          p[e] = __builtin_amdgcn_exp2f(fmaf(p[e], a.scale_log2, -lse2)) * (dp[e] - delta);
-        const bf16x8 ds = narrow(p, u);
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int ct = 0; ct < kDims; ++ct) acc[ct] = mma(kc[u][ct], ds, acc[ct]);
+          for (int e = 0; e < 4; ++e)
+            p[k][n][e] = __builtin_amdgcn_exp2f(fmaf(p[k][n][e], a.scale_log2, -lse2[n])) *
+                         (dp[k][n][e] - delta[n]);
+        ds[n] = narrow(p[0][n], p[1][n]);
       }
-      if (t2 == 0) {
 #pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) kf[ks] = KTile::rows(K, 32, ks, lane);
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int ct = 0; ct < kDims; ++ct) acc[n][ct] = mma(kc[ct], ds[n], acc[n][ct]);
+      if (half == 0) {
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) kf[ks][k] = KTile::rows(K, 32 + 16 * k, ks, lane);
       }
       __builtin_amdgcn_sched_group_barrier(kSchedValu, 36, 1);
 #pragma unroll
-      for (int i = 0; i < 2 * kDims; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 1);
+      for (int i = 0; i < kDims; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kSchedMma, 2, 1);
         __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 1);
-        __builtin_amdgcn_sched_group_barrier(kSchedValu, 36 / kDims, 1);
+        __builtin_amdgcn_sched_group_barrier(kSchedValu, 72 / kDims, 1);
       }
     }
   }
   wait_copies<0>();  // no copy may land after the workgroup has given up its LDS
-  if (!valid) return;
-  store_row<DP>(a.dq.p + t * a.dq.row + h * a.dq.head, acc, a.scale, a.head_dim, lane);
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+    if (valid[n])
+      store_row<DP>(a.dq.p + at[n] * a.dq.row + h[n] * a.dq.head, acc[n], a.scale, a.head_dim,
+                    lane);
 }
 
 template <int DP>
@@ -206,8 +237,8 @@ __device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>
                                           int g) {
   typedef typename DkdvShared<DP>::QTile QTile;
   typedef typename DkdvShared<DP>::VTile VTile;
-  constexpr int kDims = DP / 32;   // 32-column panels
-  constexpr int kSteps = DP / 16;  // products of one 32x32 square
+  constexpr int kDims = DP / 16;   // 16-column results
+  constexpr int kSteps = DP / 32;  // products of one 16x16 square
   auto& lds = shared.tiles;
   auto& vlds = shared.v;
   auto& stats = shared.stats;
@@ -218,9 +249,6 @@ __device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>
   if (!find_tile<true>(a, 1, kKeyRows, n0, s, rank, tiles)) return;
   const int row0 = (tiles - 1 - rank) * kKeyRows;  // the first keys are seen by the most queries
   const int key0 = row0 + kw * 32;                 // the wave's first key
-  const int key = key0 + (lane & 31);
-  const bool used = key < s.kn;
-  const int64_t krow = s.k0 + min(key, s.ka - 1);
   {
     VTile vt;
     vt.init(wave, lane, a.v.row, a.head_dim);
@@ -236,7 +264,6 @@ __device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>
   // first query of no masking: the one that sees the wave's last key, or none
   // if some of its keys are past the used length and must vanish
   const int wave_free = key0 + 31 < s.kn ? key0 + 31 + back : 0x7FFFFFFF;
-  const int from = used ? key + back : 0x7FFFFFFF;  // first query that sees this lane's key
 
   // this half's queries: i0 .. i0 + 31 of the group's hh-th head, n-th of all
   QTile qt, dt;
@@ -281,16 +308,26 @@ __device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>
     copy_square();
     copy_square();
   }
-  const uint16_t* kp = a.k.p + krow * a.k.row + g * a.k.head;
-  bf16x8 k[kSteps];
+  // two sets of 16 keys: a lane's key, its row, the first query that sees it
+  int64_t krow[2];
+  int from[2];
+  bool mine[2];
+  bf16x8 k[2][kSteps];
 #pragma unroll
-  for (int ks = 0; ks < kSteps; ++ks)
-    k[ks] = load8(kp, ks * 16 + 8 * (lane >> 5), a.head_dim, used);
+  for (int n = 0; n < 2; ++n) {
+    const int key = key0 + 16 * n + (lane & 15);
+    const bool used = key < s.kn;
+    mine[n] = key < s.ka;
+    from[n] = used ? key + back : 0x7FFFFFFF;
+    krow[n] = s.k0 + min(key, s.ka - 1);
+    const uint16_t* kp = a.k.p + krow[n] * a.k.row + g * a.k.head;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks)
+      k[n][ks] = load8(kp, ks * 32 + 8 * (lane >> 4), a.head_dim, used);
+  }
   wait_copies<0>();  // and the loads of k
 
-  f32x16 dk[kDims], dv[kDims];
-#pragma unroll
-  for (int ct = 0; ct < kDims; ++ct) dk[ct] = dv[ct] = f32x16{};
+  f32x4 dk[2][kDims] = {}, dv[2][kDims] = {};
   int at = per_head == 1 ? 0 : half;  // this half's square of its head
   int next = 0;
   for (int n = 0; n < total; n += 2) {
@@ -308,89 +345,124 @@ __device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>
     if (n + half >= total || i0 + 31 < wave_first) continue;
     const uint8_t* Q = lds[stage][half][0];
     const uint8_t* D = lds[stage][half][1];
-    const float* lses = stats[stage][half][0] + 4 * (lane >> 5);
-    const float* deltas = stats[stage][half][1] + 4 * (lane >> 5);
-    // S and dP; dP starts from -delta
-    f32x16 p = {}, dp;
+    const float* lses = stats[stage][half][0] + 4 * (lane >> 4);
+    const float* deltas = stats[stage][half][1] + 4 * (lane >> 4);
+    // S and dP of 32 queries; dP starts from -delta
+    f32x4 p[2][2] = {}, dp[2][2];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) dp[e] = deltas[8 * (e >> 2) + (e & 3)];
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) p = mma(QTile::rows(Q, 0, ks, lane), k[ks], p);
+      for (int n = 0; n < 2; ++n) dp[i][n] = *reinterpret_cast<const f32x4*>(deltas + 16 * i);
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks)
-      dp = mma(QTile::rows(D, 0, ks, lane), VTile::rows(vlds, kw * 32, ks, lane), dp);
-    __builtin_amdgcn_sched_group_barrier(kSchedRead, 4 + 4, 0);  // 4 of -delta
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+      for (int i = 0; i < 2; ++i) {
+        const bf16x8 qf = QTile::rows(Q, 16 * i, ks, lane);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) p[i][n] = mma(qf, k[n][ks], p[i][n]);
+      }
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) {
+      bf16x8 vf[2], df[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) vf[n] = VTile::rows(vlds, kw * 32 + 16 * n, ks, lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) df[i] = QTile::rows(D, 16 * i, ks, lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) dp[i][n] = mma(df[i], vf[n], dp[i][n]);
+    }
+    __builtin_amdgcn_sched_group_barrier(kSchedRead, 2 + 4, 0);  // 2 of -delta
+#pragma unroll
+    for (int i = 0; i < 2 * kSteps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 2, 0);
       __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < 2 * kSteps; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 2, 0);
     }
-    f32x16 lse2;
+    f32x4 lse2[2];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) lse2[e] = lses[8 * (e >> 2) + (e & 3)];
+    for (int i = 0; i < 2; ++i) lse2[i] = *reinterpret_cast<const f32x4*>(lses + 16 * i);
     if (i0 < wave_free) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (i0 + acc_row(e, lane) < from) p[e] = -INFINITY;
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i0 + 16 * i + acc_row(e, lane) < from[n]) p[i][n][e] = -INFINITY;
+    }
+    bf16x8 pu[2], du[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[i][n][e] = __builtin_amdgcn_exp2f(fmaf(p[i][n][e], a.scale_log2, -lse2[i][e]));
+          dp[i][n][e] *= p[i][n][e];
+        }
+      pu[n] = narrow(p[0][n], p[1][n]);
+      du[n] = narrow(dp[0][n], dp[1][n]);
     }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      p[e] = __builtin_amdgcn_exp2f(fmaf(p[e], a.scale_log2, -lse2[e]));
-      dp[e] *= p[e];
+    for (int ct = 0; ct < kDims; ++ct) {
+      const bf16x8 dc = QTile::columns(D, 0, ct, lane);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) dv[n][ct] = mma(dc, pu[n], dv[n][ct]);
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const bf16x8 pu = narrow(p, u), du = narrow(dp, u);
+    for (int ct = 0; ct < kDims; ++ct) {
+      const bf16x8 qc = QTile::columns(Q, 0, ct, lane);
 #pragma unroll
-      for (int ct = 0; ct < kDims; ++ct)
-        dv[ct] = mma(QTile::columns(D, 16 * u, ct, lane), pu, dv[ct]);
-#pragma unroll
-      for (int ct = 0; ct < kDims; ++ct)
-        dk[ct] = mma(QTile::columns(Q, 16 * u, ct, lane), du, dk[ct]);
+      for (int n = 0; n < 2; ++n) dk[n][ct] = mma(qc, du[n], dk[n][ct]);
     }
     __builtin_amdgcn_sched_group_barrier(kSchedRead, 8, 1);
 #pragma unroll
-    for (int i = 0; i < 4 * kDims; ++i) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 1);
+    for (int i = 0; i < 2 * kDims; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 2, 1);
       __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 1);
     }
   }
-  // The halves' sums: the first half takes dV, the second dK, 32 columns at a
-  // time through the LDS that the tiles no longer need (nothing is under way)
+  // The halves' sums: the first half takes dV, the second dK, a quarter of
+  // either at a time through the LDS that the tiles no longer need (nothing is
+  // under way)
   wait_copies<0>();
-  f32x4* mine = reinterpret_cast<f32x4*>(&lds[0][0][0][0]) + ((half * kKeyWaves + kw) * 4) * 64 + lane;
-  const f32x4* other =
-      reinterpret_cast<f32x4*>(&lds[0][0][0][0]) + (((half ^ 1) * kKeyWaves + kw) * 4) * 64 + lane;
+  constexpr int kPieces = 2 * kDims / 4;
+  f32x4* mine_lds =
+      reinterpret_cast<f32x4*>(&lds[0][0][0][0]) + (half * kKeyWaves + kw) * kPieces * 64 + lane;
+  const f32x4* other_lds = reinterpret_cast<f32x4*>(&lds[0][0][0][0]) +
+                           ((half ^ 1) * kKeyWaves + kw) * kPieces * 64 + lane;
+  static_assert(2 * kKeyWaves * kPieces * 64 * sizeof(f32x4) <= sizeof(shared.tiles), "fits");
 #pragma unroll
-  for (int ct = 0; ct < kDims; ++ct) {
+  for (int part = 0; part < 4; ++part) {
     __syncthreads();
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const f32x16& give = half == 0 ? dk[ct] : dv[ct];
-      mine[c * 64] = f32x4{give[4 * c], give[4 * c + 1], give[4 * c + 2], give[4 * c + 3]};
+    for (int c = 0; c < kPieces; ++c) {
+      const int n = (part * kPieces + c) / kDims, ct = (part * kPieces + c) % kDims;
+      mine_lds[c * 64] = half == 0 ? dk[n][ct] : dv[n][ct];
     }
     __syncthreads();
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const f32x4 add = other[c * 64];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (half == 0) dv[ct][4 * c + e] += add[e];
-        else dk[ct][4 * c + e] += add[e];
-      }
+    for (int c = 0; c < kPieces; ++c) {
+      const int n = (part * kPieces + c) / kDims, ct = (part * kPieces + c) % kDims;
+      const f32x4 add = other_lds[c * 64];
+      if (half == 0) dv[n][ct] += add;
+      else dk[n][ct] += add;
     }
   }
-  if (key >= s.ka) return;
-  if (half == 0)
-    store_row<DP>(a.dv.p + krow * a.dv.row + g * a.dv.head, dv, 1.0f, a.head_dim, lane);
-  else
-    store_row<DP>(a.dk.p + krow * a.dk.row + g * a.dk.head, dk, a.scale, a.head_dim, lane);
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    if (!mine[n]) continue;
+    if (half == 0)
+      store_row<DP>(a.dv.p + krow[n] * a.dv.row + g * a.dv.head, dv[n], 1.0f, a.head_dim, lane);
+    else
+      store_row<DP>(a.dk.p + krow[n] * a.dk.row + g * a.dk.head, dk[n], a.scale, a.head_dim, lane);
+  }
 }
 
 // Both kinds of tiles in one launch, so that neither waits for the other's
