@@ -342,11 +342,18 @@ __device__ __forceinline__ u32x2 swap16(uint32_t a, uint32_t b) {
 __device__ __forceinline__ u32x2 swap32(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(a, b, false, false));
 }
-__device__ __forceinline__ float column_max(float v) {
-  u32x2 r = swap16(__float_as_uint(v), __float_as_uint(v));
-  v = fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
-  r = swap32(__float_as_uint(v), __float_as_uint(v));
+// Of two values at once: lanes of even 16s get the max of a, of odd 16s of b;
+// both_columns hands every lane either.
+__device__ __forceinline__ float column_max(float a, float b) {
+  u32x2 r = swap16(__float_as_uint(a), __float_as_uint(b));
+  const float c = fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
+  r = swap32(__float_as_uint(c), __float_as_uint(c));
   return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
+}
+__device__ __forceinline__ void both_columns(float c, float (&v)[2]) {
+  const u32x2 r = swap16(__float_as_uint(c), __float_as_uint(c));
+  v[0] = __uint_as_float(r.x);
+  v[1] = __uint_as_float(r.y);
 }
 __device__ __forceinline__ float column_sum(float v) {
   u32x2 r = swap16(__float_as_uint(v), __float_as_uint(v));

@@ -34,6 +34,24 @@ constexpr int kStages = 3;          // tiles in LDS: one being read, two under w
 // multiplication of the accumulators.
 constexpr float kSlack = 8.0f;
 
+// The running maxima of two sets of rows take in `either` (column_max of both),
+// and their sums and accumulators are scaled to them.
+template <int DP>
+__device__ __forceinline__ void raise_maxima(float either, float (&m)[2], float (&l)[2],
+                                             f32x4 (&o)[2][DP / 16]) {
+  float top[2];
+  both_columns(either, top);
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const float next = fmaxf(m[n], top[n]);
+    const float alpha = __builtin_amdgcn_exp2f(m[n] - (next == -INFINITY ? 0.0f : next));
+    m[n] = next;
+    l[n] *= alpha;
+#pragma unroll
+    for (int ct = 0; ct < DP / 16; ++ct) o[n][ct] *= alpha;
+  }
+}
+
 template <int DP>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(AttentionArgs a) {
   typedef Tile<DP, kKeys, kWaves> KTile;
@@ -96,6 +114,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
 
   f32x4 o[2][kDims] = {};
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {};
+  float bound = -INFINITY;  // of the set whose maximum column_max leaves in this lane
   int stage = 0;
   for (int j = 0; j < nj; ++j) {
     wait_copies<2 * (kStages - 2) * KTile::kCopies>();  // later tiles' may still be under way
@@ -144,25 +163,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top[n] = fmaxf(top[n], p[k][n][e]);
-      top[n] = column_max(top[n]) * a.scale_log2;
     }
-    if (__any(top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const float next = fmaxf(m[n], top[n]);
-        const float alpha = __builtin_amdgcn_exp2f(m[n] - (next == -INFINITY ? 0.0f : next));
-        m[n] = next;
-        l[n] *= alpha;
-#pragma unroll
-        for (int ct = 0; ct < kDims; ++ct) o[n][ct] *= alpha;
-      }
+    const float either = column_max(top[0], top[1]) * a.scale_log2;
+    if (__any(either > bound)) {
+      raise_maxima<DP>(either, m, l, o);
+      bound = ((lane & 16) ? m[1] : m[0]) + kSlack;
     }
-    // P and O^T, 32 keys at a time: the exponentials of the second 32 and the
-    // reads of their V columns go between the products of the first
+    // P and O^T, 32 keys of 16 rows at a time: the exponentials of the next go
+    // between the products of one
     const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      bf16x8 pu[2];
+      if (u == 0) {
+#pragma unroll
+        for (int ct = 0; ct < kDims; ++ct) vf[1][ct] = KTile::columns(V, 32, ct, lane);
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
 #pragma unroll
@@ -172,23 +187,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
             p[k][n][e] = __builtin_amdgcn_exp2f(fmaf(p[k][n][e], a.scale_log2, -base[n]));
             l[n] += p[k][n][e];
           }
-        pu[n] = narrow(p[2 * u][n], p[2 * u + 1][n]);
+        const bf16x8 pu = narrow(p[2 * u][n], p[2 * u + 1][n]);
+#pragma unroll
+        for (int ct = 0; ct < kDims; ++ct) o[n][ct] = mma(vf[u][ct], pu, o[n][ct]);
       }
-      if (u == 0) {
-#pragma unroll
-        for (int ct = 0; ct < kDims; ++ct) vf[1][ct] = KTile::columns(V, 32, ct, lane);
-      }
-#pragma unroll
-      for (int ct = 0; ct < kDims; ++ct)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) o[n][ct] = mma(vf[u][ct], pu[n], o[n][ct]);
     }
-    __builtin_amdgcn_sched_group_barrier(kSchedValu, 56, 1);
+    __builtin_amdgcn_sched_group_barrier(kSchedValu, 28, 1);
 #pragma unroll
-    for (int i = 0; i < 2 * kDims; ++i) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMma, 2, 1);
-      __builtin_amdgcn_sched_group_barrier(kSchedRead, 2, 1);
-      __builtin_amdgcn_sched_group_barrier(kSchedValu, 56 / kDims, 1);
+    for (int i = 0; i < 4 * kDims; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMma, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedValu, 28 / kDims + 1, 1);
     }
   }
   wait_copies<0>();  // no copy may land after the workgroup has given up its LDS
@@ -350,6 +359,7 @@ __global__ __launch_bounds__(64, 1) void attention_stream_kernel(AttentionArgs a
       copy_tile(1);
       f32x4 o[2][kDims] = {};
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {};
+      float bound = -INFINITY;
       int stage = 0;
       for (int t = t0; t < t1; ++t) {
         wait_copies<2 * KTile::kCopies>();
@@ -381,18 +391,11 @@ __global__ __launch_bounds__(64, 1) void attention_stream_kernel(AttentionArgs a
           for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) top[n] = fmaxf(top[n], x[k][n][e]);
-          top[n] = column_max(top[n]) * a.scale_log2;
         }
-        if (__any(top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float next = fmaxf(m[n], top[n]);
-            const float alpha = __builtin_amdgcn_exp2f(m[n] - (next == -INFINITY ? 0.0f : next));
-            m[n] = next;
-            l[n] *= alpha;
-#pragma unroll
-            for (int ct = 0; ct < kDims; ++ct) o[n][ct] *= alpha;
-          }
+        const float either = column_max(top[0], top[1]) * a.scale_log2;
+        if (__any(either > bound)) {
+          raise_maxima<DP>(either, m, l, o);
+          bound = ((lane & 16) ? m[1] : m[0]) + kSlack;
         }
         bf16x8 xu[2];
 #pragma unroll
