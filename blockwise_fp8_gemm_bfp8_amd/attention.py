@@ -108,7 +108,7 @@ def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor = None,
     T, H, D = size
     _check_i32(positions, "positions", T, device)
     if out is None:
-        out = x.new_empty(size)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     _, _, yh = _heads(out, "out", (x.dtype,), device, size)
     length, half, _ = table.shape
     _check("bfp8_rope", lib().bfp8_rope(
@@ -170,7 +170,9 @@ def _workspace(shape, backward, given, like):
 
 
 def _output(out, like):
-    return like.new_empty(like.shape) if out is None else out
+    if out is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    return out
 
 
 def _check_lse(lse, heads, tokens, device: int):

@@ -88,6 +88,16 @@ bfp8_status scan_heads(const bfp8_heads& t, int64_t rows, int heads, int dim, hi
   return BFP8_OK;
 }
 
+// Debug mode: q whole, k and v where every row is used (rows past a sequence's
+// used length may hold anything).
+bfp8_status scan_inputs(const bfp8_attention_shape& s, const bfp8_heads& q, const bfp8_heads& k,
+                        const bfp8_heads& v, hipStream_t stream) {
+  bfp8_status st = scan_heads(q, s.total_q, s.heads, s.head_dim, stream);
+  if (st != BFP8_OK || s.k_lens != nullptr) return st;
+  st = scan_heads(k, s.total_k, s.kv_heads, s.head_dim, stream);
+  return st != BFP8_OK ? st : scan_heads(v, s.total_k, s.kv_heads, s.head_dim, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -157,11 +167,7 @@ bfp8_status bfp8_attention_forward(const bfp8_attention_shape* shape, bfp8_heads
   if ((st = check_tensor(o, s.total_q, s.heads, s.head_dim)) != BFP8_OK) return st;
   if (lse == nullptr) return BFP8_ERR_NULL;
   if (!aligned16(lse) || (workspace != nullptr && !aligned16(workspace))) return BFP8_ERR_ALIGN;
-  if (debug_checks_enabled()) {
-    if ((st = scan_heads(q, s.total_q, s.heads, s.head_dim, stream)) != BFP8_OK) return st;
-    if ((st = scan_heads(k, s.total_k, s.kv_heads, s.head_dim, stream)) != BFP8_OK) return st;
-    if ((st = scan_heads(v, s.total_k, s.kv_heads, s.head_dim, stream)) != BFP8_OK) return st;
-  }
+  if (debug_checks_enabled() && (st = scan_inputs(s, q, k, v, stream)) != BFP8_OK) return st;
   AttentionArgs a = make_args(s);
   a.q = as_heads(q);
   a.k = as_heads(k);
@@ -192,9 +198,7 @@ bfp8_status bfp8_attention_backward(const bfp8_attention_shape* shape, bfp8_head
   const size_t need = bfp8_attention_workspace_bytes(shape, 1);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BFP8_ERR_WORKSPACE;
   if (debug_checks_enabled()) {
-    if ((st = scan_heads(q, s.total_q, s.heads, s.head_dim, stream)) != BFP8_OK) return st;
-    if ((st = scan_heads(k, s.total_k, s.kv_heads, s.head_dim, stream)) != BFP8_OK) return st;
-    if ((st = scan_heads(v, s.total_k, s.kv_heads, s.head_dim, stream)) != BFP8_OK) return st;
+    if ((st = scan_inputs(s, q, k, v, stream)) != BFP8_OK) return st;
     if ((st = scan_heads(dout, s.total_q, s.heads, s.head_dim, stream)) != BFP8_OK) return st;
   }
   AttentionArgs a = make_args(s);

@@ -185,6 +185,42 @@ def test_single_queries_over_a_long_cache():
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+STREAMED = {
+    # name: (queries, used keys, room, heads, kv heads, head size, causal)
+    "hundred_sequences": ([(1, 0, 2, 1)[i % 4] for i in range(100)],
+                          [(i * 97) % 3300 for i in range(100)], 3300, 2, 1, 64, True),
+    "many_rows": ([50, 1], [2500, 2000], 2500, 8, 2, 128, True),
+    "not_causal": ([3, 40], [1, 1999], 2000, 4, 2, 80, False),
+    "wide_group": ([1, 5], [1024, 1025], 1100, 16, 1, 128, True),
+    "one_sequence": ([1], [5000], 5000, 1, 1, 128, True),
+    "no_keys": ([2, 1, 1], [0, 1500, 0], 1500, 2, 2, 8, True),
+    "no_queries": ([0, 3, 0, 0], [1500, 1400, 10, 0], 1500, 2, 2, 104, True),
+    "more_queries_than_keys": ([40, 2], [7, 1200], 1200, 2, 1, 64, True),
+}
+
+
+@pytest.mark.parametrize("name", list(STREAMED))
+def test_streamed_keys(name):
+    """The kernel of few rows over many keys (it asks for a workspace), its
+    joined parts, and the rows of no sequence left alone."""
+    queries, used, room, H, KV, D, causal = STREAMED[name]
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    T, S = sum(queries) + 2, room * len(used)
+    q, k, v = tensors(T, S, H, KV, D, "dense", gen)
+    cq, ck = cu(queries), cu([room] * len(used))
+    args = (q, k, v, gpu_ints(cq), gpu_ints(ck), gpu_ints(used))
+    assert bfp8.attention_workspace_bytes(*args, causal=causal) > 0
+    o = torch.full((T, H, D), 7.0, device="cuda", dtype=torch.bfloat16)
+    lse = torch.full((H, T), 7.0, device="cuda")
+    bfp8.attention_forward(*args, causal=causal, out=o, lse=lse)
+    assert (o[-2:] == 7).all() and (lse[:, -2:] == 7).all()
+    want, wl, ob, lb = ref.attention(f64(q), f64(k), f64(v), cq, ck, used, causal, D ** -0.5)
+    within(o, want, ob, name + " o")
+    within(lse, wl, lb, name + " lse")
+    o2, lse2 = bfp8.attention_forward(*args, causal=causal)
+    assert torch.equal(o[:-2], o2[:-2]) and torch.equal(lse[:, :-2], lse2[:, :-2])
+
+
 def test_scores_of_any_size():
     """Scores in the thousands (a running maximum that keeps growing, and one
     that starts at its largest), the same result for keys in either order."""
