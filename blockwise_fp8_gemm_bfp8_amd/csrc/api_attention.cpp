@@ -150,8 +150,8 @@ bfp8_status bfp8_rope(const void* x, int64_t x_row, int64_t x_head, void* y, int
 size_t bfp8_attention_workspace_bytes(const bfp8_attention_shape* shape, int backward) {
   if (check_shape(shape) != BFP8_OK || (backward != 0 && backward != 1))
     return static_cast<size_t>(-1);
-  if (backward) return static_cast<size_t>(shape->heads) * shape->total_q * 2 * sizeof(float);
-  return attention_forward_workspace(make_args(*shape));
+  const AttentionArgs a = make_args(*shape);
+  return backward ? attention_backward_workspace(a) : attention_forward_workspace(a);
 }
 
 bfp8_status bfp8_attention_forward(const bfp8_attention_shape* shape, bfp8_heads q, bfp8_heads k,
@@ -211,9 +211,7 @@ bfp8_status bfp8_attention_backward(const bfp8_attention_shape* shape, bfp8_head
   a.dk = as_heads(dk);
   a.dv = as_heads(dv);
   a.lse = const_cast<float*>(lse);
-  a.lse2 = static_cast<float*>(workspace);
-  a.delta = a.lse2 + s.heads * s.total_q;
-  return launch_attention_backward(a, stream);
+  return launch_attention_backward(a, workspace, stream);
 }
 
 }  // extern "C"

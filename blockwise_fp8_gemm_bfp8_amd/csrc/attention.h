@@ -2,6 +2,9 @@
 // of the ABI; see include/bfp8_attention.h).
 #pragma once
 
+#include <algorithm>
+#include <cmath>
+
 #include "bfp8_attention.h"
 #include "common.h"
 
@@ -11,6 +14,16 @@ namespace bfp8 {
 struct Heads {
   uint16_t* p;  // bf16 bits
   int64_t row, head;
+};
+
+// A tile of n steps has ceil(n / chunk) parts, at most `most`: only long tiles
+// are split, whatever the lengths that the host cannot see.
+struct Split {
+  int most, chunk;
+  __host__ __device__ __forceinline__ int parts(int n) const {
+    return most == 1 || n <= chunk ? 1 : min_int(most, (n - 1) / chunk + 1);
+  }
+  static __host__ __device__ __forceinline__ int min_int(int a, int b) { return a < b ? a : b; }
 };
 
 struct AttentionArgs {
@@ -25,12 +38,60 @@ struct AttentionArgs {
   float* lse;                  // [heads][total_q]
   float* lse2;                 // [heads][total_q] each (backward): L log2(e), or 0
   float* delta;                // for L = -inf, and -sum dO O
+  // Where few workgroups meet long sequences, a tile's sum is split over
+  // several, and a later kernel adds their float32 parts in order (see Split).
+  Split split_q;               // of the keys of a row tile, in tiles of 64
+  Split split_k;               // of the queries of a dkdv tile, in pairs of squares
+  float* part_o;               // forward: [parts][heads][total_q][head_dim]
+  float2* part_ml;             // [parts][heads][total_q]: maximum and sum
+  float* part_dq;              // backward: [parts][heads][total_q][head_dim]
+  float* part_dk;              // [parts][kv_heads][total_k][head_dim]
+  float* part_dv;
 };
+
+// An upper bound on the tiles of all sequences, whose lengths are on the device.
+inline int64_t tile_bound(const int32_t* cu, int64_t batch, int64_t total, int64_t mult,
+                          int64_t unit) {
+  if (cu == nullptr) return batch * ((total / batch * mult + unit - 1) / unit);
+  return (total * mult + batch * (unit - 1)) / unit;
+}
+
+// What the host can say of the sequences' lengths, which are on the device:
+// with cu, the longest of `batch` random cuts is about H(batch) times their
+// mean (the harmonic sum), and a row's own sequence twice the mean; without,
+// all are equal.
+struct Lengths {
+  double mean, longest, own;
+  Lengths(const int32_t* cu, int64_t batch, int64_t total) {
+    mean = static_cast<double>(total) / static_cast<double>(batch);
+    longest = own = mean;
+    if (cu != nullptr && batch > 1) {
+      longest = mean * std::min(std::log(static_cast<double>(batch)) + 0.577,
+                                static_cast<double>(batch));
+      own = mean * std::min(2.0, longest / mean);
+    }
+  }
+};
+
+// How to split a kernel's tiles over several workgroups: into stretches of the
+// time that all its work takes evenly shared (`balanced` us, at least 12: a
+// workgroup's start and end take 5 to 8).  A step takes `step` us, the longest
+// tile about `longest`, and one part of every tile is `floats` values, written
+// and read at 5 TB/s; not to split at all if a long tile would not gain.
+inline Split choose_split(double longest, double balanced, double step, double floats) {
+  const double chunk = std::max(balanced, 12.0);
+  const double most = std::min(16.0, std::ceil(longest / chunk));
+  // a longest tile in the middle between the mean and that estimate, and the launch that adds
+  const double likely = 0.7 * longest, parts = std::ceil(likely / chunk);
+  if (most < 2 || likely - likely / parts < parts * floats * 8 / 5e6 + 8) return Split{1, 1};
+  return Split{static_cast<int>(most), std::max(1, static_cast<int>(chunk / step))};
+}
 
 bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
                                      size_t workspace_bytes, hipStream_t stream);
-bfp8_status launch_attention_backward(const AttentionArgs& a, hipStream_t stream);
 size_t attention_forward_workspace(const AttentionArgs& a);
+bfp8_status launch_attention_backward(AttentionArgs a, void* workspace, hipStream_t stream);
+size_t attention_backward_workspace(const AttentionArgs& a);
 
 bfp8_status launch_rope_table(float* table, int64_t positions, int rot_dim, double base,
                               double factor, double original_length, int scaling,
@@ -65,6 +126,16 @@ constexpr float kLn2 = 0.6931471805599453f;
 // classes of instructions for __builtin_amdgcn_sched_group_barrier
 constexpr int kSchedValu = 0x2, kSchedMma = 0x8, kSchedRead = 0x100;
 constexpr int kNoData = 0x7FFFFFF0;  // a buffer offset past every extent: reads as zero
+
+// The kernel's arguments (its first parameter), read again from where they were
+// passed: what only a kernel's end needs would otherwise wait in scalar
+// registers through its loops, more of them than there are.
+__device__ __forceinline__ AttentionArgs late_args() {
+  typedef const __attribute__((address_space(4))) AttentionArgs* Passed;
+  Passed p = (Passed)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));  // not before this point
+  return *(const AttentionArgs*)p;
+}
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -103,6 +174,26 @@ __device__ __forceinline__ Sequence from_lane(const Sequence& s, int l) {
 }
 __device__ __forceinline__ Sequence load_sequence(const AttentionArgs& a, int b) {
   return from_lane(lane_sequence(a, b), 0);
+}
+
+// Last key that row r of a kv head's rows (query r / group) sees; -1: none.
+__device__ __forceinline__ int last_key(const AttentionArgs& a, const Sequence& s, int r) {
+  return min(r / a.group + (a.causal ? s.kn - s.qn : s.kn), s.kn - 1);
+}
+// Tiles of 64 keys that the row tile row0 .. row0 + unit - 1 sees.
+__device__ __forceinline__ int key_tiles(const AttentionArgs& a, const Sequence& s, int row0,
+                                         int unit) {
+  const int last = last_key(a, s, min(row0 + unit, s.qn * a.group) - 1);
+  return last < 0 ? 0 : last / 64 + 1;
+}
+// First query, a multiple of 32, that sees key row0 or later, and the squares of
+// 32 queries from there on, of one head.
+__device__ __forceinline__ int first_square(const AttentionArgs& a, const Sequence& s, int row0,
+                                            int& per_head) {
+  const int back = a.causal ? s.qn - s.kn : -s.kn;  // key j is first seen by query j + back
+  const int first = row0 < s.kn ? max(row0 + back, 0) & ~31 : s.qn;
+  per_head = first < s.qn ? (s.qn - first + 31) / 32 : 0;
+  return first;
 }
 
 // Sum over the 64 lanes of a wave (data-parallel moves: row shifts, then two
@@ -199,8 +290,8 @@ __device__ __forceinline__ i32x4 buffer(uint64_t addr, int bytes) {
 // A walk over the rows of one head of a tensor (all of it wave-uniform): the
 // rows at its place as a buffer whose end is the last row's last value, so a
 // tile row past it reads zeros, whoever's rows lie there.  Row strides are at
-// most 2^22 elements and tiles at most 128 rows, so offsets inside a tile and
-// steps of the walk fit 31 bits; the place itself is a 64-bit address.
+// most 2^22 elements and tiles at most 128 rows, so offsets inside a tile fit
+// 31 bits; the place itself is a 64-bit address.
 struct Walk {
   uint64_t at;
   int row_bytes, dim_bytes;
@@ -212,7 +303,7 @@ struct Walk {
   __device__ __forceinline__ i32x4 rows(int n) const {
     return buffer(at, n > 0 ? (n - 1) * row_bytes + dim_bytes : 0);
   }
-  __device__ __forceinline__ void step(int n) { at += static_cast<int64_t>(n * row_bytes); }
+  __device__ __forceinline__ void step(int n) { at += static_cast<int64_t>(n) * row_bytes; }
 };
 
 // 16 bytes per lane from a buffer to LDS, the 64 lanes side by side from LDS

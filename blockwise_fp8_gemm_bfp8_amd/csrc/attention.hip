@@ -14,8 +14,6 @@
 // (query, head of the group) pair: the heads that share keys share their
 // tiles, and few queries fill more of a tile.  Each wave owns 32 rows; tiles
 // of 64 keys pass through two LDS stages, filled by LDS-DMA one tile ahead.
-#include <algorithm>
-
 #include "attention.h"
 
 namespace bfp8 {
@@ -53,7 +51,7 @@ __device__ __forceinline__ void raise_maxima(float either, float (&m)[2], float 
 }
 
 template <int DP>
-__global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(AttentionArgs a, int places) {
   typedef Tile<DP, kKeys, kWaves> KTile;
   constexpr int kDims = DP / 16;   // 16-column results
   constexpr int kSteps = DP / 32;  // products of one 16x16 square
@@ -62,22 +60,27 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
   const int g = blockIdx.x % a.kv_heads;
   Sequence s;
   int rank, tiles;
-  if (!find_tile<false>(a, a.group, kRows, blockIdx.x / a.kv_heads, s, rank, tiles)) return;
+  const int place = blockIdx.x / a.kv_heads;
+  const int split = place / places;  // first every tile's first part
+  if (!find_tile<false>(a, a.group, kRows, place - split * places, s, rank, tiles)) return;
   const int row0 = rank * kRows;  // the last rows see the most keys
   const int rows = s.qn * a.group;
-  // last visible key of the workgroup's last row and of the wave's first and last
-  const int shift = a.causal ? s.kn - s.qn : s.kn;
-  const int block_lim = min((min(row0 + kRows, rows) - 1) / a.group + shift, s.kn - 1);
+  const int all = key_tiles(a, s, row0, kRows);
+  const int parts = a.split_q.parts(all);
+  if (split >= parts) return;
+  const int j0 = static_cast<int>(static_cast<int64_t>(all) * split / parts);
+  const int nj = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / parts);
+  // last key that the wave's last row sees, and its first
   const int wave_first = row0 + wave * 32;
-  const int wave_lim =
-      wave_first < rows ? min((min(wave_first + 32, rows) - 1) / a.group + shift, s.kn - 1) : -1;
-  const int wave_free = min(wave_first / a.group + shift, s.kn - 1);  // seen by every row
+  const int wave_lim = wave_first < rows ? last_key(a, s, min(wave_first + 32, rows) - 1) : -1;
+  const int wave_free = last_key(a, s, wave_first);  // seen by every row
 
   KTile kt, vt;
   kt.init(wave, lane, a.k.row, a.head_dim);
   vt.init(wave, lane, a.v.row, a.head_dim);
-  Walk kw(a.k, s.k0, g, a.head_dim), vw(a.v, s.k0, g, a.head_dim);
-  int left = s.kn, ahead = 0;  // keys from the walks' place on; stage of the next copies
+  Walk kw(a.k, (int64_t)s.k0 + j0 * kKeys, g, a.head_dim);
+  Walk vw(a.v, (int64_t)s.k0 + j0 * kKeys, g, a.head_dim);
+  int left = s.kn - j0 * kKeys, ahead = 0;  // keys from there on; stage of the next copies
   auto copy_tile = [&]() {     // tiles in their order; past the end zeros, counted as the others
     const int n = min(left, kKeys);
     kt.copy(lds[ahead][0], wave, kw.rows(n));
@@ -87,8 +90,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
     left -= kKeys;
     ahead = ahead == kStages - 1 ? 0 : ahead + 1;
   };
-  const int nj = block_lim < 0 ? 0 : block_lim / kKeys + 1;
-  if (nj > 0) {
+  if (nj > j0) {
 #pragma unroll
     for (int n = 0; n < kStages - 1; ++n) copy_tile();
   }
@@ -101,10 +103,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
   for (int n = 0; n < 2; ++n) {
     const int r = wave_first + 16 * n + (lane & 15);
     valid[n] = r < rows;
-    const int i = min(r, rows - 1) / a.group;
     h[n] = g * a.group + r % a.group;
-    lim[n] = min(i + shift, s.kn - 1);
-    t[n] = s.q0 + i;
+    lim[n] = last_key(a, s, min(r, rows - 1));
+    t[n] = s.q0 + min(r, rows - 1) / a.group;
     const uint16_t* qrow = a.q.p + t[n] * a.q.row + h[n] * a.q.head;
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks)
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {};
   float bound = -INFINITY;  // of the set whose maximum column_max leaves in this lane
   int stage = 0;
-  for (int j = 0; j < nj; ++j) {
+  for (int j = j0; j < nj; ++j) {
     wait_copies<2 * (kStages - 2) * KTile::kCopies>();  // later tiles' may still be under way
     __syncthreads();
     copy_tile();
@@ -205,11 +206,62 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
   for (int n = 0; n < 2; ++n) {
     const float sum = column_sum(l[n]);
     if (!valid[n]) continue;
+    if (parts > 1) {
+      const int64_t part = ((int64_t)split * a.heads + h[n]) * a.total_q + t[n];
+#pragma unroll
+      for (int ct = 0; ct < kDims; ++ct) {
+        const int d = ct * 16 + 4 * (lane >> 4);
+        if (d < a.head_dim)
+          *reinterpret_cast<f32x4*>(a.part_o + part * a.head_dim + d) = o[n][ct];
+      }
+      if (lane < 16) a.part_ml[part] = make_float2(m[n], sum);
+      continue;
+    }
     uint16_t* orow = a.o.p + t[n] * a.o.row + h[n] * a.o.head;
     store_row<DP>(orow, o[n], sum > 0.0f ? 1.0f / sum : 0.0f, a.head_dim, lane);
     if (lane < 16)
       a.lse[(int64_t)h[n] * a.total_q + t[n]] =
           sum > 0.0f ? (m[n] + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+// Joins the parts of each row that has several, in their order: one thread per 4
+// values of one row of sequence blockIdx.y, whole rows to a workgroup.
+__global__ __launch_bounds__(256) void attention_join_splits_kernel(AttentionArgs a) {
+  const Sequence s = load_sequence(a, blockIdx.y);
+  const unsigned per_row = a.head_dim / 4, slots = 256 / per_row;
+  const unsigned slot = threadIdx.x / per_row;
+  const int d = (threadIdx.x - slot * per_row) * 4;
+  if (slot >= slots) return;
+  const int64_t rows = (int64_t)a.heads * a.total_q;
+  const unsigned heads = a.heads;
+  for (unsigned r = blockIdx.x * slots + slot; r < s.qn * heads; r += gridDim.x * slots) {
+    const unsigned i = r / heads, h = r - i * heads;
+    const int tile = static_cast<int>(i * a.group + h % a.group) / kRows;
+    const int parts = a.split_q.parts(key_tiles(a, s, tile * kRows, kRows));
+    if (parts == 1) continue;
+    const int64_t t = s.q0 + i;
+    const int64_t row = (int64_t)h * a.total_q + t;
+    float top = -INFINITY, sum = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int n = 0; n < parts; ++n) {
+      const float2 x = a.part_ml[n * rows + row];
+      const f32x4 v = *reinterpret_cast<const f32x4*>(a.part_o + (n * rows + row) * a.head_dim + d);
+      const float next = fmaxf(top, x.x);
+      const float base = next == -INFINITY ? 0.0f : next;
+      const float keep = __builtin_amdgcn_exp2f(top - base);
+      const float mul = __builtin_amdgcn_exp2f(x.x - base);
+      top = next;
+      sum = sum * keep + x.y * mul;
+      o = o * keep + v * mul;
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    u32x2 w;
+    w.x = pack_bf16x2(o[0] * inv, o[1] * inv);
+    w.y = pack_bf16x2(o[2] * inv, o[3] * inv);
+    *reinterpret_cast<u32x2*>(a.o.p + t * a.o.row + h * a.o.head + d) = w;
+    if (d == 0) a.lse[row] = sum > 0.0f ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
   }
 }
 
@@ -546,16 +598,33 @@ bool streams_keys(const AttentionArgs& a) {
          most_rows * a.kv_heads * most_keys < (int64_t(1) << 31);
 }
 
+// The split of the row tiles' keys; a tile of 64 keys takes about 1.1 us.
+Split key_split(const AttentionArgs& a) {
+  if (a.total_q == 0 || a.total_k == 0 || a.batch > 65535) return Split{1, 1};
+  if ((int64_t)a.total_q * a.heads >= (int64_t(1) << 31)) return Split{1, 1};  // rows in 32 bits
+  const Lengths keys(a.cu_k, a.batch, a.total_k);
+  const double step = 1.1, tile = step / kKeys, cus = 256;
+  const double workgroups = static_cast<double>(
+      tile_bound(a.cu_q, a.batch, a.total_q, a.group, kRows) * a.kv_heads);
+  const double balanced = workgroups * keys.own * tile * (a.causal ? 0.5 : 1.0) / cus;
+  return choose_split(keys.longest * tile, balanced, step,
+                      static_cast<double>(a.total_q) * a.heads * (a.head_dim + 2));
+}
+
 }  // namespace
 
 size_t attention_forward_workspace(const AttentionArgs& a) {
-  if (!streams_keys(a)) return 0;
-  return static_cast<size_t>(2 * kStreams) * 32 * (a.head_dim + 2) * sizeof(float);
+  const size_t floats = a.head_dim + 2;
+  if (streams_keys(a)) return static_cast<size_t>(2 * kStreams) * 32 * floats * sizeof(float);
+  const int most = key_split(a).most;
+  return most == 1 ? 0 : static_cast<size_t>(most) * a.heads * a.total_q * floats * sizeof(float);
 }
 
-bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
+bfp8_status launch_attention_forward(const AttentionArgs& given, void* workspace,
                                      size_t workspace_bytes, hipStream_t stream) {
-  if (streams_keys(a) && workspace != nullptr && workspace_bytes >= attention_forward_workspace(a)) {
+  AttentionArgs a = given;
+  const bool room = workspace != nullptr && workspace_bytes >= attention_forward_workspace(a);
+  if (room && streams_keys(a)) {
     Parts parts;
     parts.o = static_cast<float*>(workspace);
     parts.ml = reinterpret_cast<float2*>(parts.o + 2 * kStreams * 32 * a.head_dim);
@@ -566,18 +635,25 @@ bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
     if (st != BFP8_OK) return st;
     return launch(attention_join_kernel, dim3(kStreams - 1), dim3(kJoinThreads), stream, a, parts);
   }
-  // an upper bound on the tiles of all sequences: the lengths are on the device
-  int64_t tiles;
-  if (a.cu_q == nullptr)
-    tiles = a.batch * (((int64_t)a.total_q / a.batch * a.group + kRows - 1) / kRows);
-  else
-    tiles = ((int64_t)a.total_q * a.group + (int64_t)a.batch * (kRows - 1)) / kRows;
-  const int64_t blocks = tiles * a.kv_heads;
+  a.split_q = room ? key_split(a) : Split{1, 1};
+  const int64_t rows = (int64_t)a.heads * a.total_q;
+  if (a.split_q.most > 1) {
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + a.split_q.most * rows * a.head_dim);
+  }
+  const int64_t places = tile_bound(a.cu_q, a.batch, a.total_q, a.group, kRows);
+  const int64_t blocks = places * a.kv_heads * a.split_q.most;
   if (blocks == 0) return BFP8_OK;
   if (blocks >= (int64_t(1) << 31)) return BFP8_ERR_SHAPE;
   const dim3 grid(static_cast<unsigned>(blocks));
-  if (a.head_dim <= 64) return launch(attention_forward_kernel<64>, grid, dim3(64 * kWaves), stream, a);
-  return launch(attention_forward_kernel<128>, grid, dim3(64 * kWaves), stream, a);
+  const bfp8_status st =
+      a.head_dim <= 64
+          ? launch(attention_forward_kernel<64>, grid, dim3(64 * kWaves), stream, a, places)
+          : launch(attention_forward_kernel<128>, grid, dim3(64 * kWaves), stream, a, places);
+  if (st != BFP8_OK || a.split_q.most == 1) return st;
+  const int64_t join = rows / a.batch * (a.head_dim / 4) / 256 + 1;  // of an average sequence
+  return launch(attention_join_splits_kernel, dim3(static_cast<unsigned>(join), a.batch), dim3(256),
+                stream, a);
 }
 
 }  // namespace bfp8

@@ -50,14 +50,25 @@ __global__ __launch_bounds__(256) void attention_stats_kernel(AttentionArgs a) {
   }
 }
 
+// The accumulator of one row as float32 part number `row`.
+template <int DP>
+__device__ __forceinline__ void store_part(float* parts, int64_t row, const f32x4 (&acc)[DP / 16],
+                                           int dim, int lane) {
+#pragma unroll
+  for (int ct = 0; ct < DP / 16; ++ct) {
+    const int d = ct * 16 + 4 * (lane >> 4);
+    if (d < dim) *reinterpret_cast<f32x4*>(parts + row * dim + d) = acc[ct];
+  }
+}
+
 template <int DP>
 struct DqShared {
   uint8_t tiles[kStages][2][Tile<DP, kKeys, kWaves>::kBytes];  // K and V rows
 };
 
 template <int DP>
-__device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& shared, int n,
-                                        int g) {
+__device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& shared, int place,
+                                        int places, int g) {
   typedef Tile<DP, kKeys, kWaves> KTile;
   constexpr int kDims = DP / 16;   // 16-column results
   constexpr int kSteps = DP / 32;  // products of one 16x16 square
@@ -65,22 +76,26 @@ __device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& sh
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   Sequence s;
   int rank, tiles;
-  if (!find_tile<false>(a, a.group, kRows, n, s, rank, tiles)) return;
+  const int split = place / places;  // first every tile's first part
+  if (!find_tile<false>(a, a.group, kRows, place - split * places, s, rank, tiles)) return;
   const int row0 = rank * kRows;  // the last rows see the most keys
   const int rows = s.qn * a.group;
-  // last visible key of the workgroup's last row and of the wave's first and last
-  const int shift = a.causal ? s.kn - s.qn : s.kn;
-  const int block_lim = min((min(row0 + kRows, rows) - 1) / a.group + shift, s.kn - 1);
+  const int all = key_tiles(a, s, row0, kRows);
+  const int parts = a.split_q.parts(all);
+  if (split >= parts) return;
+  const int j0 = static_cast<int>(static_cast<int64_t>(all) * split / parts);
+  const int nj = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / parts);
+  // last key that the wave's last row sees, and its first
   const int wave_first = row0 + wave * 32;
-  const int wave_lim =
-      wave_first < rows ? min((min(wave_first + 32, rows) - 1) / a.group + shift, s.kn - 1) : -1;
-  const int wave_free = min(wave_first / a.group + shift, s.kn - 1);  // seen by every row
+  const int wave_lim = wave_first < rows ? last_key(a, s, min(wave_first + 32, rows) - 1) : -1;
+  const int wave_free = last_key(a, s, wave_first);  // seen by every row
 
   KTile kt, vt;
   kt.init(wave, lane, a.k.row, a.head_dim);
   vt.init(wave, lane, a.v.row, a.head_dim);
-  Walk kw(a.k, s.k0, g, a.head_dim), vw(a.v, s.k0, g, a.head_dim);
-  int left = s.kn, ahead = 0;  // keys from the walks' place on; stage of the next copies
+  Walk kw(a.k, (int64_t)s.k0 + j0 * kKeys, g, a.head_dim);
+  Walk vw(a.v, (int64_t)s.k0 + j0 * kKeys, g, a.head_dim);
+  int left = s.kn - j0 * kKeys, ahead = 0;  // keys from there on; stage of the next copies
   auto copy_tile = [&]() {     // tiles in their order; past the end zeros, counted as the others
     const int n = min(left, kKeys);
     kt.copy(lds[ahead][0], wave, kw.rows(n));
@@ -90,8 +105,7 @@ __device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& sh
     left -= kKeys;
     ahead = ahead == kStages - 1 ? 0 : ahead + 1;
   };
-  const int nj = block_lim < 0 ? 0 : block_lim / kKeys + 1;
-  if (nj > 0) {
+  if (nj > j0) {
 #pragma unroll
     for (int n = 0; n < kStages - 1; ++n) copy_tile();
   }
@@ -105,10 +119,9 @@ __device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& sh
   for (int n = 0; n < 2; ++n) {
     const int r = wave_first + 16 * n + (lane & 15);
     valid[n] = r < rows;
-    const int i = min(r, rows - 1) / a.group;
     h[n] = g * a.group + r % a.group;
-    lim[n] = min(i + shift, s.kn - 1);
-    at[n] = s.q0 + i;
+    lim[n] = last_key(a, s, min(r, rows - 1));
+    at[n] = s.q0 + min(r, rows - 1) / a.group;
     const uint16_t* qrow = a.q.p + at[n] * a.q.row + h[n] * a.q.head;
     const uint16_t* drow = a.dout.p + at[n] * a.dout.row + h[n] * a.dout.head;
 #pragma unroll
@@ -127,7 +140,7 @@ __device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& sh
 
   f32x4 acc[2][kDims] = {};
   int stage = 0;
-  for (int j = 0; j < nj; ++j) {
+  for (int j = j0; j < nj; ++j) {
     wait_copies<2 * (kStages - 2) * KTile::kCopies>();  // later tiles' may still be under way
     __syncthreads();
     copy_tile();
@@ -216,11 +229,17 @@ __device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& sh
     }
   }
   wait_copies<0>();  // no copy may land after the workgroup has given up its LDS
+  const AttentionArgs end = late_args();
 #pragma unroll
-  for (int n = 0; n < 2; ++n)
-    if (valid[n])
-      store_row<DP>(a.dq.p + at[n] * a.dq.row + h[n] * a.dq.head, acc[n], a.scale, a.head_dim,
-                    lane);
+  for (int n = 0; n < 2; ++n) {
+    if (!valid[n]) continue;
+    if (parts > 1)
+      store_part<DP>(end.part_dq, ((int64_t)split * end.heads + h[n]) * end.total_q + at[n], acc[n],
+                     end.head_dim, lane);
+    else
+      store_row<DP>(end.dq.p + at[n] * end.dq.row + h[n] * end.dq.head, acc[n], end.scale,
+                    end.head_dim, lane);
+  }
 }
 
 template <int DP>
@@ -233,8 +252,8 @@ struct DkdvShared {
 };
 
 template <int DP>
-__device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>& shared, int n0,
-                                          int g) {
+__device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>& shared,
+                                          int place, int places, int g) {
   typedef typename DkdvShared<DP>::QTile QTile;
   typedef typename DkdvShared<DP>::VTile VTile;
   constexpr int kDims = DP / 16;   // 16-column results
@@ -246,20 +265,28 @@ __device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>
   const int half = wave / kKeyWaves, kw = wave % kKeyWaves;
   Sequence s;
   int rank, tiles;
-  if (!find_tile<true>(a, 1, kKeyRows, n0, s, rank, tiles)) return;
+  const int split = place / places;  // first every tile's first part
+  if (!find_tile<true>(a, 1, kKeyRows, place - split * places, s, rank, tiles)) return;
   const int row0 = (tiles - 1 - rank) * kKeyRows;  // the first keys are seen by the most queries
   const int key0 = row0 + kw * 32;                 // the wave's first key
+  // squares of queries, head after head, of which this part's: n0 .. total - 1
+  // (an even n0: the halves take them in turn)
+  int per_head;
+  const int first = first_square(a, s, row0, per_head);
+  const int pairs = (per_head * a.group + 1) / 2;
+  const int parts = a.split_k.parts(pairs);
+  if (split >= parts) return;
+  const int n0 = 2 * static_cast<int>(static_cast<int64_t>(pairs) * split / parts);
+  const int total = min(2 * static_cast<int>(static_cast<int64_t>(pairs) * (split + 1) / parts),
+                        per_head * a.group);
+  // query i sees keys up to i + kn - qn: key j is first seen by query j + back
+  const int back = a.causal ? s.qn - s.kn : -s.kn;
   {
     VTile vt;
     vt.init(wave, lane, a.v.row, a.head_dim);
     const Walk vw(a.v, (int64_t)s.k0 + row0, g, a.head_dim);
     vt.copy(vlds, wave, vw.rows(min(s.kn - row0, kKeyRows)));
   }
-  // query i sees keys up to i + kn - qn: key j is first seen by query j + back
-  const int back = a.causal ? s.qn - s.kn : -s.kn;
-  const int first = row0 < s.kn ? max(row0 + back, 0) & ~31 : s.qn;
-  const int per_head = first < s.qn ? (s.qn - first + 31) / 32 : 0;
-  const int total = per_head * a.group;  // squares of queries, head after head
   const int wave_first = key0 + back;
   // first query of no masking: the one that sees the wave's last key, or none
   // if some of its keys are past the used length and must vanish
@@ -291,8 +318,15 @@ __device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>
         left += per_head * 32;
       }
   };
-  if (half == 1 && total > 0) pass(1);
-  int copied = half;
+  if (n0 > 0) {
+    const int heads = n0 / per_head, squares = n0 - heads * per_head;
+    qw.at += heads * a.q.head * 2;
+    dw.at += heads * a.dout.head * 2;
+    stat_at += (int64_t)heads * a.total_q * 4;
+    pass(squares);
+  }
+  if (half == 1 && total > n0) pass(1);
+  int copied = n0 + half;
   int ahead = 0;  // stage of the next copies
   auto copy_square = [&]() {  // past the last: zeros, counted as the others
     const int rows = copied < total ? min(left, 32) : 0;
@@ -304,7 +338,7 @@ __device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>
     copied += 2;  // the halves take squares in turn
     pass(2);
   };
-  if (total > 0) {
+  if (total > n0) {
     copy_square();
     copy_square();
   }
@@ -328,9 +362,9 @@ __device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>
   wait_copies<0>();  // and the loads of k
 
   f32x4 dk[2][kDims] = {}, dv[2][kDims] = {};
-  int at = per_head == 1 ? 0 : half;  // this half's square of its head
+  int at = total > n0 ? (n0 + half) % per_head : 0;  // this half's square of its head
   int next = 0;
-  for (int n = 0; n < total; n += 2) {
+  for (int n = n0; n < total; n += 2) {
     // the next square's copies may still be under way
     if (kw < 2) wait_copies<2 * QTile::kCopies + 1>();
     else wait_copies<2 * QTile::kCopies>();
@@ -455,62 +489,165 @@ __device__ __forceinline__ void dkdv_tile(const AttentionArgs& a, DkdvShared<DP>
       else dk[n][ct] += add;
     }
   }
+  const AttentionArgs end = late_args();
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     if (!mine[n]) continue;
-    if (half == 0)
-      store_row<DP>(a.dv.p + krow[n] * a.dv.row + g * a.dv.head, dv[n], 1.0f, a.head_dim, lane);
+    if (parts > 1)
+      store_part<DP>(half == 0 ? end.part_dv : end.part_dk,
+                     ((int64_t)split * end.kv_heads + g) * end.total_k + krow[n],
+                     half == 0 ? dv[n] : dk[n], end.head_dim, lane);
+    else if (half == 0)
+      store_row<DP>(end.dv.p + krow[n] * end.dv.row + g * end.dv.head, dv[n], 1.0f, end.head_dim,
+                    lane);
     else
-      store_row<DP>(a.dk.p + krow[n] * a.dk.row + g * a.dk.head, dk[n], a.scale, a.head_dim, lane);
+      store_row<DP>(end.dk.p + krow[n] * end.dk.row + g * end.dk.head, dk[n], end.scale,
+                    end.head_dim, lane);
   }
 }
 
-// Both kinds of tiles in one launch, so that neither waits for the other's
-// last workgroups: of every total places, q_tiles are dq tiles, evenly spread
-// (each kind's come by descending work).  The kv head changes fastest, which
-// puts all tiles of a head on one XCD where the heads are a multiple of 8.
+// Both kinds of tiles in one launch, so that the second kind's workgroups start
+// where the first kind's long ones still run.  Not interleaved: workgroups of
+// one kind that run together share the rows they read through their XCD's L2
+// (dq and dkdv tiles in turn took 11 % longer at 4 x 4096 and 1 x 16384), and
+// dq first took 2 % longer.  The kv head changes fastest, which puts all tiles
+// of a head on one XCD where the heads are a multiple of 8.
 template <int DP>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_backward_kernel(AttentionArgs a,
-                                                                           unsigned q_tiles,
-                                                                           unsigned total) {
+                                                                           int k_tiles,
+                                                                           int q_tiles) {
   union Shared {
     DqShared<DP> dq;
     DkdvShared<DP> dkdv;
   };
   __shared__ __attribute__((aligned(1024))) Shared shared;
   const int g = blockIdx.x % a.kv_heads;
-  const unsigned place = blockIdx.x / a.kv_heads;
-  if (place < total - q_tiles)
-    dkdv_tile<DP>(a, shared.dkdv, place, g);
+  const int place = blockIdx.x / a.kv_heads;
+  const int k_places = k_tiles * a.split_k.most;
+  if (place < k_places)
+    dkdv_tile<DP>(a, shared.dkdv, place, k_tiles, g);
   else
-    dq_tile<DP>(a, shared.dq, place - (total - q_tiles), g);
+    dq_tile<DP>(a, shared.dq, place - k_places, q_tiles, g);
 }
 
-// An upper bound on the tiles of all sequences, whose lengths are on the device.
-int64_t tile_bound(const int32_t* cu, int64_t batch, int64_t total, int64_t mult, int64_t unit) {
-  if (cu == nullptr) return batch * ((total / batch * mult + unit - 1) / unit);
-  return (total * mult + batch * (unit - 1)) / unit;
+// Adds the parts of the gradients' rows that have several, in their order: one
+// thread per 4 values of a row of sequence blockIdx.y, whole rows to a workgroup.
+__global__ __launch_bounds__(256) void attention_sum_kernel(AttentionArgs a) {
+  const unsigned per_row = a.head_dim / 4, slots = 256 / per_row;
+  const unsigned slot = threadIdx.x / per_row;
+  const int d = (threadIdx.x - slot * per_row) * 4;
+  if (slot >= slots) return;
+  const Sequence s = load_sequence(a, blockIdx.y);
+  auto sum = [&](const float* p, int64_t stride, int parts, const Heads& out, int64_t t, unsigned h,
+                 float mul) {
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) x += *reinterpret_cast<const f32x4*>(p + k * stride);
+    u32x2 w;
+    w.x = pack_bf16x2(x[0] * mul, x[1] * mul);
+    w.y = pack_bf16x2(x[2] * mul, x[3] * mul);
+    *reinterpret_cast<u32x2*>(out.p + t * out.row + h * out.head + d) = w;
+  };
+  if (a.split_q.most > 1) {
+    const unsigned heads = a.heads;
+    const int64_t stride = (int64_t)a.heads * a.total_q * a.head_dim;
+    for (unsigned r = blockIdx.x * slots + slot; r < s.qn * heads; r += gridDim.x * slots) {
+      const unsigned i = r / heads, h = r - i * heads;
+      const int tile = static_cast<int>(i * a.group + h % a.group) / kRows;
+      const int parts = a.split_q.parts(key_tiles(a, s, tile * kRows, kRows));
+      if (parts == 1) continue;
+      const int64_t t = s.q0 + i;
+      sum(a.part_dq + ((int64_t)h * a.total_q + t) * a.head_dim + d, stride, parts, a.dq, t, h,
+          a.scale);
+    }
+  }
+  if (a.split_k.most > 1) {
+    const unsigned heads = a.kv_heads;
+    const int64_t stride = (int64_t)a.kv_heads * a.total_k * a.head_dim;
+    for (unsigned r = blockIdx.x * slots + slot; r < s.ka * heads; r += gridDim.x * slots) {
+      const unsigned j = r / heads, g = r - j * heads;
+      int per_head;
+      first_square(a, s, static_cast<int>(j) / kKeyRows * kKeyRows, per_head);
+      const int parts = a.split_k.parts((per_head * a.group + 1) / 2);
+      if (parts == 1) continue;
+      const int64_t t = s.k0 + j, at = ((int64_t)g * a.total_k + t) * a.head_dim + d;
+      sum(a.part_dk + at, stride, parts, a.dk, t, g, a.scale);
+      sum(a.part_dv + at, stride, parts, a.dv, t, g, 1.0f);
+    }
+  }
+}
+
+struct BackwardPlan {
+  int64_t q_tiles, k_tiles;
+  Split split_q, split_k;
+};
+
+// A dq tile takes about 1.5 us for 64 keys, a dkdv tile 1.5 us for 64 queries
+// of one head (a pair of squares).
+BackwardPlan backward_plan(const AttentionArgs& a) {
+  BackwardPlan p{0, 0, Split{1, 1}, Split{1, 1}};
+  if (a.batch == 0) return p;
+  p.q_tiles = tile_bound(a.cu_q, a.batch, a.total_q, a.group, kRows);
+  p.k_tiles = tile_bound(a.cu_k, a.batch, a.total_k, 1, kKeyRows);
+  if (a.total_q == 0 || a.total_k == 0 || a.batch > 65535) return p;
+  if ((int64_t)a.total_q * a.heads >= (int64_t(1) << 31) ||  // rows counted in 32 bits
+      (int64_t)a.total_k * a.kv_heads >= (int64_t(1) << 31))
+    return p;
+  const Lengths keys(a.cu_k, a.batch, a.total_k), queries(a.cu_q, a.batch, a.total_q);
+  const double step = 1.5, cus = 256;
+  const double balanced = (p.q_tiles * keys.own + p.k_tiles * queries.own * a.group) * a.kv_heads *
+                          step / 64 * (a.causal ? 0.5 : 1.0) / cus;
+  p.split_q = choose_split(keys.longest * step / 64, balanced, step,
+                           static_cast<double>(a.total_q) * a.heads * a.head_dim);
+  p.split_k = choose_split(queries.longest * a.group * step / 64, balanced, step,
+                           2.0 * a.total_k * a.kv_heads * a.head_dim);
+  return p;
 }
 
 }  // namespace
 
-bfp8_status launch_attention_backward(const AttentionArgs& a, hipStream_t stream) {
-  const int64_t q_tiles = tile_bound(a.cu_q, a.batch, a.total_q, a.group, kRows);
-  const int64_t total = q_tiles + tile_bound(a.cu_k, a.batch, a.total_k, 1, kKeyRows);
-  const int64_t blocks = total * a.kv_heads;
-  const int64_t stat_blocks = ((int64_t)a.total_q * a.heads + 15) / 16;
+size_t attention_backward_workspace(const AttentionArgs& a) {
+  const BackwardPlan p = backward_plan(a);
+  const size_t q_rows = static_cast<size_t>(a.heads) * a.total_q;
+  const size_t k_rows = static_cast<size_t>(a.kv_heads) * a.total_k;
+  size_t floats = 2 * q_rows;
+  if (p.split_q.most > 1 || p.split_k.most > 1) floats = (floats + 3) / 4 * 4;  // 16 bytes
+  if (p.split_q.most > 1) floats += p.split_q.most * q_rows * a.head_dim;
+  if (p.split_k.most > 1) floats += 2 * p.split_k.most * k_rows * a.head_dim;
+  return floats * sizeof(float);
+}
+
+bfp8_status launch_attention_backward(AttentionArgs a, void* workspace, hipStream_t stream) {
+  const BackwardPlan p = backward_plan(a);
+  const int64_t q_rows = (int64_t)a.heads * a.total_q, k_rows = (int64_t)a.kv_heads * a.total_k;
+  a.split_q = p.split_q;
+  a.split_k = p.split_k;
+  a.lse2 = static_cast<float*>(workspace);
+  a.delta = a.lse2 + q_rows;
+  a.part_dq = a.lse2 + (2 * q_rows + 3) / 4 * 4;
+  a.part_dk = a.part_dq + (a.split_q.most > 1 ? a.split_q.most * q_rows * a.head_dim : 0);
+  a.part_dv = a.part_dk + a.split_k.most * k_rows * a.head_dim;
+  const int64_t blocks =
+      (p.k_tiles * a.split_k.most + p.q_tiles * a.split_q.most) * a.kv_heads;
+  const int64_t stat_blocks = (q_rows + 15) / 16;
   if (blocks >= (int64_t(1) << 31) || stat_blocks >= (int64_t(1) << 31)) return BFP8_ERR_SHAPE;
-  if (stat_blocks > 0) {
-    const bfp8_status st = launch(attention_stats_kernel, dim3(static_cast<unsigned>(stat_blocks)),
-                                  dim3(256), stream, a);
-    if (st != BFP8_OK) return st;
-  }
-  if (blocks == 0) return BFP8_OK;
+  bfp8_status st = BFP8_OK;
+  if (stat_blocks > 0)
+    st = launch(attention_stats_kernel, dim3(static_cast<unsigned>(stat_blocks)), dim3(256), stream,
+                a);
+  if (st != BFP8_OK || blocks == 0) return st;
   const dim3 grid(static_cast<unsigned>(blocks));
-  return a.head_dim <= 64
-             ? launch(attention_backward_kernel<64>, grid, dim3(64 * kWaves), stream, a, q_tiles, total)
-             : launch(attention_backward_kernel<128>, grid, dim3(64 * kWaves), stream, a, q_tiles,
-                      total);
+  st = a.head_dim <= 64 ? launch(attention_backward_kernel<64>, grid, dim3(64 * kWaves), stream, a,
+                                 p.k_tiles, p.q_tiles)
+                        : launch(attention_backward_kernel<128>, grid, dim3(64 * kWaves), stream, a,
+                                 p.k_tiles, p.q_tiles);
+  if (st != BFP8_OK || (a.split_q.most == 1 && a.split_k.most == 1)) return st;
+  // workgroups for an average sequence's rows
+  const int64_t split_rows =
+      std::max(a.split_q.most > 1 ? q_rows : 0, a.split_k.most > 1 ? k_rows : 0);
+  const int64_t sum = split_rows / a.batch * (a.head_dim / 4) / 256 + 1;
+  return launch(attention_sum_kernel, dim3(static_cast<unsigned>(sum), a.batch), dim3(256), stream,
+                a);
 }
 
 }  // namespace bfp8

@@ -221,6 +221,54 @@ def test_streamed_keys(name):
     assert torch.equal(o[:-2], o2[:-2]) and torch.equal(lse[:, :-2], lse2[:, :-2])
 
 
+SPLIT = {
+    # name: (q lens, k rows, used keys or None, heads, kv heads, head size, causal)
+    "one_long": ([2000], [2000], None, 2, 1, 128, True),
+    "ragged": ([30, 2600, 0, 700, 1], [30, 2600, 0, 700, 1], None, 2, 1, 64, True),
+    "ragged_one_head": ([0, 2600, 30], [0, 2600, 30], None, 1, 1, 64, True),
+    "cross": ([1900], [2500], None, 3, 1, 40, False),
+    "empty_rows": ([2600], [2100], None, 2, 2, 128, True),
+    "part_used": ([1500, 100], [2600, 2600], [2500, 1], 4, 1, 80, True),
+}
+
+
+@pytest.mark.parametrize("name", list(SPLIT))
+def test_split_tiles(name):
+    """Few workgroups over long sequences: long tiles' sums are split over
+    several workgroups and added later, short ones are not, in one call."""
+    q_lens, k_rows, used, H, KV, D, causal = SPLIT[name]
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    T, S = sum(q_lens) + 3, sum(k_rows) + 2
+    q, k, v = tensors(T, S, H, KV, D, "dense", gen)
+    do = torch.randn(q.shape, device="cuda", generator=gen).to(torch.bfloat16)
+    cq, ck = cu(q_lens), cu(k_rows)
+    args = (q, k, v, gpu_ints(cq), gpu_ints(ck), gpu_ints(used) if used else None)
+    # "ragged" splits the gradients alone
+    assert (bfp8.attention_workspace_bytes(*args, causal=causal) > 0) == (name != "ragged")
+    assert bfp8.attention_workspace_bytes(*args, causal=causal, backward=True) > 8 * H * T + 16
+    o = torch.full((T, H, D), 7.0, device="cuda", dtype=torch.bfloat16)
+    lse = torch.full((H, T), 7.0, device="cuda")
+    bfp8.attention_forward(*args, causal=causal, out=o, lse=lse)
+    assert (o[-3:] == 7).all() and (lse[:, -3:] == 7).all()
+    ref_args = (cq, ck, used, causal, D ** -0.5)
+    want, wl, ob, lb = ref.attention(f64(q), f64(k), f64(v), *ref_args)
+    within(o, want, ob, name + " o")
+    within(lse, wl, lb, name + " lse")
+    whole, _ = bfp8.attention_forward(*args, causal=causal,
+                                      workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    within(whole, want, ob, name + " o without a workspace")
+    d = [torch.full(t.shape, 7.0, device="cuda", dtype=torch.bfloat16) for t in (q, k, v)]
+    grads = bfp8.attention_backward(do, q, k, v, o, lse, *args[3:], causal=causal, dq=d[0], dk=d[1],
+                                    dv=d[2])
+    assert (d[0][-3:] == 7).all() and (d[1][-2:] == 7).all() and (d[2][-2:] == 7).all()
+    ref_g = ref.attention_gradient(f64(do), f64(q), f64(k), f64(v), *ref_args)
+    for i, n in enumerate(("dq", "dk", "dv")):
+        within(grads[i], ref_g[i], ref_g[3 + i], f"{name} {n}")
+    again = bfp8.attention_backward(do, q, k, v, o, lse, *args[3:], causal=causal)
+    for a, b, rows in zip(grads, again, (T - 3, S - 2, S - 2)):
+        assert torch.equal(a[:rows], b[:rows])
+
+
 def test_scores_of_any_size():
     """Scores in the thousands (a running maximum that keeps growing, and one
     that starts at its largest), the same result for keys in either order."""

@@ -13,8 +13,9 @@ from blockwise_fp8_gemm_bfp8_amd import build as bfp8_build
 
 KERNELS = {"attention.hip": ["attention_forward_kernelILi64", "attention_forward_kernelILi128",
                              "attention_stream_kernelILi64", "attention_stream_kernelILi128",
-                             "attention_join_kernel"],
-           "attention_bwd.hip": ["attention_stats_kernel", "attention_backward_kernelILi64",
+                             "attention_join_kernel", "attention_join_splits_kernel"],
+           "attention_bwd.hip": ["attention_stats_kernel", "attention_sum_kernel",
+                                 "attention_backward_kernelILi64",
                                  "attention_backward_kernelILi128"],
            "rope.hip": ["rope_table_kernel", "rope_kernelItLi8ELb0", "rope_kernelItLi4ELb1",
                         "rope_kernelIfLi4ELb0", "rope_kernelIfLi2ELb1"]}
