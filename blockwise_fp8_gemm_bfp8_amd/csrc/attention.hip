@@ -1,19 +1,32 @@
 // Attention forward for gfx950: O = softmax(scale Q K^T) V and its
 // log-sum-exp, one pass over the keys with a running maximum and sum.
 //
-// All products are turned so that a lane owns one query row throughout:
+// All products are turned so that a lane owns its query rows throughout:
 //   S^T [key][query] = K Q^T   (K rows from LDS, Q rows in registers)
 //   O^T [dim][query] = V^T P^T (V columns by transposing LDS reads, P^T the
 //                               accumulator of S^T rounded to bf16 in place)
-// With v_mfma_f32_32x32x16_bf16 lane l holds query l % 32 of both results, so
-// the row maximum and sum are taken over registers (and one exchange with
-// lane l ^ 32), the rescaling factor is one register, and P never moves
-// between lanes.
+// With v_mfma_f32_16x16x32_bf16 lane l holds query l % 16 of both results, so
+// the row maximum and sum are taken over registers and then over the lanes l,
+// l ^ 16, l ^ 32, l ^ 48, the rescaling factor is one register, and P never
+// moves between lanes.  P is rounded to bf16 for its product only (an error
+// like the output's own rounding); its sum is of the float32 values.
 //
 // A workgroup of 8 waves takes 256 rows of one kv head, a row being one
 // (query, head of the group) pair: the heads that share keys share their
-// tiles, and few queries fill more of a tile.  Each wave owns 32 rows; tiles
-// of 64 keys pass through two LDS stages, filled by LDS-DMA one tile ahead.
+// tiles, and few queries fill more of a tile.  Each wave owns 32 rows, two
+// sets of 16; tiles of 64 keys pass through three LDS stages, filled by
+// LDS-DMA two tiles ahead with one barrier a tile.
+//
+// What bounds it: the matrix cores and, above that, the card's power.  16 query
+// and 8 key/value heads of 128, causal: 4 sequences of 4096 take 252 us (1090
+// TFLOP/s), one of 16384 takes 897 us (1230 TFLOP/s), 13 sequences of 1 to 2417
+// tokens, 8274 in all, 67 us (the last workgroups' time, and the first tiles'
+// latency).  The same long sequence of zeros, which draws less power, takes 726
+// us.  Of 967 us, before its last steps, it took 13 % less without the softmax's
+// arithmetic, 12 % without LDS reads, 4 % without copies and barriers: none of
+// them alone bounds it.  Workgroups of 4 waves, two to a CU, and half of the
+// waves starting half a tile late were within 1 % or slower; 64 rows a wave
+// does not fit the registers.
 #include "attention.h"
 
 namespace bfp8 {
@@ -51,7 +64,8 @@ __device__ __forceinline__ void raise_maxima(float either, float (&m)[2], float 
 }
 
 template <int DP>
-__global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(AttentionArgs a, int places) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(AttentionArgs a,
+                                                                          int places) {
   typedef Tile<DP, kKeys, kWaves> KTile;
   constexpr int kDims = DP / 16;   // 16-column results
   constexpr int kSteps = DP / 32;  // products of one 16x16 square
@@ -225,7 +239,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
   }
 }
 
-// Joins the parts of each row that has several, in their order: one thread per 4
+// Joins the parts of each row that has several, in their order (memory-bound:
+// the parts once, the output once): one thread per 4
 // values of one row of sequence blockIdx.y, whole rows to a workgroup.
 __global__ __launch_bounds__(256) void attention_join_splits_kernel(AttentionArgs a) {
   const Sequence s = load_sequence(a, blockIdx.y);
@@ -276,6 +291,12 @@ __global__ __launch_bounds__(256) void attention_join_splits_kernel(AttentionArg
 // Where a stretch ends inside a segment (one kv head's 32 rows), its float32
 // results go to the workspace, and a second kernel joins a segment's parts in
 // their order.
+//
+// What bounds it: latency and the reading of K and V.  16 sequences of 1 query
+// over 1 to 4096 cached keys, 16/8 heads of 128 (103 MB of K and V): 22 us, 4.7
+// TB/s, and 8 us to join; a copy's rate would take 20.  A workgroup of 4 waves
+// per (sequence, head, stretch) took 65 us for both, one persistent workgroup
+// of joined waves per CU 88.
 constexpr int kStreams = 1024;  // one on each SIMD (its registers leave no room for two)
 constexpr int kMinShare = 3;    // line units of a stretch at least
 // A segment counts for so many tiles more than it has, for the latency of its
@@ -512,7 +533,8 @@ __global__ __launch_bounds__(64, 1) void attention_stream_kernel(AttentionArgs a
 // segment and is the first that does, it joins that segment.  16 rows at a
 // time; where there are fewer, several groups of threads share a row's parts.
 constexpr int kJoinThreads = 512;
-__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionArgs a, Parts parts) {
+__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionArgs a,
+                                                                      Parts parts) {
   __shared__ f32x4 other_o[kJoinThreads];
   __shared__ float2 other_ml[kJoinThreads];
   int length, at;
@@ -599,6 +621,8 @@ bool streams_keys(const AttentionArgs& a) {
 }
 
 // The split of the row tiles' keys; a tile of 64 keys takes about 1.1 us.
+// Measured, without / with the parts: one sequence of 4463, one head of 64,
+// causal, 84 / 31 us; 12545 tokens in 9 sequences, 4/2 heads of 64, 47 / 38 us.
 Split key_split(const AttentionArgs& a) {
   if (a.total_q == 0 || a.total_k == 0 || a.batch > 65535) return Split{1, 1};
   if ((int64_t)a.total_q * a.heads >= (int64_t(1) << 31)) return Split{1, 1};  // rows in 32 bits

@@ -129,9 +129,9 @@ typedef struct {
  * for an invalid shape. */
 size_t bfp8_attention_workspace_bytes(const bfp8_attention_shape* shape, int backward);
 
-/* o and lse from q, k, v.  The workspace holds partial results where the keys
- * of few query rows are split over workgroups; smaller or NULL: no split (same
- * contract, slower). */
+/* o and lse from q, k, v.  The workspace holds float32 partial results where the
+ * keys of few query rows are split over workgroups; smaller or NULL: no split
+ * (same contract, slower). */
 bfp8_status bfp8_attention_forward(const bfp8_attention_shape* shape, bfp8_heads q, bfp8_heads k,
                                    bfp8_heads v, bfp8_heads_out o, float* lse, void* workspace,
                                    size_t workspace_bytes, hipStream_t stream);
@@ -139,8 +139,9 @@ bfp8_status bfp8_attention_forward(const bfp8_attention_shape* shape, bfp8_heads
 /* dq, dk, dv from the forward pass's inputs, its o and lse, and the gradient
  * dout of o; the probabilities are recomputed from lse.  Rows of dk and dv
  * past a sequence's used length become zero; rows that belong to no sequence
- * are not written.  The workspace (bfp8_attention_workspace_bytes(shape, 1))
- * is required: BFP8_ERR_WORKSPACE if it is NULL or smaller.  dq, dk and dv
+ * are not written.  The workspace (bfp8_attention_workspace_bytes(shape, 1):
+ * two float32 values a row and head, and partial gradients where few workgroups
+ * meet long sequences) is required: BFP8_ERR_WORKSPACE if it is NULL or smaller.  dq, dk and dv
  * must not overlap each other or the inputs. */
 bfp8_status bfp8_attention_backward(const bfp8_attention_shape* shape, bfp8_heads q, bfp8_heads k,
                                     bfp8_heads v, bfp8_heads o, const float* lse, bfp8_heads dout,
