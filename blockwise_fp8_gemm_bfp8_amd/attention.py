@@ -33,9 +33,9 @@ def _heads(t: torch.Tensor, name: str, dtypes, device: int = None, shape=None):
     """Check a tensor of heads; returns its device, shape and bfp8_heads.
     The strides of axes with one entry do not matter and take the values of a
     dense tensor."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
     at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must be a device tensor")
     if device is not None and at != device:
         raise ValueError(f"{name} must be on device {device}, got {at}")
     size = t.shape
@@ -56,11 +56,21 @@ def _heads(t: torch.Tensor, name: str, dtypes, device: int = None, shape=None):
     return at, size, Heads(t.data_ptr(), row, head)
 
 
+def _result(out, like: torch.Tensor, name: str, device: int, size):
+    """The tensor of a result that has `like`'s shape (`size`) and dtype, a new
+    dense one if `out` is None, and its bfp8_heads."""
+    if out is None:
+        out = torch.empty_like(like, memory_format=torch.contiguous_format)
+        _, H, D = size
+        return out, Heads(out.data_ptr(), max(H, 1) * D, D)
+    return out, _heads(out, name, (like.dtype,), device, size)[2]
+
+
 def _check_i32(t, name: str, n: int, device: int):
     if t is None:
         return
-    if (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()
-            or not t.is_cuda or t.get_device() != device):
+    if (t.get_device() != device or t.dtype is not torch.int32 or t.dim() != 1
+            or not t.is_contiguous()):
         raise ValueError(f"{name} must be a dense 1-D int32 tensor on device {device}")
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
@@ -103,13 +113,11 @@ def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor = None,
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
     device, size, xh = _heads(x, "x", DTYPES)
     if (table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32
-            or not table.is_contiguous() or not table.is_cuda or table.get_device() != device):
+            or not table.is_contiguous() or table.get_device() != device):
         raise ValueError(f"table must be a dense float32 [length][rot_dim/2][2] on device {device}")
     T, H, D = size
     _check_i32(positions, "positions", T, device)
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    _, _, yh = _heads(out, "out", (x.dtype,), device, size)
+    out, yh = _result(out, x, "out", device, size)
     length, half, _ = table.shape
     _check("bfp8_rope", lib().bfp8_rope(
         xh.data, xh.row, xh.head, yh.data, yh.row, yh.head, DTYPES[x.dtype], T, H, D, 2 * half,
@@ -126,7 +134,7 @@ _INVALID = ctypes.c_size_t(-1).value  # bfp8_attention_workspace_bytes of an inv
 
 def _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale):
     """Check the inputs; returns (device, bfp8_attention_shape, q, k, v as
-    bfp8_heads)."""
+    bfp8_heads, the shapes of q and of k)."""
     device, qs, qh = _heads(q, "q", _BF16)
     _, ks, kh = _heads(k, "k", _BF16, device)
     _, _, vh = _heads(v, "v", _BF16, device, ks)
@@ -144,7 +152,7 @@ def _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale):
         scale = 1.0 / math.sqrt(D) if D else 1.0
     shape = AttentionShape(batch, Tq, Tk, _pointer(cu_q), _pointer(cu_k), _pointer(k_lens), H, KV,
                            D, int(causal), scale)
-    return device, shape, qh, kh, vh
+    return device, shape, qh, kh, vh, qs, ks
 
 
 def attention_workspace_bytes(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = None,
@@ -164,20 +172,14 @@ def _workspace(shape, backward, given, like):
         n = lib().bfp8_attention_workspace_bytes(ctypes.byref(shape), backward)
         if n == 0 or n == _INVALID:  # the call itself reports what is wrong with a shape
             return None, 0
-        given = like.new_empty((n,), dtype=torch.uint8)
+        given = torch.empty(n, dtype=torch.uint8, device=like.device)
         return given, n
     return given, given.numel() * given.element_size()
 
 
-def _output(out, like):
-    if out is None:
-        return torch.empty_like(like, memory_format=torch.contiguous_format)
-    return out
-
-
 def _check_lse(lse, heads, tokens, device: int):
     if (lse.shape != (heads, tokens) or lse.dtype != torch.float32 or not lse.is_contiguous()
-            or not lse.is_cuda or lse.get_device() != device):
+            or lse.get_device() != device):
         raise ValueError(f"lse must be a dense float32 [{heads}][{tokens}] on device {device}")
 
 
@@ -193,11 +195,10 @@ def attention_forward(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = N
     causal      query i of n sees keys 0 .. i + m - n of m.
     scale       default 1/sqrt(D).
     A workspace is allocated when the library asks for one and none is given."""
-    device, s, qh, kh, vh = _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
-    out = _output(out, q)
-    _, _, oh = _heads(out, "out", _BF16, device, q.shape)
+    device, s, qh, kh, vh, qs, _ = _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
+    out, oh = _result(out, q, "out", device, qs)
     if lse is None:
-        lse = q.new_empty((s.heads, s.total_q), dtype=torch.float32)
+        lse = torch.empty(qs[1], qs[0], dtype=torch.float32, device=q.device)
     else:
         _check_lse(lse, s.heads, s.total_q, device)
     workspace, nbytes = _workspace(s, 0, workspace, q)
@@ -214,14 +215,13 @@ def attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, k_lens=Non
     """Gradients (dq, dk, dv) of attention_forward for the gradient `dout` of
     its `out`, given the `lse` it returned and the same sequences, mask and
     scale; see bfp8_attention_backward."""
-    device, s, qh, kh, vh = _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
-    _, _, oh = _heads(out, "out", _BF16, device, q.shape)
-    _, _, doh = _heads(dout, "dout", _BF16, device, q.shape)
+    device, s, qh, kh, vh, qs, ks = _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
+    _, _, oh = _heads(out, "out", _BF16, device, qs)
+    _, _, doh = _heads(dout, "dout", _BF16, device, qs)
     _check_lse(lse, s.heads, s.total_q, device)
-    dq, dk, dv = _output(dq, q), _output(dk, k), _output(dv, v)
-    _, _, dqh = _heads(dq, "dq", _BF16, device, q.shape)
-    _, _, dkh = _heads(dk, "dk", _BF16, device, k.shape)
-    _, _, dvh = _heads(dv, "dv", _BF16, device, k.shape)
+    dq, dqh = _result(dq, q, "dq", device, qs)
+    dk, dkh = _result(dk, k, "dk", device, ks)
+    dv, dvh = _result(dv, v, "dv", device, ks)
     workspace, nbytes = _workspace(s, 1, workspace, q)
     _check("bfp8_attention_backward", lib().bfp8_attention_backward(
         ctypes.byref(s), qh, kh, vh, oh, lse.data_ptr(), doh, dqh, dkh, dvh, _pointer(workspace),
