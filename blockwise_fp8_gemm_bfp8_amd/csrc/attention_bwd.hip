@@ -211,7 +211,8 @@ __device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& sh
             for (int e = 0; e < 4; ++e)
               if (key0 + 16 * k + acc_row(e, lane) > lim[n]) p[k][n][e] = -INFINITY;
       }
-      // dQ^T; the K rows of the next 32 keys are read meanwhile
+      // dQ^T; the K rows of the next 32 keys are read meanwhile.  Products begin
+      // after the first 24 instructions of dS (36 or 8: 1 % slower).
       bf16x8 ds[2];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -233,7 +234,7 @@ __device__ __forceinline__ void dq_tile(const AttentionArgs& a, DqShared<DP>& sh
 #pragma unroll
           for (int k = 0; k < 2; ++k) kf[ks][k] = KTile::rows(K, 32 + 16 * k, ks, lane);
       }
-      __builtin_amdgcn_sched_group_barrier(kSchedValu, 36, 1);
+      __builtin_amdgcn_sched_group_barrier(kSchedValu, 24, 1);
 #pragma unroll
       for (int i = 0; i < kDims; ++i) {
         __builtin_amdgcn_sched_group_barrier(kSchedMma, 2, 1);
