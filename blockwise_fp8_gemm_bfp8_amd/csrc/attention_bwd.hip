@@ -21,8 +21,11 @@
 // as long (310 us for the 225 us of 13 sequences, 8274 tokens in all).
 //
 // What bounds it: the matrix cores and the card's power.  16/8 heads of 128,
-// causal: 4 sequences of 4096 take 833 us (stats 30; 1210 TFLOP/s of the seven
-// products), one of 16384 takes 3.0 ms (1296), those 13 ragged sequences 220.
+// causal: 4 sequences of 4096 take 819 to 844 us (stats 30; 1196 TFLOP/s of the
+// seven products and more: cards differ), one of 16384 takes 2.9 to 3.1 ms
+// (1254), those 13 ragged sequences 208 to 222.  The loops alone do 1386 (dkdv)
+// and 1438 TFLOP/s (dq), as a large library product; the rest is the workgroups'
+// starts and ends, 8 to 9 us of each, and the XCDs' clocks, which differ.
 // Kept from the forward kernel's trials: three stages, 16x16x32 products.
 #include "attention.h"
 
