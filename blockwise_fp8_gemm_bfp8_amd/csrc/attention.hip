@@ -19,14 +19,15 @@
 //
 // What bounds it: the matrix cores and, above that, the card's power.  16 query
 // and 8 key/value heads of 128, causal: 4 sequences of 4096 take 250 to 262 us
-// (1068 TFLOP/s and more: cards differ), one of 16384 takes 897 to 954 us (1157),
-// 13 sequences of 1 to 2417 tokens, 8274 in all, 67 us (the longest workgroup:
-// 38 tiles of keys one after another where an even share is 29 a CU).  The same long sequence of zeros, which draws less power, takes 726
-// us.  Of 967 us, before its last steps, it took 13 % less without the softmax's
-// arithmetic, 12 % without LDS reads, 4 % without copies and barriers: none of
-// them alone bounds it.  Workgroups of 4 waves, two to a CU, and half of the
-// waves starting half a tile late were within 1 % or slower; 64 rows a wave
-// does not fit the registers.
+// (1068 TFLOP/s and more: cards differ), one of 16384 takes 897 to 954 us
+// (1157), 13 sequences of 1 to 2417 tokens, 8274 in all, 67 us (the longest
+// workgroup: 38 tiles of keys one after another where an even share is 29 a CU).
+// The same long sequence of zeros, which draws less power, takes 726 us.  Of 967
+// us, before its last steps, it took 13 % less without the softmax's arithmetic,
+// 12 % without LDS reads, 4 % without copies and barriers: none of them alone
+// bounds it.  Workgroups of 4 waves, two to a CU, and half of the waves starting
+// half a tile late were within 1 % or slower; 64 rows a wave does not fit the
+// registers.
 #include "attention.h"
 
 namespace bfp8 {
