@@ -31,8 +31,8 @@ def _stream_of(device: int):
 
 def _heads(t: torch.Tensor, name: str, dtypes, device: int = None, shape=None):
     """Check a tensor of heads; returns its device, shape and bfp8_heads.
-    The strides of axes with one entry do not matter and take the values of a
-    dense tensor."""
+    The strides of axes with one entry do not matter and are given as head_dim,
+    which every check passes whatever the other stride is."""
     at = t.get_device()
     if at < 0:
         raise ValueError(f"{name} must be a device tensor")
@@ -52,7 +52,7 @@ def _heads(t: torch.Tensor, name: str, dtypes, device: int = None, shape=None):
     if H <= 1:
         head = D
     if T <= 1:
-        row = max(H * head, D)
+        row = D
     return at, size, Heads(t.data_ptr(), row, head)
 
 
