@@ -183,9 +183,14 @@ def _check_lse(lse, heads, tokens, device: int):
         raise ValueError(f"lse must be a dense float32 [{heads}][{tokens}] on device {device}")
 
 
+# bfp8_attention_shape.clear
+_CLEAR_O, _CLEAR_LSE, _CLEAR_DQ, _CLEAR_DK, _CLEAR_DV = 1, 2, 4, 8, 16
+
+
 def attention_forward(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = None,
                       causal: bool = True, scale: float = None, out: torch.Tensor = None,
-                      lse: torch.Tensor = None, workspace: torch.Tensor = None):
+                      lse: torch.Tensor = None, workspace: torch.Tensor = None,
+                      zero_rest: bool = False):
     """Attention of q [Tq][H][D] over k, v [Tk][KV][D] (bfloat16, H a multiple
     of KV) -> (o [Tq][H][D], lse float32 [H][Tq]); see bfp8_attention_forward.
 
@@ -194,8 +199,13 @@ def attention_forward(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = N
     k_lens      int32 [batch]: used rows of each sequence's keys; None: all.
     causal      query i of n sees keys 0 .. i + m - n of m.
     scale       default 1/sqrt(D).
+    zero_rest   rows of no sequence (before cu_q[0], from cu_q[-1] on) become 0
+                (lse: -inf) in a given out and lse, too; they always do in
+                results that the call allocates.
     A workspace is allocated when the library asks for one and none is given."""
     device, s, qh, kh, vh, qs, _ = _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
+    s.clear = ((_CLEAR_O if out is None or zero_rest else 0)
+               | (_CLEAR_LSE if lse is None or zero_rest else 0))
     out, oh = _result(out, q, "out", device, qs)
     if lse is None:
         lse = torch.empty(qs[1], qs[0], dtype=torch.float32, device=q.device)
@@ -211,14 +221,18 @@ def attention_forward(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = N
 def attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, k_lens=None,
                        batch: int = None, causal: bool = True, scale: float = None,
                        dq: torch.Tensor = None, dk: torch.Tensor = None, dv: torch.Tensor = None,
-                       workspace: torch.Tensor = None):
+                       workspace: torch.Tensor = None, zero_rest: bool = False):
     """Gradients (dq, dk, dv) of attention_forward for the gradient `dout` of
     its `out`, given the `lse` it returned and the same sequences, mask and
-    scale; see bfp8_attention_backward."""
+    scale; see bfp8_attention_backward.  Rows of no sequence are zero in
+    gradients that the call allocates and, with `zero_rest`, in given ones."""
     device, s, qh, kh, vh, qs, ks = _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
     _, _, oh = _heads(out, "out", _BF16, device, qs)
     _, _, doh = _heads(dout, "dout", _BF16, device, qs)
     _check_lse(lse, s.heads, s.total_q, device)
+    s.clear = ((_CLEAR_DQ if dq is None or zero_rest else 0)
+               | (_CLEAR_DK if dk is None or zero_rest else 0)
+               | (_CLEAR_DV if dv is None or zero_rest else 0))
     dq, dqh = _result(dq, q, "dq", device, qs)
     dk, dkh = _result(dk, k, "dk", device, ks)
     dv, dvh = _result(dv, v, "dv", device, ks)

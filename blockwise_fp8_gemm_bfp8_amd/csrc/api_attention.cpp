@@ -14,6 +14,8 @@ namespace {
 
 constexpr int64_t kMaxRow = int64_t(1) << 22;   // elements; see head_rows
 constexpr int64_t kMaxHead = int64_t(1) << 40;  // elements
+constexpr int kClearAll =
+    BFP8_CLEAR_O | BFP8_CLEAR_LSE | BFP8_CLEAR_DQ | BFP8_CLEAR_DK | BFP8_CLEAR_DV;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -40,6 +42,7 @@ bfp8_status check_shape(const bfp8_attention_shape* s) {
   if (s->head_dim <= 0 || s->head_dim > 128 || s->head_dim % 8 != 0) return BFP8_ERR_SHAPE;
   if (s->causal != 0 && s->causal != 1) return BFP8_ERR_SHAPE;
   if (!(s->scale > 0.0f) || isinf(s->scale)) return BFP8_ERR_SHAPE;
+  if (s->clear < 0 || s->clear > kClearAll) return BFP8_ERR_SHAPE;
   if (s->batch == 0) return s->total_q == 0 && s->total_k == 0 ? BFP8_OK : BFP8_ERR_SHAPE;
   if (s->cu_q == nullptr && s->total_q % s->batch != 0) return BFP8_ERR_SHAPE;
   if (s->cu_k == nullptr && s->total_k % s->batch != 0) return BFP8_ERR_SHAPE;
@@ -174,6 +177,7 @@ bfp8_status bfp8_attention_forward(const bfp8_attention_shape* shape, bfp8_heads
   a.v = as_heads(v);
   a.o = as_heads(o);
   a.lse = lse;
+  if (s.cu_q != nullptr) a.clear = s.clear & (BFP8_CLEAR_O | BFP8_CLEAR_LSE);
   return launch_attention_forward(a, workspace, workspace_bytes, stream);
 }
 
@@ -211,6 +215,8 @@ bfp8_status bfp8_attention_backward(const bfp8_attention_shape* shape, bfp8_head
   a.dk = as_heads(dk);
   a.dv = as_heads(dv);
   a.lse = const_cast<float*>(lse);
+  if (s.cu_q != nullptr) a.clear |= s.clear & BFP8_CLEAR_DQ;
+  if (s.cu_k != nullptr) a.clear |= s.clear & (BFP8_CLEAR_DK | BFP8_CLEAR_DV);
   return launch_attention_backward(a, workspace, stream);
 }
 

@@ -47,6 +47,10 @@ struct AttentionArgs {
   float* part_dq;              // backward: [parts][heads][total_q][head_dim]
   float* part_dk;              // [parts][kv_heads][total_k][head_dim]
   float* part_dv;
+  // The results (BFP8_CLEAR_*) whose rows of no sequence become zero (L: -inf);
+  // workgroups clear_from and later of one of the call's kernels do that.
+  int clear;
+  unsigned clear_from;
 };
 
 // An upper bound on the tiles of all sequences, whose lengths are on the device.
@@ -85,6 +89,13 @@ inline Split choose_split(double longest, double balanced, double step, double f
   const double likely = 0.7 * longest, parts = std::ceil(likely / chunk);
   if (most < 2 || likely - likely / parts < parts * floats * 8 / 5e6 + 8) return Split{1, 1};
   return Split{static_cast<int>(most), std::max(1, static_cast<int>(chunk / step))};
+}
+
+// Workgroups that clear the rows of no sequence, which the host cannot count, of
+// results of so many values in all: one for 64 K values, at most 64 (usually
+// they find nothing).
+inline unsigned clear_workgroups(int64_t values) {
+  return static_cast<unsigned>(std::min<int64_t>(values / 65536 + 1, 64));
 }
 
 bfp8_status launch_attention_forward(const AttentionArgs& a, void* workspace,
@@ -174,6 +185,56 @@ __device__ __forceinline__ Sequence from_lane(const Sequence& s, int l) {
 }
 __device__ __forceinline__ Sequence load_sequence(const AttentionArgs& a, int b) {
   return from_lane(lane_sequence(a, b), 0);
+}
+
+// The rows [0, start) and [end, total) of no sequence.
+struct Rest {
+  int start, end, count;
+  __device__ __forceinline__ Rest(const int32_t* cu, int batch, int total) {
+    start = clampi(cu[0], 0, total);
+    end = clampi(cu[batch], start, total);
+    count = start + total - end;
+  }
+  __device__ __forceinline__ int64_t row(int64_t n) const { return n < start ? n : n - start + end; }
+};
+
+// Zeros in those rows of a tensor of heads, 16 bytes a thread.
+__device__ __forceinline__ void clear_heads(const AttentionArgs& a, const Rest& rest,
+                                            const Heads& t, int heads) {
+  const unsigned part = blockIdx.x - a.clear_from, parts = gridDim.x - a.clear_from;
+  const int per_head = a.head_dim / 8;
+  const int64_t n = (int64_t)rest.count * heads * per_head;
+  for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; i < n; i += parts * blockDim.x) {
+    const int64_t at = i / per_head;  // row, then head
+    const int64_t r = at / heads;
+    *reinterpret_cast<u32x4*>(t.p + rest.row(r) * t.row + (at - r * heads) * t.head +
+                              (i - at * per_head) * 8) = u32x4{0, 0, 0, 0};
+  }
+}
+
+// What the workgroups from clear_from on do, of the forward results.
+__device__ __forceinline__ void clear_forward(const AttentionArgs& a) {
+  const Rest rest(a.cu_q, a.batch, a.total_q);
+  if (rest.count == 0) return;
+  if (a.clear & BFP8_CLEAR_O) clear_heads(a, rest, a.o, a.heads);
+  if ((a.clear & BFP8_CLEAR_LSE) == 0) return;
+  const unsigned part = blockIdx.x - a.clear_from, parts = gridDim.x - a.clear_from;
+  const int64_t n = (int64_t)rest.count * a.heads;
+  for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; i < n; i += parts * blockDim.x) {
+    const int64_t h = i / rest.count;
+    a.lse[h * a.total_q + rest.row(i - h * rest.count)] = -INFINITY;
+  }
+}
+// And of the gradients.
+__device__ __forceinline__ void clear_backward(const AttentionArgs& a) {
+  if (a.clear & BFP8_CLEAR_DQ) {
+    const Rest rest(a.cu_q, a.batch, a.total_q);
+    clear_heads(a, rest, a.dq, a.heads);
+  }
+  if ((a.clear & (BFP8_CLEAR_DK | BFP8_CLEAR_DV)) == 0) return;
+  const Rest rest(a.cu_k, a.batch, a.total_k);
+  if (a.clear & BFP8_CLEAR_DK) clear_heads(a, rest, a.dk, a.kv_heads);
+  if (a.clear & BFP8_CLEAR_DV) clear_heads(a, rest, a.dv, a.kv_heads);
 }
 
 // Last key that row r of a kv head's rows (query r / group) sees; -1: none.

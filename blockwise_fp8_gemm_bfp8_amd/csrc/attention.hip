@@ -71,6 +71,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
   constexpr int kDims = DP / 16;   // 16-column results
   constexpr int kSteps = DP / 32;  // products of one 16x16 square
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages][2][KTile::kBytes];
+  if (blockIdx.x >= a.clear_from) return clear_forward(a);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int g = blockIdx.x % a.kv_heads;
   Sequence s;
@@ -538,6 +539,7 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
                                                                       Parts parts) {
   __shared__ f32x4 other_o[kJoinThreads];
   __shared__ float2 other_ml[kJoinThreads];
+  if (blockIdx.x >= a.clear_from) return clear_forward(a);
   int length, at;
   Place p;
   const int n = blockIdx.x;
@@ -648,6 +650,8 @@ size_t attention_forward_workspace(const AttentionArgs& a) {
 bfp8_status launch_attention_forward(const AttentionArgs& given, void* workspace,
                                      size_t workspace_bytes, hipStream_t stream) {
   AttentionArgs a = given;
+  const unsigned clearing =
+      a.clear == 0 ? 0 : clear_workgroups((int64_t)a.total_q * a.heads * a.head_dim);
   const bool room = workspace != nullptr && workspace_bytes >= attention_forward_workspace(a);
   if (room && streams_keys(a)) {
     Parts parts;
@@ -658,7 +662,9 @@ bfp8_status launch_attention_forward(const AttentionArgs& given, void* workspace
             ? launch(attention_stream_kernel<64>, dim3(kStreams), dim3(64), stream, a, parts)
             : launch(attention_stream_kernel<128>, dim3(kStreams), dim3(64), stream, a, parts);
     if (st != BFP8_OK) return st;
-    return launch(attention_join_kernel, dim3(kStreams - 1), dim3(kJoinThreads), stream, a, parts);
+    a.clear_from = kStreams - 1;
+    return launch(attention_join_kernel, dim3(kStreams - 1 + clearing), dim3(kJoinThreads), stream, a,
+                  parts);
   }
   a.split_q = room ? key_split(a) : Split{1, 1};
   const int64_t rows = (int64_t)a.heads * a.total_q;
@@ -670,7 +676,8 @@ bfp8_status launch_attention_forward(const AttentionArgs& given, void* workspace
   const int64_t blocks = places * a.kv_heads * a.split_q.most;
   if (blocks == 0) return BFP8_OK;
   if (blocks >= (int64_t(1) << 31)) return BFP8_ERR_SHAPE;
-  const dim3 grid(static_cast<unsigned>(blocks));
+  a.clear_from = static_cast<unsigned>(blocks);
+  const dim3 grid(a.clear_from + clearing);
   const bfp8_status st =
       a.head_dim <= 64
           ? launch(attention_forward_kernel<64>, grid, dim3(64 * kWaves), stream, a, places)

@@ -43,9 +43,10 @@ constexpr int kKeyRows = 32 * kKeyWaves;
 static_assert(kWaves == 2 * kKeyWaves, "two halves");
 
 // lse2 and -delta of every row of every head, for the kernel below: 16 lanes a
-// row, 8 values a lane.  Memory-bound: O and dO once (16384 tokens, 16 heads of
+// row, 8 values a lane (and zeros in the gradients' rows of no sequence).  Memory-bound: O and dO once (16384 tokens, 16 heads of
 // 128: 30 us, 5.4 TB/s).
 __global__ __launch_bounds__(256) void attention_stats_kernel(AttentionArgs a) {
+  if (blockIdx.x >= a.clear_from) return clear_backward(a);
   const int64_t at = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;  // row, then head
   const int d = threadIdx.x % 16 * 8;
   const int64_t t = at / a.heads;
@@ -652,9 +653,11 @@ bfp8_status launch_attention_backward(AttentionArgs a, void* workspace, hipStrea
   const int64_t stat_blocks = (q_rows + 15) / 16;
   if (blocks >= (int64_t(1) << 31) || stat_blocks >= (int64_t(1) << 31)) return BFP8_ERR_SHAPE;
   bfp8_status st = BFP8_OK;
-  if (stat_blocks > 0)
-    st = launch(attention_stats_kernel, dim3(static_cast<unsigned>(stat_blocks)), dim3(256), stream,
-                a);
+  const unsigned clearing =
+      a.clear == 0 ? 0 : clear_workgroups((q_rows + 2 * k_rows) * a.head_dim);
+  a.clear_from = static_cast<unsigned>(stat_blocks);
+  if (stat_blocks + clearing > 0)
+    st = launch(attention_stats_kernel, dim3(a.clear_from + clearing), dim3(256), stream, a);
   if (st != BFP8_OK || blocks == 0) return st;
   const dim3 grid(static_cast<unsigned>(blocks));
   st = a.head_dim <= 64 ? launch(attention_backward_kernel<64>, grid, dim3(64 * kWaves), stream, a,

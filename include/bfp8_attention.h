@@ -102,7 +102,17 @@ bfp8_status bfp8_rope(const void* x, int64_t x_row, int64_t x_head, void* y, int
  *       rows of sequence b are used (a cache with room).
  * The host cannot see these arrays: the kernels clamp every entry into the
  * tensors' rows, so no entry makes them read or write elsewhere.
+ *
+ * Rows before cu[0] and from cu[batch] on belong to no sequence.  A result
+ * keeps what it held there, unless `clear` names it: then it is 0 (L: -inf).
  */
+enum {
+  BFP8_CLEAR_O = 1, /* of the forward call */
+  BFP8_CLEAR_LSE = 2,
+  BFP8_CLEAR_DQ = 4, /* of the backward call */
+  BFP8_CLEAR_DK = 8,
+  BFP8_CLEAR_DV = 16
+};
 typedef struct {
   int64_t batch;
   int64_t total_q, total_k; /* rows of q, o, dq, do / of k, v, dk, dv; < 2^31 */
@@ -113,6 +123,7 @@ typedef struct {
   int head_dim;        /* a multiple of 8, at most 128 */
   int causal;          /* 0 or 1 */
   float scale;
+  int clear;           /* a sum of BFP8_CLEAR_*, 0: none */
 } bfp8_attention_shape;
 
 /* A tensor of heads: pointer and strides in elements (see the top). */
@@ -138,8 +149,7 @@ bfp8_status bfp8_attention_forward(const bfp8_attention_shape* shape, bfp8_heads
 
 /* dq, dk, dv from the forward pass's inputs, its o and lse, and the gradient
  * dout of o; the probabilities are recomputed from lse.  Rows of dk and dv
- * past a sequence's used length become zero; rows that belong to no sequence
- * are not written.  The workspace (bfp8_attention_workspace_bytes(shape, 1):
+ * past a sequence's used length become zero.  The workspace (bfp8_attention_workspace_bytes(shape, 1):
  * two float32 values a row and head, and partial gradients where few workgroups
  * meet long sequences) is required: BFP8_ERR_WORKSPACE if it is NULL or smaller.  dq, dk and dv
  * must not overlap each other or the inputs. */
