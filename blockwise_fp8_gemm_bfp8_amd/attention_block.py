@@ -26,7 +26,13 @@ class AttentionBlock:
     """w_qkv [(heads + 2 kv_heads) head_dim][hidden], w_o [hidden][heads head_dim]
     (bfloat16, rows q heads, k heads, v heads); `tokens` rows a pass, in
     sequences starting at `cu` (int32 [batch+1], device); `table` from
-    rope_table, `positions` int32 [tokens].  All sizes multiples of 128."""
+    rope_table, `positions` int32 [tokens].  All sizes multiples of 128.
+
+    The sequences need not fill the rows, and `cu` and `positions` may hold
+    other values in every pass: rows of no sequence (before cu[0], from cu[-1]
+    on) count as zeros where attention leaves off, so y and dx are 0 there and
+    the weights' gradients take nothing from them, whatever their positions.
+    x and dy must be finite there, as they share a 128-token group's scale."""
 
     def __init__(self, w_qkv, w_o, heads: int, kv_heads: int, tokens: int, cu, positions, table,
                  scale: float = None):
@@ -42,6 +48,8 @@ class AttentionBlock:
                 raise ValueError(f"{name} must be a multiple of 128, got {n}")
         self.w_qkv, self.w_o = w_qkv, w_o
         self.heads, self.kv_heads, self.head_dim, self.scale = heads, kv_heads, D, scale
+        if positions is None:  # token t stands at t
+            positions = torch.arange(tokens, dtype=torch.int32, device=w_qkv.device)
         self.cu, self.positions, self.table = cu, positions, table
         dev, M, E = w_qkv.device, tokens, heads * D
         u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
@@ -60,6 +68,7 @@ class AttentionBlock:
         b["qkv"], b["dqkv"] = new((M, heads + 2 * kv_heads, D), bf), new((M, heads + 2 * kv_heads, D), bf)
         b["a"], b["da"] = new((M, heads, D), bf), new((M, heads, D), bf)
         b["lse"] = new((heads, M), f32)
+        b["positions"] = new((M,), torch.int32)
         b["y"], b["dx"] = new((M, hidden), bf), new((M, hidden), bf)
         b["dw_qkv"], b["dw_o"] = new((rows, hidden), bf), new((hidden, E), bf)
         need = max(gemm_workspace_bytes("NT", "act_km", "act_km", rows, hidden, M),
@@ -75,7 +84,12 @@ class AttentionBlock:
 
     def _turn(self, rows, inverse):
         turned = rows[:, :self.heads + self.kv_heads]
-        rope(turned, self.table, self.positions, inverse=inverse, out=turned)
+        positions = self.positions
+        if inverse:
+            # A position outside the table turns even a zero row into NaN.  A token of a
+            # sequence with such a position has had its NaN in the forward pass.
+            positions = torch.clamp(positions, 0, self.table.shape[0] - 1, out=self.buf["positions"])
+        rope(turned, self.table, positions, inverse=inverse, out=turned)
 
     def quantize_weights(self):
         """Codes of both weights, once per optimizer step."""
@@ -93,7 +107,7 @@ class AttentionBlock:
              out=b["qkv"].view(M, -1), workspace=b["gemm_ws"])
         self._turn(b["qkv"], False)
         attention_forward(*self._heads(b["qkv"]), self.cu, self.cu, scale=self.scale, out=b["a"],
-                          lse=b["lse"], workspace=b["attn_ws"])
+                          lse=b["lse"], workspace=b["attn_ws"], zero_rest=True)
         quantize_act_dual_kmajor(b["a"].view(M, -1), b["aq"], b["as"], b["aqt"], b["ast"])
         return gemm("NT", b["aq"], b["as"], b["wo_q"], b["wo_s"], "act_km", "block", out=b["y"],
                     workspace=b["gemm_ws"])
@@ -109,7 +123,8 @@ class AttentionBlock:
              workspace=b["gemm_ws"])
         dq, dk, dv = self._heads(b["dqkv"])
         attention_backward(b["da"], *self._heads(b["qkv"]), b["a"], b["lse"], self.cu, self.cu,
-                           scale=self.scale, dq=dq, dk=dk, dv=dv, workspace=b["attn_ws"])
+                           scale=self.scale, dq=dq, dk=dk, dv=dv, workspace=b["attn_ws"],
+                           zero_rest=True)
         self._turn(b["dqkv"], True)
         quantize_act_dual_kmajor(b["dqkv"].view(M, -1), b["dqkvq"], b["dqkvs"], b["dqkvqt"],
                                  b["dqkvst"])
