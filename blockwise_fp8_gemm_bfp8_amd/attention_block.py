@@ -82,6 +82,13 @@ class AttentionBlock:
         H, KV = self.heads, self.kv_heads
         return rows[:, :H], rows[:, H:H + KV], rows[:, H + KV:]
 
+    def _check_rows(self, t, name):
+        """The quantisers take their sizes from t and write to this block's buffers."""
+        y = self.buf["y"]
+        if t.shape != y.shape or t.device != y.device:
+            raise ValueError(f"{name} must be {list(y.shape)} on {y.device}, got {list(t.shape)} on "
+                             f"{t.device}")
+
     def _turn(self, rows, inverse):
         turned = rows[:, :self.heads + self.kv_heads]
         positions = self.positions
@@ -100,6 +107,7 @@ class AttentionBlock:
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         """y [tokens][hidden] of x [tokens][hidden] (bfloat16); the buffers keep
         what backward needs."""
+        self._check_rows(x, "x")
         b = self.buf
         M = b["y"].shape[0]
         quantize_act_dual_kmajor(x, b["xq"], b["xs"], b["xqt"], b["xst"])
@@ -114,6 +122,7 @@ class AttentionBlock:
 
     def backward(self, dy: torch.Tensor):
         """(dx, dw_qkv, dw_o) for the gradient dy of the last forward's y."""
+        self._check_rows(dy, "dy")
         b = self.buf
         M = b["y"].shape[0]
         quantize_act_dual_kmajor(dy, b["dyq"], b["dys"], b["dyqt"], b["dyst"])
