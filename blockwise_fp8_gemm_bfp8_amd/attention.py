@@ -174,6 +174,8 @@ def _workspace(shape, backward, given, like):
             return None, 0
         given = torch.empty(n, dtype=torch.uint8, device=like.device)
         return given, n
+    if given.get_device() != like.get_device() or not given.is_contiguous():
+        raise ValueError(f"workspace must be a dense tensor on device {like.get_device()}")
     return given, given.numel() * given.element_size()
 
 
