@@ -616,11 +616,13 @@ bool streams_keys(const AttentionArgs& a) {
   const int64_t row_tiles =
       std::max<int64_t>(a.batch, ((int64_t)a.total_q * a.group + 31) / 32) * a.kv_heads;
   const int64_t key_tiles = (int64_t)a.total_k / a.batch / 32;
-  // the line's units, counted in 32 bits: any split of total_q over the sequences
-  const int64_t most_rows = (int64_t)a.total_q * a.group / 32 + a.batch;
-  const int64_t most_keys = (int64_t)a.total_k / 32 + (1 + kSegmentCost) * a.batch;
-  return key_tiles >= 32 && row_tiles <= std::min<int64_t>(key_tiles, 256) &&
-         most_rows * a.kv_heads * most_keys < (int64_t(1) << 31);
+  if (key_tiles < 32 || row_tiles > std::min<int64_t>(key_tiles, 256)) return false;
+  // The line's units and the starts of its stretches are counted in 32 bits, also
+  // where falling starts of sequences give every one of them all rows and keys.
+  // (256 row tiles over 2^23 keys in 32 sequences are the smallest refused.)
+  const int64_t segments = ((int64_t)a.total_q * a.group + 31) / 32 * a.kv_heads;
+  const int64_t units = kSegmentCost + ((int64_t)a.total_k + 31) / 32;
+  return segments * units * a.batch < (int64_t(1) << 31) - kStreams;
 }
 
 // The split of the row tiles' keys; a tile of 64 keys takes about 1.1 us.
