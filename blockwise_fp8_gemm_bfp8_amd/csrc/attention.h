@@ -53,6 +53,11 @@ struct AttentionArgs {
   unsigned clear_from;
 };
 
+// A launch has fewer than 2^32 threads along an axis.
+inline bool grid_fits(int64_t blocks, int64_t threads) {
+  return blocks < (int64_t(1) << 32) / threads;
+}
+
 // An upper bound on the tiles of all sequences, whose lengths are on the device.
 inline int64_t tile_bound(const int32_t* cu, int64_t batch, int64_t total, int64_t mult,
                           int64_t unit) {

@@ -677,7 +677,7 @@ bfp8_status launch_attention_forward(const AttentionArgs& given, void* workspace
   const int64_t places = tile_bound(a.cu_q, a.batch, a.total_q, a.group, kRows);
   const int64_t blocks = places * a.kv_heads * a.split_q.most;
   if (blocks == 0) return BFP8_OK;
-  if (blocks >= (int64_t(1) << 31)) return BFP8_ERR_SHAPE;
+  if (!grid_fits(blocks + clearing, 64 * kWaves)) return BFP8_ERR_SHAPE;
   a.clear_from = static_cast<unsigned>(blocks);
   const dim3 grid(a.clear_from + clearing);
   const bfp8_status st =

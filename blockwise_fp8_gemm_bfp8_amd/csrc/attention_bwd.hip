@@ -651,10 +651,11 @@ bfp8_status launch_attention_backward(AttentionArgs a, void* workspace, hipStrea
   const int64_t blocks =
       (p.k_tiles * a.split_k.most + p.q_tiles * a.split_q.most) * a.kv_heads;
   const int64_t stat_blocks = (q_rows + 15) / 16;
-  if (blocks >= (int64_t(1) << 31) || stat_blocks >= (int64_t(1) << 31)) return BFP8_ERR_SHAPE;
-  bfp8_status st = BFP8_OK;
   const unsigned clearing =
       a.clear == 0 ? 0 : clear_workgroups((q_rows + 2 * k_rows) * a.head_dim);
+  if (!grid_fits(blocks, 64 * kWaves) || !grid_fits(stat_blocks + clearing, 256))
+    return BFP8_ERR_SHAPE;
+  bfp8_status st = BFP8_OK;
   a.clear_from = static_cast<unsigned>(stat_blocks);
   if (stat_blocks + clearing > 0)
     st = launch(attention_stats_kernel, dim3(a.clear_from + clearing), dim3(256), stream, a);

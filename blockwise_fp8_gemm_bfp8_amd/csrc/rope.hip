@@ -129,6 +129,7 @@ bfp8_status launch_units(const RopeArgs& a, hipStream_t stream) {
   const int units = turned + copied;  // at most head_dim / 2
   const int slots = 256 / units;
   const int64_t blocks = (a.tokens * a.heads + slots - 1) / slots;
+  if (!grid_fits(blocks, 256)) return BFP8_ERR_SHAPE;
   return launch(rope_kernel<T, V, INTERLEAVED>, dim3(static_cast<unsigned>(blocks)), dim3(256),
                 stream, a, units, slots, turned);
 }
@@ -153,9 +154,10 @@ bfp8_status launch_rope_typed(const RopeArgs& a, bool interleaved, hipStream_t s
 bfp8_status launch_rope_table(float* table, int64_t positions, int rot_dim, double base,
                               double factor, double original_length, int scaling,
                               hipStream_t stream) {
-  const int64_t count = positions * (rot_dim / 2);
-  return launch(rope_table_kernel, dim3(static_cast<unsigned>((count + 255) / 256)), dim3(256),
-                stream, reinterpret_cast<float2*>(table), count, rot_dim / 2, rot_dim, base, factor,
+  const int64_t count = positions * (rot_dim / 2), blocks = (count + 255) / 256;
+  if (!grid_fits(blocks, 256)) return BFP8_ERR_SHAPE;
+  return launch(rope_table_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), stream,
+                reinterpret_cast<float2*>(table), count, rot_dim / 2, rot_dim, base, factor,
                 original_length, scaling);
 }
 

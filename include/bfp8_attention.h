@@ -17,6 +17,12 @@
  * q, k and v heads of a fused projection's rows, tensors stored head by head
  * and caches are all taken as they lie.  Pointers are 16-byte aligned, strides
  * keep every head 16-byte aligned, and row strides are at most 2^22 elements.
+ *
+ * Sizes.  A call whose launch would need 2^32 threads or more is refused with
+ * BFP8_ERR_SHAPE: a rotation of 2^29 heads in all (of 128 bf16 values in 16-byte
+ * units, 2^24 at the least), a table of 2^32 pairs, attention of about 2^31 rows (tokens
+ * times query heads), its gradient of 2^28 rows or 2^30 keys (tokens times kv
+ * heads).
  */
 #ifndef BFP8_ATTENTION_H_
 #define BFP8_ATTENTION_H_
