@@ -14,6 +14,7 @@ namespace {
 
 constexpr int64_t kMaxRow = int64_t(1) << 22;   // elements; see head_rows
 constexpr int64_t kMaxHead = int64_t(1) << 40;  // elements
+constexpr int64_t kMaxTile = 512;  // rows or keys of a tile and the next at most
 constexpr int kClearAll =
     BFP8_CLEAR_O | BFP8_CLEAR_LSE | BFP8_CLEAR_DQ | BFP8_CLEAR_DK | BFP8_CLEAR_DV;
 
@@ -36,6 +37,8 @@ bfp8_status check_shape(const bfp8_attention_shape* s) {
   if (s->batch < 0 || s->total_q < 0 || s->total_k < 0 || s->batch >= limit ||
       s->total_q >= limit || s->total_k >= limit)
     return BFP8_ERR_SHAPE;
+  // a query's place and a key's, and a tile past either, are added in 32 bits
+  if (s->total_q + s->total_k > limit - kMaxTile) return BFP8_ERR_SHAPE;
   if (s->heads <= 0 || s->kv_heads <= 0 || s->heads % s->kv_heads != 0) return BFP8_ERR_SHAPE;
   // rows of a kv head (queries times heads of its group) are counted in 32 bits
   if (s->total_q * (s->heads / s->kv_heads) >= limit) return BFP8_ERR_SHAPE;

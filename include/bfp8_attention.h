@@ -121,7 +121,8 @@ enum {
 };
 typedef struct {
   int64_t batch;
-  int64_t total_q, total_k; /* rows of q, o, dq, do / of k, v, dk, dv; < 2^31 */
+  int64_t total_q, total_k; /* rows of q, o, dq, do / of k, v, dk, dv; at most
+                               2^31 - 512 together */
   const int32_t* cu_q;
   const int32_t* cu_k;
   const int32_t* k_lens;

@@ -65,3 +65,16 @@ def test_long_rope(L, tokens, heads, dim, rot, dt):
 def test_long_table(L):
     for n, rot in ((1 << 24, 512), (1 << 30, 8), ((1 << 31) - 1, 64)):
         assert L.bfp8_rope_table(P, n, rot, 1e4, 0, 1.0, 0, None) == SHAPE
+
+
+@pytest.mark.parametrize("total_q,total_k", [(1, (1 << 31) - 1), (64, (1 << 31) - 575), (512, (1 << 31) - 513),
+                                             (1 << 30, (1 << 30) - 511)])
+@pytest.mark.parametrize("causal", [0, 1])
+def test_rows_and_keys_together(L, total_q, total_k, causal):
+    """Without a causal mask query i's last key was i + total_k in 32 bits: past
+    2^31 it came out negative and the query saw nothing; and the streamed keys
+    of (1, 2^31 - 1) were counted as total_k + 31."""
+    s = shape(total_q, total_k, causal=causal)
+    for back in (0, 1):
+        assert L.bfp8_attention_workspace_bytes(ctypes.byref(s), back) == ctypes.c_size_t(-1).value
+    assert forward(L, s) == SHAPE and backward(L, s) == SHAPE
