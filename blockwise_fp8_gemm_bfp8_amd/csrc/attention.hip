@@ -46,6 +46,14 @@ constexpr int kStages = 3;          // tiles in LDS: one being read, two under w
 // multiplication of the accumulators.
 constexpr float kSlack = 8.0f;
 
+// What a row's sum over its maximum (in powers of two) makes of its output and
+// its log-sum-exp: a sum of zero is a row that sees no key, one that is NaN stays
+// NaN in both.
+__device__ __forceinline__ float row_factor(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+__device__ __forceinline__ float row_lse(float top, float sum) {
+  return sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
 // The running maxima of two sets of rows take in `either` (column_max of both),
 // and their sums and accumulators are scaled to them.
 template <int DP>
@@ -234,10 +242,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_forward_kernel(Atten
       continue;
     }
     uint16_t* orow = a.o.p + t[n] * a.o.row + h[n] * a.o.head;
-    store_row<DP>(orow, o[n], sum > 0.0f ? 1.0f / sum : 0.0f, a.head_dim, lane);
+    store_row<DP>(orow, o[n], row_factor(sum), a.head_dim, lane);
     if (lane < 16)
-      a.lse[(int64_t)h[n] * a.total_q + t[n]] =
-          sum > 0.0f ? (m[n] + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+      a.lse[(int64_t)h[n] * a.total_q + t[n]] = row_lse(m[n], sum);
   }
 }
 
@@ -273,12 +280,12 @@ __global__ __launch_bounds__(256) void attention_join_splits_kernel(AttentionArg
       sum = sum * keep + x.y * mul;
       o = o * keep + v * mul;
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = row_factor(sum);
     u32x2 w;
     w.x = pack_bf16x2(o[0] * inv, o[1] * inv);
     w.y = pack_bf16x2(o[2] * inv, o[3] * inv);
     *reinterpret_cast<u32x2*>(a.o.p + t * a.o.row + h * a.o.head + d) = w;
-    if (d == 0) a.lse[row] = sum > 0.0f ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+    if (d == 0) a.lse[row] = row_lse(top, sum);
   }
 }
 
@@ -502,10 +509,9 @@ __global__ __launch_bounds__(64, 1) void attention_stream_kernel(AttentionArgs a
         if (!valid[n]) continue;
         if (t0 == 0 && end == p.units) {
           uint16_t* orow = a.o.p + at[n] * a.o.row + h[n] * a.o.head;
-          store_row<DP>(orow, o[n], sum > 0.0f ? 1.0f / sum : 0.0f, a.head_dim, lane);
+          store_row<DP>(orow, o[n], row_factor(sum), a.head_dim, lane);
           if (lane < 16)
-            a.lse[(int64_t)h[n] * a.total_q + at[n]] =
-                sum > 0.0f ? (m[n] + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+            a.lse[(int64_t)h[n] * a.total_q + at[n]] = row_lse(m[n], sum);
         } else {
           const int64_t part = (2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * 32 + 16 * n + (lane & 15);
           float* to = parts.o + part * a.head_dim;
@@ -591,14 +597,12 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
       add(other_ml[from], other_o[from]);
     }
     const int i = (row0 + r) / a.group, h = g * a.group + (row0 + r) % a.group;
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float inv = row_factor(sum);
     u32x2 w;
     w.x = pack_bf16x2(o[0] * inv, o[1] * inv);
     w.y = pack_bf16x2(o[2] * inv, o[3] * inv);
     *reinterpret_cast<u32x2*>(a.o.p + (int64_t)(s.q0 + i) * a.o.row + h * a.o.head + d) = w;
-    if (d == 0)
-      a.lse[(int64_t)h * a.total_q + s.q0 + i] =
-          sum > 0.0f ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+    if (d == 0) a.lse[(int64_t)h * a.total_q + s.q0 + i] = row_lse(top, sum);
   }
 }
 

@@ -97,7 +97,7 @@ bfp8_status bfp8_rope(const void* x, int64_t x_row, int64_t x_head, void* y, int
  * other sequences, and of rows past a sequence's used length, are never part
  * of a result, whatever they hold; Inf or NaN within a sequence's own used
  * rows is outside the contract (no fault, but any row of that sequence may be
- * affected).  With BFP8_DEBUG (see bfp8.h) q, dout and, without k_lens, k and v
+ * affected; a query with a NaN score gets NaN in O and L).  With BFP8_DEBUG (see bfp8.h) q, dout and, without k_lens, k and v
  * are scanned whole, rows of no sequence among them.
  *
  * Sequences lie one after another in the tensors' rows:
