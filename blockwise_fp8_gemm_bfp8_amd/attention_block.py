@@ -51,6 +51,7 @@ class AttentionBlock:
         if positions is None:  # token t stands at t
             positions = torch.arange(tokens, dtype=torch.int32, device=w_qkv.device)
         self.cu, self.positions, self.table = cu, positions, table
+        self._quantized = self._ran = False  # what the buffers hold
         dev, M, E = w_qkv.device, tokens, heads * D
         u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
         new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
@@ -99,15 +100,18 @@ class AttentionBlock:
         rope(turned, self.table, positions, inverse=inverse, out=turned)
 
     def quantize_weights(self):
-        """Codes of both weights, once per optimizer step."""
+        """Codes of both weights, once per optimizer step (and before the first forward)."""
         b = self.buf
         quantize_weight_batch([self.w_qkv, self.w_o], [b["wqkv_q"], b["wo_q"]],
                               [b["wqkv_s"], b["wo_s"]])
+        self._quantized = True
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         """y [tokens][hidden] of x [tokens][hidden] (bfloat16); the buffers keep
         what backward needs."""
         self._check_rows(x, "x")
+        if not self._quantized:
+            raise RuntimeError("quantize_weights() comes before the first forward")
         b = self.buf
         M = b["y"].shape[0]
         quantize_act_dual_kmajor(x, b["xq"], b["xs"], b["xqt"], b["xst"])
@@ -117,12 +121,15 @@ class AttentionBlock:
         attention_forward(*self._heads(b["qkv"]), self.cu, self.cu, scale=self.scale, out=b["a"],
                           lse=b["lse"], workspace=b["attn_ws"], zero_rest=True)
         quantize_act_dual_kmajor(b["a"].view(M, -1), b["aq"], b["as"], b["aqt"], b["ast"])
+        self._ran = True
         return gemm("NT", b["aq"], b["as"], b["wo_q"], b["wo_s"], "act_km", "block", out=b["y"],
                     workspace=b["gemm_ws"])
 
     def backward(self, dy: torch.Tensor):
         """(dx, dw_qkv, dw_o) for the gradient dy of the last forward's y."""
         self._check_rows(dy, "dy")
+        if not self._ran:
+            raise RuntimeError("forward() comes before backward")
         b = self.buf
         M = b["y"].shape[0]
         quantize_act_dual_kmajor(dy, b["dyq"], b["dys"], b["dyqt"], b["dyst"])

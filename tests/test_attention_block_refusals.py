@@ -24,3 +24,19 @@ def test_rows_of_another_size():
         block.forward(x.cpu())
     with pytest.raises(ValueError, match="dy must be"):
         block.backward(dy.cpu())
+
+
+def test_steps_out_of_order():
+    """Without codes of the weights, or a forward pass, the buffers hold nothing."""
+    block, x, dy = base.make()
+    fresh = base.AttentionBlock(block.w_qkv, block.w_o, base.HEADS, base.KV, x.shape[0], block.cu,
+                                block.positions, block.table)
+    with pytest.raises(RuntimeError, match="quantize_weights"):
+        fresh.forward(x)
+    with pytest.raises(RuntimeError, match="forward"):
+        fresh.backward(dy)
+    fresh.quantize_weights()
+    with pytest.raises(RuntimeError, match="forward"):
+        fresh.backward(dy)
+    want = [block.forward(x), *block.backward(dy)]
+    assert all(torch.equal(a, b) for a, b in zip([fresh.forward(x), *fresh.backward(dy)], want))
