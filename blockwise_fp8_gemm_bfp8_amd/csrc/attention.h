@@ -381,13 +381,13 @@ __device__ __forceinline__ void copy16(uint32_t lds, uint32_t off, i32x4 rsrc) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(off), "s"(rsrc)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ void copy4(uint32_t lds, uint32_t off, i32x4 rsrc) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(off), "s"(rsrc)
-               : "memory");
+               : "memory", "m0");
 }
 // Until at most LEFT of this wave's copies are under way (they end in order).
 template <int LEFT>
