@@ -32,7 +32,8 @@ class AttentionBlock:
     other values in every pass: rows of no sequence (before cu[0], from cu[-1]
     on) count as zeros where attention leaves off, so y and dx are 0 there and
     the weights' gradients take nothing from them, whatever their positions.
-    x and dy must be finite there, as they share a 128-token group's scale."""
+    x and dy must be finite there, as they share a 128-token group's scale.
+    (BFP8_DEBUG's scan takes a position outside the table for what it gives: NaN.)"""
 
     def __init__(self, w_qkv, w_o, heads: int, kv_heads: int, tokens: int, cu, positions, table,
                  scale: float = None):

@@ -21,7 +21,8 @@
 // and 8 key/value heads of 128, causal: 4 sequences of 4096 take 250 to 262 us
 // (1068 TFLOP/s and more: cards differ), one of 16384 takes 897 to 954 us
 // (1157), 13 sequences of 1 to 2417 tokens, 8274 in all, 67 us (the longest
-// workgroup: 38 tiles of keys one after another where an even share is 29 a CU).
+// workgroup: 38 tiles of keys one after another where an even share is 29 a CU;
+// and the starts and ends of 2.4 workgroups a CU, one at a time).
 // The same long sequence of zeros, which draws less power, takes 726 us.  Of 967
 // us, before its last steps, it took 13 % less without the softmax's arithmetic,
 // 12 % without LDS reads, 4 % without copies and barriers: none of them alone
@@ -306,7 +307,10 @@ __global__ __launch_bounds__(256) void attention_join_splits_kernel(AttentionArg
 // TB/s, and 8 us to join; a copy's rate would take 20.  A workgroup of 4 waves
 // per (sequence, head, stretch) took 65 us for both, one persistent workgroup
 // of joined waves per CU 88.
-constexpr int kStreams = 1024;  // one on each SIMD (its registers leave no room for two)
+// One on each SIMD.  With heads of 128 its registers (244) would leave room for
+// two, the LDS of a CU for five in all; 1280 and 2048 of them took 36 us for both
+// kernels where 1024 take 30.
+constexpr int kStreams = 1024;
 constexpr int kMinShare = 3;    // line units of a stretch at least
 // A segment counts for so many tiles more than it has, for the latency of its
 // first loads; they come first.
@@ -614,7 +618,8 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
 // 128 in us, the other kernel / this one: R 8: K 16 12 / 15, K 32 19 / 14, K
 // 128 62 / 17; R 64: K 64 35 / 34, K 128 92 / 43; R 128: K 32 21 / 26, K 128
 // 64 / 55; R 256: K 64 47 / 55, K 128 93 / 97, K 512 350 / 298; R 512: K 128
-// 94 / 153.
+// 94 / 153.  (Both sides measured up to R 512; the other kernel alone takes 383
+// us for 128 requests over 4096 keys each, R 1024, and 760 for 256.)
 bool streams_keys(const AttentionArgs& a) {
   if (a.total_q == 0) return false;
   const int64_t row_tiles =

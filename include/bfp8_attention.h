@@ -20,9 +20,9 @@
  *
  * Sizes.  A call whose launch would need 2^32 threads or more is refused with
  * BFP8_ERR_SHAPE: a rotation of 2^29 heads in all (of 128 bf16 values in 16-byte
- * units, 2^24 at the least), a table of 2^32 pairs, attention of about 2^31 rows (tokens
- * times query heads), its gradient of 2^28 rows or 2^30 keys (tokens times kv
- * heads).
+ * units, 2^24 at the least), a table of 2^32 pairs, attention of about 2^31 rows
+ * (tokens times query heads), its gradient of 2^28 rows or 2^30 keys (tokens
+ * times kv heads).
  */
 #ifndef BFP8_ATTENTION_H_
 #define BFP8_ATTENTION_H_
@@ -49,7 +49,10 @@ extern "C" {
  *   BFP8_ROPE_YARN    g_i f_i + (1 - g_i) f_i / factor,
  *                     g_i = clamp((t_i - 1) / 31, 0, 1) with t_i =
  *                     original_length * f_i / (2 pi) the turns a pair makes
- *                     over the original context; m = 0.1 ln(factor) + 1.
+ *                     over the original context; m = 0.1 ln(factor) + 1.  (The
+ *                     ramp is linear in the turns, from 1 to 32; models whose
+ *                     program ramps over the pair's index, or between other
+ *                     bounds, need another table of the same layout.)
  */
 typedef enum { BFP8_ROPE_HALF = 0, BFP8_ROPE_INTERLEAVED = 1 } bfp8_rope_layout;
 typedef enum {
@@ -97,8 +100,9 @@ bfp8_status bfp8_rope(const void* x, int64_t x_row, int64_t x_head, void* y, int
  * other sequences, and of rows past a sequence's used length, are never part
  * of a result, whatever they hold; Inf or NaN within a sequence's own used
  * rows is outside the contract (no fault, but any row of that sequence may be
- * affected; a query with a NaN score gets NaN in O and L).  With BFP8_DEBUG (see bfp8.h) q, dout and, without k_lens, k and v
- * are scanned whole, rows of no sequence among them.
+ * affected; a query with a NaN score gets NaN in O and L).  With BFP8_DEBUG (see
+ * bfp8.h) q, dout and, without k_lens, k and v are scanned whole, rows of no
+ * sequence among them.
  *
  * Sequences lie one after another in the tensors' rows:
  *   cu_q [batch+1], cu_k [batch+1]  int32 device arrays, non-decreasing:
@@ -147,19 +151,20 @@ typedef struct {
  * for an invalid shape. */
 size_t bfp8_attention_workspace_bytes(const bfp8_attention_shape* shape, int backward);
 
-/* o and lse from q, k, v.  The workspace holds float32 partial results where the
- * keys of few query rows are split over workgroups; smaller or NULL: no split
- * (same contract, slower). */
+/* o and lse, which must not overlap the inputs, from q, k, v.  The workspace
+ * holds float32 partial results where the keys of few query rows are split over
+ * workgroups; smaller or NULL: no split (same contract, slower). */
 bfp8_status bfp8_attention_forward(const bfp8_attention_shape* shape, bfp8_heads q, bfp8_heads k,
                                    bfp8_heads v, bfp8_heads_out o, float* lse, void* workspace,
                                    size_t workspace_bytes, hipStream_t stream);
 
 /* dq, dk, dv from the forward pass's inputs, its o and lse, and the gradient
  * dout of o; the probabilities are recomputed from lse.  Rows of dk and dv
- * past a sequence's used length become zero.  The workspace (bfp8_attention_workspace_bytes(shape, 1):
- * two float32 values a row and head, and partial gradients where few workgroups
- * meet long sequences) is required: BFP8_ERR_WORKSPACE if it is NULL or smaller.  dq, dk and dv
- * must not overlap each other or the inputs. */
+ * past a sequence's used length become zero.  The workspace
+ * (bfp8_attention_workspace_bytes(shape, 1): two float32 values a row and head,
+ * and partial gradients where few workgroups meet long sequences) is required:
+ * BFP8_ERR_WORKSPACE if it is NULL or smaller.  dq, dk and dv must not overlap
+ * each other or the inputs. */
 bfp8_status bfp8_attention_backward(const bfp8_attention_shape* shape, bfp8_heads q, bfp8_heads k,
                                     bfp8_heads v, bfp8_heads o, const float* lse, bfp8_heads dout,
                                     bfp8_heads_out dq, bfp8_heads_out dk, bfp8_heads_out dv,
