@@ -102,7 +102,7 @@ class AttentionShape(ctypes.Structure):
     """bfp8_attention_shape."""
     _fields_ = [("batch", _i64), ("total_q", _i64), ("total_k", _i64), ("cu_q", _vp),
                 ("cu_k", _vp), ("k_lens", _vp), ("heads", _int), ("kv_heads", _int),
-                ("head_dim", _int), ("causal", _int), ("scale", ctypes.c_float), ("clear", _int)]
+                ("head_dim", _int), ("causal", _int), ("scale", ctypes.c_float)]
 
 
 class Heads(ctypes.Structure):

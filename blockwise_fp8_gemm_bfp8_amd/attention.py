@@ -150,9 +150,11 @@ def _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale):
     _check_i32(k_lens, "k_lens", batch, device)
     if scale is None:
         scale = 1.0 / math.sqrt(D) if D else 1.0
-    shape = AttentionShape(batch, Tq, Tk, _pointer(cu_q), _pointer(cu_k), _pointer(k_lens), H, KV,
-                           D, int(causal), scale)
-    return device, shape, qh, kh, vh, qs, ks
+    s = AttentionShape(batch, Tq, Tk, _pointer(cu_q), _pointer(cu_k), _pointer(k_lens), H, KV,
+                       D, int(causal), scale)
+    if s.causal not in (0, 1):  # other bits are the library's BFP8_CLEAR_*
+        raise ValueError(f"causal must be true or false, got {causal}")
+    return device, s, qh, kh, vh, qs, ks
 
 
 def attention_workspace_bytes(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = None,
@@ -185,8 +187,8 @@ def _check_lse(lse, heads, tokens, device: int):
         raise ValueError(f"lse must be a dense float32 [{heads}][{tokens}] on device {device}")
 
 
-# bfp8_attention_shape.clear
-_CLEAR_O, _CLEAR_LSE, _CLEAR_DQ, _CLEAR_DK, _CLEAR_DV = 1, 2, 4, 8, 16
+# BFP8_CLEAR_* in bfp8_attention_shape.causal
+_CLEAR_O, _CLEAR_LSE, _CLEAR_DQ, _CLEAR_DK, _CLEAR_DV = (1 << i for i in range(8, 13))
 
 
 def attention_forward(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = None,
@@ -206,8 +208,8 @@ def attention_forward(q, k, v, cu_q=None, cu_k=None, k_lens=None, batch: int = N
                 results that the call allocates.
     A workspace is allocated when the library asks for one and none is given."""
     device, s, qh, kh, vh, qs, _ = _problem(q, k, v, cu_q, cu_k, k_lens, batch, causal, scale)
-    s.clear = ((_CLEAR_O if out is None or zero_rest else 0)
-               | (_CLEAR_LSE if lse is None or zero_rest else 0))
+    s.causal |= ((_CLEAR_O if out is None or zero_rest else 0)
+                 | (_CLEAR_LSE if lse is None or zero_rest else 0))
     out, oh = _result(out, q, "out", device, qs)
     if lse is None:
         lse = torch.empty(qs[1], qs[0], dtype=torch.float32, device=q.device)
@@ -232,9 +234,9 @@ def attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, k_lens=Non
     _, _, oh = _heads(out, "out", _BF16, device, qs)
     _, _, doh = _heads(dout, "dout", _BF16, device, qs)
     _check_lse(lse, s.heads, s.total_q, device)
-    s.clear = ((_CLEAR_DQ if dq is None or zero_rest else 0)
-               | (_CLEAR_DK if dk is None or zero_rest else 0)
-               | (_CLEAR_DV if dv is None or zero_rest else 0))
+    s.causal |= ((_CLEAR_DQ if dq is None or zero_rest else 0)
+                 | (_CLEAR_DK if dk is None or zero_rest else 0)
+                 | (_CLEAR_DV if dv is None or zero_rest else 0))
     dq, dqh = _result(dq, q, "dq", device, qs)
     dk, dkh = _result(dk, k, "dk", device, ks)
     dv, dvh = _result(dv, v, "dv", device, ks)

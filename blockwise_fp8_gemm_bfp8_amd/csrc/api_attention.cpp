@@ -43,9 +43,8 @@ bfp8_status check_shape(const bfp8_attention_shape* s) {
   // rows of a kv head (queries times heads of its group) are counted in 32 bits
   if (s->total_q * (s->heads / s->kv_heads) >= limit) return BFP8_ERR_SHAPE;
   if (s->head_dim <= 0 || s->head_dim > 128 || s->head_dim % 8 != 0) return BFP8_ERR_SHAPE;
-  if (s->causal != 0 && s->causal != 1) return BFP8_ERR_SHAPE;
+  if ((s->causal & ~(1 | kClearAll)) != 0) return BFP8_ERR_SHAPE;
   if (!(s->scale > 0.0f) || isinf(s->scale)) return BFP8_ERR_SHAPE;
-  if (s->clear < 0 || s->clear > kClearAll) return BFP8_ERR_SHAPE;
   if (s->batch == 0) return s->total_q == 0 && s->total_k == 0 ? BFP8_OK : BFP8_ERR_SHAPE;
   if (s->cu_q == nullptr && s->total_q % s->batch != 0) return BFP8_ERR_SHAPE;
   if (s->cu_k == nullptr && s->total_k % s->batch != 0) return BFP8_ERR_SHAPE;
@@ -64,7 +63,7 @@ AttentionArgs make_args(const bfp8_attention_shape& s) {
   a.kv_heads = s.kv_heads;
   a.group = s.heads / s.kv_heads;
   a.head_dim = s.head_dim;
-  a.causal = s.causal;
+  a.causal = s.causal & 1;
   a.scale = s.scale;
   a.scale_log2 = static_cast<float>(s.scale * 1.4426950408889634);
   return a;
@@ -180,7 +179,7 @@ bfp8_status bfp8_attention_forward(const bfp8_attention_shape* shape, bfp8_heads
   a.v = as_heads(v);
   a.o = as_heads(o);
   a.lse = lse;
-  if (s.cu_q != nullptr) a.clear = s.clear & (BFP8_CLEAR_O | BFP8_CLEAR_LSE);
+  if (s.cu_q != nullptr) a.clear = s.causal & (BFP8_CLEAR_O | BFP8_CLEAR_LSE);
   return launch_attention_forward(a, workspace, workspace_bytes, stream);
 }
 
@@ -218,8 +217,8 @@ bfp8_status bfp8_attention_backward(const bfp8_attention_shape* shape, bfp8_head
   a.dk = as_heads(dk);
   a.dv = as_heads(dv);
   a.lse = const_cast<float*>(lse);
-  if (s.cu_q != nullptr) a.clear |= s.clear & BFP8_CLEAR_DQ;
-  if (s.cu_k != nullptr) a.clear |= s.clear & (BFP8_CLEAR_DK | BFP8_CLEAR_DV);
+  if (s.cu_q != nullptr) a.clear |= s.causal & BFP8_CLEAR_DQ;
+  if (s.cu_k != nullptr) a.clear |= s.causal & (BFP8_CLEAR_DK | BFP8_CLEAR_DV);
   return launch_attention_backward(a, workspace, stream);
 }
 

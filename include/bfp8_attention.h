@@ -114,14 +114,15 @@ bfp8_status bfp8_rope(const void* x, int64_t x_row, int64_t x_head, void* y, int
  * tensors' rows, so no entry makes them read or write elsewhere.
  *
  * Rows before cu[0] and from cu[batch] on belong to no sequence.  A result
- * keeps what it held there, unless `clear` names it: then it is 0 (L: -inf).
+ * keeps what it held there, unless the bit added to `causal` names it: then it is
+ * 0 (L: -inf).
  */
 enum {
-  BFP8_CLEAR_O = 1, /* of the forward call */
-  BFP8_CLEAR_LSE = 2,
-  BFP8_CLEAR_DQ = 4, /* of the backward call */
-  BFP8_CLEAR_DK = 8,
-  BFP8_CLEAR_DV = 16
+  BFP8_CLEAR_O = 1 << 8, /* of the forward call */
+  BFP8_CLEAR_LSE = 1 << 9,
+  BFP8_CLEAR_DQ = 1 << 10, /* of the backward call */
+  BFP8_CLEAR_DK = 1 << 11,
+  BFP8_CLEAR_DV = 1 << 12
 };
 typedef struct {
   int64_t batch;
@@ -132,9 +133,8 @@ typedef struct {
   const int32_t* k_lens;
   int heads, kv_heads; /* heads a multiple of kv_heads */
   int head_dim;        /* a multiple of 8, at most 128 */
-  int causal;          /* 0 or 1 */
+  int causal;          /* 0 or 1, plus BFP8_CLEAR_* of the results to clear */
   float scale;
-  int clear;           /* a sum of BFP8_CLEAR_*, 0: none */
 } bfp8_attention_shape;
 
 /* A tensor of heads: pointer and strides in elements (see the top). */

@@ -120,12 +120,19 @@ def test_each_result_by_itself():
     assert (rest(dq, mine) == 0).all() and (rest(dv, keys) == 0).all()
 
 
+def test_causal_is_a_truth_value():
+    q = torch.zeros((4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for causal in (2, 1 << 8, -1):
+        with pytest.raises(ValueError, match="causal"):
+            bfp8.attention_forward(q, q, q, causal=causal)
+
+
 def test_clear_is_checked():
-    """An unknown bit of `clear` is refused before any HIP call."""
-    s = bfp8.AttentionShape(1, 4, 4, 0x10000, 0x10000, None, 1, 1, 64, 1, 0.125, 32)
+    """An unknown bit is refused before any HIP call."""
     h = bfp8.Heads(0x10000, 64, 64)
-    assert bfp8.lib().bfp8_attention_forward(ctypes.byref(s), h, h, h, h, 0x10000, None, 0,
-                                             None) == 2
-    s.clear = -1
-    assert bfp8.lib().bfp8_attention_workspace_bytes(ctypes.byref(s), 0) == \
-        ctypes.c_size_t(-1).value
+    for causal in (2, 1 << 7, 1 << 13, 1 | 1 << 14, -1):
+        s = bfp8.AttentionShape(1, 4, 4, 0x10000, 0x10000, None, 1, 1, 64, causal, 0.125)
+        assert bfp8.lib().bfp8_attention_forward(ctypes.byref(s), h, h, h, h, 0x10000, None, 0,
+                                                 None) == 2
+        assert bfp8.lib().bfp8_attention_workspace_bytes(ctypes.byref(s), 0) == \
+            ctypes.c_size_t(-1).value
