@@ -49,8 +49,6 @@ class AttentionBlock:
                 raise ValueError(f"{name} must be a multiple of 128, got {n}")
         self.w_qkv, self.w_o = w_qkv, w_o
         self.heads, self.kv_heads, self.head_dim, self.scale = heads, kv_heads, D, scale
-        if positions is None:  # token t stands at t
-            positions = torch.arange(tokens, dtype=torch.int32, device=w_qkv.device)
         self.cu, self.positions, self.table = cu, positions, table
         self._quantized = self._ran = False  # what the buffers hold
         dev, M, E = w_qkv.device, tokens, heads * D
@@ -70,7 +68,6 @@ class AttentionBlock:
         b["qkv"], b["dqkv"] = new((M, heads + 2 * kv_heads, D), bf), new((M, heads + 2 * kv_heads, D), bf)
         b["a"], b["da"] = new((M, heads, D), bf), new((M, heads, D), bf)
         b["lse"] = new((heads, M), f32)
-        b["positions"] = new((M,), torch.int32)
         b["y"], b["dx"] = new((M, hidden), bf), new((M, hidden), bf)
         b["dw_qkv"], b["dw_o"] = new((rows, hidden), bf), new((hidden, E), bf)
         need = max(gemm_workspace_bytes("NT", "act_km", "act_km", rows, hidden, M),
@@ -93,12 +90,7 @@ class AttentionBlock:
 
     def _turn(self, rows, inverse):
         turned = rows[:, :self.heads + self.kv_heads]
-        positions = self.positions
-        if inverse:
-            # A position outside the table turns even a zero row into NaN.  A token of a
-            # sequence with such a position has had its NaN in the forward pass.
-            positions = torch.clamp(positions, 0, self.table.shape[0] - 1, out=self.buf["positions"])
-        rope(turned, self.table, positions, inverse=inverse, out=turned)
+        rope(turned, self.table, self.positions, inverse=inverse, out=turned)
 
     def quantize_weights(self):
         """Codes of both weights, once per optimizer step (and before the first forward)."""

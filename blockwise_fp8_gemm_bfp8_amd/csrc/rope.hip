@@ -68,6 +68,11 @@ __device__ __forceinline__ void store_values(T* p, const float (&x)[N]) {
   *reinterpret_cast<typename Values<T, N>::V*>(p) = w;
 }
 
+// A pair (a, b) turned by an angle that is not known: NaN, but a zero stays one.
+__device__ __forceinline__ void turn_unknown(float a, float b, float& ya, float& yb) {
+  ya = yb = a == 0.0f && b == 0.0f ? 0.0f : NAN;
+}
+
 // A unit is V pairs of one head (2 V values), or 2 V of its values past
 // rot_dim, which are copied.  A workgroup's threads are `slots` heads of
 // `units` units each; consecutive slots are consecutive heads, then tokens.
@@ -96,7 +101,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int units, int sl
   load_values<float, 2 * V>(a.table + ((inside ? p : 0) * half + u * V) * 2, cs);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    c[e] = inside ? cs[2 * e] : NAN;
+    c[e] = cs[2 * e];
     s[e] = a.inverse ? -cs[2 * e + 1] : cs[2 * e + 1];
   }
   if (INTERLEAVED) {
@@ -106,6 +111,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int units, int sl
     for (int e = 0; e < V; ++e) {
       r[2 * e] = w[2 * e] * c[e] - w[2 * e + 1] * s[e];
       r[2 * e + 1] = w[2 * e] * s[e] + w[2 * e + 1] * c[e];
+      if (!inside) turn_unknown(w[2 * e], w[2 * e + 1], r[2 * e], r[2 * e + 1]);
     }
     store_values<T, 2 * V>(y + u * 2 * V, r);
   } else {
@@ -116,6 +122,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int units, int sl
     for (int e = 0; e < V; ++e) {
       r0[e] = w0[e] * c[e] - w1[e] * s[e];
       r1[e] = w0[e] * s[e] + w1[e] * c[e];
+      if (!inside) turn_unknown(w0[e], w1[e], r0[e], r1[e]);
     }
     store_values<T, V>(y + u * V, r0);
     store_values<T, V>(y + half + u * V, r1);

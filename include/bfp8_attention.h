@@ -76,7 +76,8 @@ bfp8_status bfp8_rope_table(float* table, int64_t positions, int rot_dim, double
  *   table      [table_rows][rot_dim/2][2] from bfp8_rope_table
  *   positions  int32 [tokens], or NULL: token t stands at position t.  A
  *              token whose position is outside [0, table_rows) gets NaN in
- *              its turned values.
+ *              its turned values, but a pair of zeros stays zero: so padding
+ *              may stand at any position, -1 among them.
  *   inverse    0, or 1: turns by -p f_i, which is the gradient: dx from dy
  *              (the transpose of the turn, so the factor m stays).
  * head_dim * (size of dt) is a multiple of 16 bytes; rot_dim is even and
