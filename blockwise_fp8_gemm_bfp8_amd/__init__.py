@@ -29,6 +29,15 @@ Between the QKV and output projections (include/bfp8_attention.h; module attenti
   rope(x, table, positions, ...)       -> x with its heads' pairs turned (or turned back)
   attention_forward(q, k, v, ...)      -> (o bf16 [T][H][D], lse f32 [H][T])
   attention_backward(dout, q, k, v, o, lse, ...) -> (dq, dk, dv)
+Around the linears and after them (include/bfp8_layer.h; module layer):
+  rmsnorm(x, weight, residual)         -> (y, r = x + residual, rstd)
+  rmsnorm_quantize(x, weight, residual, scales, transposed) -> (q, s[, qt, st], r, rstd)
+  rmsnorm_backward(dy, r, weight, rstd, dsum) -> (dx, dweight f32)
+  swiglu(gate, up)                     -> silu(gate) * up
+  swiglu_quantize(gate, up, scales, transposed) -> (q, s[, qt, st])
+  swiglu_backward(dh, gate, up)        -> (dgate, dup)
+  swiglu_backward_quantize(dh, gate, up, scales, transposed) -> the codes of [dgate | dup]
+  grad_norm(grads), clip_grads(grads, max_norm), GradClip(grads, out): the global norm
 """
 
 import ctypes
@@ -63,6 +72,17 @@ __all__ = [
     "attention_forward",
     "attention_backward",
     "attention_workspace_bytes",
+    "rmsnorm",
+    "rmsnorm_quantize",
+    "rmsnorm_backward",
+    "rmsnorm_backward_workspace_bytes",
+    "swiglu",
+    "swiglu_quantize",
+    "swiglu_backward",
+    "swiglu_backward_quantize",
+    "grad_norm",
+    "clip_grads",
+    "GradClip",
     "lib",
     "BFP8Error",
     "STATUS",
@@ -110,6 +130,19 @@ class Heads(ctypes.Structure):
     _fields_ = [("data", _vp), ("row", _i64), ("head", _i64)]
 
 
+class GradJob(ctypes.Structure):
+    """bfp8_grad_job."""
+    _fields_ = [("g", _vp), ("out", _vp), ("rows", _i64), ("cols", _i64), ("ldg", _i64),
+                ("ldo", _i64), ("dt", _i64)]
+
+
+_f32 = ctypes.c_float
+_size = ctypes.c_size_t
+_jobs = ctypes.POINTER(GradJob)
+_norm_head = [_vp, _i64, _vp, _i64, _vp, _int, _int, _i64, _i64]  # x, residual, w, dtypes, sizes
+_glu_head = [_vp, _i64, _vp, _i64, _int, _i64, _i64]              # gate, up, dtype, sizes
+_codes = [_int, _vp, _i64, _vp, _vp, _i64, _vp]                   # format, q, s, qt, st
+
 _SIGNATURES = {
     "bfp8_quantize_act": [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _vp],
     "bfp8_quantize_act_transposed": [_vp, _int, _i64, _i64, _i64, _vp, _i64, _vp, _vp],
@@ -143,12 +176,26 @@ _SIGNATURES = {
                                _vp, ctypes.c_size_t, _vp],
     "bfp8_attention_backward": [ctypes.POINTER(AttentionShape), Heads, Heads, Heads, Heads, _vp,
                                 Heads, Heads, Heads, Heads, _vp, ctypes.c_size_t, _vp],
+    "bfp8_rmsnorm": [*_norm_head, _f32, _vp, _i64, _vp, _i64, _vp, _vp],
+    "bfp8_rmsnorm_quantize": [*_norm_head, _f32, _vp, _i64, _vp, *_codes, _vp],
+    "bfp8_rmsnorm_backward": [_vp, _i64, _vp, _i64, _vp, _int, _vp, _vp, _i64, _int, _i64, _i64, _vp,
+                              _i64, _vp, _vp, _size, _vp],
+    "bfp8_rmsnorm_backward_workspace_bytes": [_i64, _i64],
+    "bfp8_swiglu": [*_glu_head, _vp, _i64, _vp],
+    "bfp8_swiglu_quantize": [*_glu_head, *_codes, _vp],
+    "bfp8_swiglu_backward": [_vp, _i64, *_glu_head, _vp, _i64, _vp, _i64, _vp],
+    "bfp8_swiglu_backward_quantize": [_vp, _i64, *_glu_head, *_codes, _vp],
+    "bfp8_grad_norm": [_jobs, _i64, _vp, _vp, _size, _vp],
+    "bfp8_grad_norm_workspace_bytes": [_jobs, _i64],
+    "bfp8_grad_clip": [_jobs, _i64, _vp, _f32, _vp],
     "bfp8_status_str": [_int],
     "bfp8_abi_version": [],
 }
 _RESTYPES = {
     "bfp8_gemm_workspace_bytes": ctypes.c_size_t,
     "bfp8_attention_workspace_bytes": ctypes.c_size_t,
+    "bfp8_rmsnorm_backward_workspace_bytes": ctypes.c_size_t,
+    "bfp8_grad_norm_workspace_bytes": ctypes.c_size_t,
     "bfp8_status_str": ctypes.c_char_p,
 }
 
@@ -539,3 +586,6 @@ def gemm_mx(layout: str, qa, sa, qb, sb, mode_a: str = "act", mode_b: str = "blo
 
 from .attention import (attention_backward, attention_forward,  # noqa: E402
                         attention_workspace_bytes, rope, rope_table)
+from .layer import (GradClip, clip_grads, grad_norm, rmsnorm, rmsnorm_backward,  # noqa: E402
+                    rmsnorm_backward_workspace_bytes, rmsnorm_quantize, swiglu, swiglu_backward,
+                    swiglu_backward_quantize, swiglu_quantize)

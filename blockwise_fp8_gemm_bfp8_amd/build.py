@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libbfp8.so")
 SOURCES = ["api.cpp", "api_attention.cpp", "quantize.hip", "gemm.hip", "rope.hip", "attention.hip",
-           "attention_bwd.hip"]
+           "attention_bwd.hip", "api_layer.cpp", "norm.hip", "glu.hip", "clip.hip"]
 ARCH = "gfx950"
 
 

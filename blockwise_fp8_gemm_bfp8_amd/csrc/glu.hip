@@ -1,0 +1,151 @@
+// The gated activation, its gradient, and the codes of either (bfp8_layer.h).
+// Element by element and memory-bound: every input is read once and only
+// results are written; in the tiles of codes the values stay in registers
+// between the row groups and the token groups.
+
+#include "layer.h"
+
+namespace bfp8 {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// e = exp(-g), at most 2^126 so that e / (1 + e) below stays a number where
+// sigma(g) is already 0 to float32.
+__device__ __forceinline__ float exp_minus(float g) {
+  return __builtin_amdgcn_exp2f(fminf(g * -kLog2e, 126.0f));
+}
+
+__device__ __forceinline__ float silu_gate(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + exp_minus(g)) * u;
+}
+
+// sigma(g) (1 + g (1 - sigma(g))), with 1 - sigma(g) = e sigma(g) free of
+// cancellation.
+__device__ __forceinline__ void silu_gate_grad(float dh, float g, float u, float& dg, float& du) {
+  const float e = exp_minus(g);
+  const float s = __builtin_amdgcn_rcpf(1.0f + e);
+  dg = dh * u * (s * fmaf(g, e * s, 1.0f));
+  du = dh * (g * s);
+}
+
+// Vectors of 8 values, one a thread.
+template <typename T, bool GRAD>
+__global__ __launch_bounds__(256) void glu_values_kernel(GluArgs a, unsigned per_row, unsigned count) {
+  const unsigned item = blockIdx.x * 256u + threadIdx.x;
+  if (item >= count) return;
+  const unsigned row = item / per_row;
+  const int64_t c = static_cast<int64_t>(item - row * per_row) * 8;
+  const int n = valid8(c, a.cols);
+  Raw8<T> g, u, dh;
+  g.load(a.gate, row * a.ldg + c, n);
+  u.load(a.up, row * a.ldu + c, n);
+  if (GRAD) dh.load(a.dh, row * a.lddh + c, n);
+  float x[8], y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (GRAD) silu_gate_grad(dh.get(i), g.get(i), u.get(i), x[i], y[i]);
+    else x[i] = silu_gate(g.get(i), u.get(i));
+  }
+  store8(static_cast<T*>(a.a) + row * a.lda + c, x, n);
+  if (GRAD) store8(static_cast<T*>(a.b) + row * a.ldb + c, y, n);
+}
+
+// Row groups: 16 lanes a chunk of 128 columns.  With K-block-major scales
+// neighbouring chunks are neighbouring rows of one column block, whose scales
+// lie side by side.
+template <typename T, int FORMAT, bool GRAD>
+__global__ __launch_bounds__(256) void glu_rows_kernel(GluArgs a, unsigned chunks, unsigned per_row,
+                                                       CodesOut o) {
+  const unsigned chunk = blockIdx.x * 16u + (threadIdx.x >> 4);
+  if (chunk >= chunks) return;
+  const int lane16 = threadIdx.x & 15;
+  const unsigned rows = static_cast<unsigned>(a.rows);
+  const unsigned block = Codes<FORMAT>::kMajor ? chunk / rows : chunk % per_row;
+  const int64_t row = Codes<FORMAT>::kMajor ? chunk - block * rows : chunk / per_row;
+  const int64_t c0 = static_cast<int64_t>(block) * 128, c = c0 + lane16 * 8;
+  Raw8<T> g, u, dh;
+  g.load(a.gate, row * a.ldg + c, 8);
+  u.load(a.up, row * a.ldu + c, 8);
+  if (GRAD) dh.load(a.dh, row * a.lddh + c, 8);
+  float x[8], y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (GRAD) silu_gate_grad(dh.get(i), g.get(i), u.get(i), x[i], y[i]);
+    else x[i] = silu_gate(g.get(i), u.get(i));
+  }
+  emit_row_chunk<FORMAT>(o, row, c0, lane16, x);
+  if (GRAD) emit_row_chunk<FORMAT>(o, row, a.cols + c0, lane16, y);
+}
+
+template <typename T, int FORMAT, bool GRAD>
+__global__ __launch_bounds__(kTileThreads) void glu_tile_kernel(GluArgs a, unsigned col_tiles,
+                                                                CodesOut o) {
+  __shared__ __attribute__((aligned(16))) TileShared sh;
+  const unsigned tm = blockIdx.x / col_tiles, tc = blockIdx.x - tm * col_tiles;
+  const int64_t m0 = static_cast<int64_t>(tm) * 128, c0 = static_cast<int64_t>(tc) * 128;
+  const int64_t c = c0 + (threadIdx.x & 15) * 8, m = m0 + (threadIdx.x >> 4) * 4;
+  Raw8<T> g[4], u[4], dh[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    g[i].load(a.gate, (m + i) * a.ldg + c, 8);
+    u[i].load(a.up, (m + i) * a.ldu + c, 8);
+    if (GRAD) dh[i].load(a.dh, (m + i) * a.lddh + c, 8);
+  }
+  float x[4][8], y[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (GRAD) silu_gate_grad(dh[i].get(k), g[i].get(k), u[i].get(k), x[i][k], y[i][k]);
+      else x[i][k] = silu_gate(g[i].get(k), u[i].get(k));
+    }
+  emit_tile<FORMAT>(o, m0, c0, x, sh);
+  if (GRAD) emit_tile<FORMAT>(o, m0, a.cols + c0, y, sh);
+}
+
+template <typename T, bool GRAD>
+bfp8_status values_typed(const GluArgs& a, hipStream_t stream) {
+  const int64_t per_row = (a.cols + 7) / 8, count = a.rows * per_row, blocks = (count + 255) / 256;
+  if (!threads_fit(blocks, 256)) return BFP8_ERR_SHAPE;
+  return launch(glu_values_kernel<T, GRAD>, dim3(static_cast<unsigned>(blocks)), dim3(256), stream,
+                a, static_cast<unsigned>(per_row), static_cast<unsigned>(count));
+}
+
+template <typename T, bool GRAD>
+bfp8_status codes_typed(const GluArgs& a, bfp8_code_format format, const CodesOut& o,
+                        hipStream_t stream) {
+  const int64_t per_row = a.cols / 128;
+  if (o.qt == nullptr) {
+    const int64_t chunks = a.rows * per_row, blocks = (chunks + 15) / 16;
+    if (!threads_fit(blocks, 256)) return BFP8_ERR_SHAPE;
+    return BFP8_WITH_FORMAT(
+        format, (launch(glu_rows_kernel<T, F, GRAD>, dim3(static_cast<unsigned>(blocks)), dim3(256),
+                        stream, a, static_cast<unsigned>(chunks), static_cast<unsigned>(per_row), o)));
+  }
+  const int64_t tiles = a.rows / 128 * per_row;
+  return BFP8_WITH_FORMAT(
+      format, (launch(glu_tile_kernel<T, F, GRAD>, dim3(static_cast<unsigned>(tiles)),
+                      dim3(kTileThreads), stream, a, static_cast<unsigned>(per_row), o)));
+}
+
+}  // namespace
+
+bfp8_status launch_swiglu(const GluArgs& a, bfp8_in_dtype dt, hipStream_t stream) {
+  if (a.dh == nullptr)
+    return dt == BFP8_IN_F32 ? values_typed<float, false>(a, stream)
+                             : values_typed<uint16_t, false>(a, stream);
+  return dt == BFP8_IN_F32 ? values_typed<float, true>(a, stream)
+                           : values_typed<uint16_t, true>(a, stream);
+}
+
+bfp8_status launch_swiglu_quantize(const GluArgs& a, bfp8_in_dtype dt, bfp8_code_format format,
+                                   const CodesOut& o, hipStream_t stream) {
+  if (a.dh == nullptr)
+    return dt == BFP8_IN_F32 ? codes_typed<float, false>(a, format, o, stream)
+                             : codes_typed<uint16_t, false>(a, format, o, stream);
+  return dt == BFP8_IN_F32 ? codes_typed<float, true>(a, format, o, stream)
+                           : codes_typed<uint16_t, true>(a, format, o, stream);
+}
+
+}  // namespace bfp8

@@ -1,0 +1,324 @@
+// RMS norm with the residual's addition, its codes, and its gradient
+// (bfp8_layer.h).  All of it is memory-bound: a handful of VALU operations per
+// value, so a row is read once, kept in registers between its sum of squares
+// and its use, and nothing but outputs is written.
+
+#include <algorithm>
+
+#include "layer.h"
+
+namespace bfp8 {
+namespace {
+
+// Sum over the 16 lanes of a DPP row, in every lane.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false));
+  return v;
+}
+
+// Sum over the TPR threads of a row, in every one of them.  Rows of more than
+// a wave are a workgroup's, and its `parts` in LDS are free again only after
+// the next barrier: two are used in turn.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* parts) {
+  v = row16_sum(v);
+  if (TPR == 16) return v;
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  if (TPR == 64) return v;
+  if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < TPR / 64; ++w) v += parts[w];
+  return v;
+}
+
+// The weight's values of this thread's columns.
+template <int TPR, int NV>
+__device__ __forceinline__ void load_weight(const void* w, bool f32, int lane, int cols,
+                                            float (&v)[NV][8]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * TPR + lane) * 8, n = valid8(c, cols);
+    if (f32) Load8<float>::run(static_cast<const float*>(w) + c, v[j], n);
+    else Load8<uint16_t>::run(static_cast<const uint16_t*>(w) + c, v[j], n);
+  }
+}
+
+constexpr int block_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+// What a pass over the rows leaves beside r and rstd.
+constexpr int kStats = -2, kValues = -1;  // otherwise a bfp8_code_format
+
+// TPR threads a row, NV vectors of 8 values a thread: vector j of a thread
+// holds columns 8 (j TPR + lane), so that a wave's loads are contiguous and 16
+// lanes hold a 128-group.
+template <typename T, int TPR, int NV, int OUT>
+__global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs a, CodesOut o) {
+  __shared__ float parts[2][TPR < 256 ? 1 : TPR / 64];
+  constexpr int kRows = block_threads(TPR) / TPR;  // of a workgroup at once
+  const int lane = threadIdx.x % TPR;
+  float w[NV][8];
+  if (OUT != kStats) load_weight<TPR, NV>(a.w, a.w_f32, lane, a.cols, w);
+  int turn = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR; row < a.rows;
+       row += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
+    Raw8<T> x[NV], y[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8, n = valid8(c, a.cols);
+      x[j].load(a.x, row * a.ldx + c, n);
+      if (a.residual != nullptr) y[j].load(a.residual, row * a.ldres + c, n);
+    }
+    float r[NV][8], square = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8, n = valid8(c, a.cols);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[j][i] = x[j].get(i);
+      if (a.residual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[j][i] += y[j].get(i);
+        if (sizeof(T) == 2) {  // the norm is of the stored sum
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const uint32_t b = pack_bf16x2(r[j][i], r[j][i + 1]);
+            r[j][i] = __uint_as_float(b << 16);
+            r[j][i + 1] = __uint_as_float(b & 0xFFFF0000u);
+          }
+        }
+        store8(static_cast<T*>(a.sum) + row * a.ldsum + c, r[j], n);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) square = fmaf(r[j][i], r[j][i], square);
+    }
+    square = row_sum<TPR>(square, parts[turn]);
+    const float rstd = 1.0f / sqrtf(square / static_cast<float>(a.cols) + a.eps);
+    if (lane == 0) a.rstd[row] = rstd;
+    if (OUT == kStats) continue;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8, n = valid8(c, a.cols);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = r[j][i] * rstd * w[j][i];
+      if (OUT == kValues) store8(static_cast<T*>(a.y) + row * a.ldy + c, v, n);
+      else if (n > 0) emit_row_chunk<OUT < 0 ? 0 : OUT>(o, row, c & ~127, lane & 15, v);
+    }
+  }
+}
+
+// The threads and vectors of a row: the fewest that hold it.
+#define BFP8_WITH_ROW(cols, CALL)                                               \
+  ((cols) <= 128     ? [&] { constexpr int P = 16, V = 1; return CALL; }()      \
+   : (cols) <= 512   ? [&] { constexpr int P = 64, V = 1; return CALL; }()      \
+   : (cols) <= 1024  ? [&] { constexpr int P = 64, V = 2; return CALL; }()      \
+   : (cols) <= 2048  ? [&] { constexpr int P = 64, V = 4; return CALL; }()      \
+   : (cols) <= 4096  ? [&] { constexpr int P = 256, V = 2; return CALL; }()     \
+   : (cols) <= 8192  ? [&] { constexpr int P = 256, V = 4; return CALL; }()     \
+                     : [&] { constexpr int P = 1024, V = 2; return CALL; }())
+
+template <typename T, int TPR, int NV, int OUT>
+bfp8_status launch_rows(const NormArgs& a, const CodesOut& o, hipStream_t stream) {
+  constexpr int kRows = block_threads(TPR) / TPR;
+  const int64_t blocks = std::min<int64_t>((a.rows + kRows - 1) / kRows, 1 << 16);
+  return launch(norm_rows_kernel<T, TPR, NV, OUT>, dim3(static_cast<unsigned>(blocks)),
+                dim3(block_threads(TPR)), stream, a, o);
+}
+template <typename T, int OUT>
+bfp8_status launch_rows_of(const NormArgs& a, const CodesOut& o, hipStream_t stream) {
+  return BFP8_WITH_ROW(a.cols, (launch_rows<T, P, V, OUT>(a, o, stream)));
+}
+
+// Both layouts' codes of a tile from r and the rows' statistics.  A row's
+// statistics need the whole row and a token group needs 128 rows, which no
+// workgroup holds at once: so r is read a second time, from the last-level
+// cache where it fits.
+template <typename T, int FORMAT>
+__global__ __launch_bounds__(kTileThreads) void norm_tile_kernel(const void* r, int64_t ldr,
+                                                                 const float* rstd, const void* w,
+                                                                 bool w_f32, unsigned col_tiles,
+                                                                 CodesOut o) {
+  __shared__ __attribute__((aligned(16))) TileShared sh;
+  const unsigned tm = blockIdx.x / col_tiles, tc = blockIdx.x - tm * col_tiles;
+  const int64_t m0 = static_cast<int64_t>(tm) * 128, c0 = static_cast<int64_t>(tc) * 128;
+  const int lane16 = threadIdx.x & 15, rsub = threadIdx.x >> 4;
+  Raw8<T> raw[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) raw[u].load(r, (m0 + 4 * rsub + u) * ldr + c0 + lane16 * 8, 8);
+  float wv[8], v[4][8];
+  if (w_f32) Load8<float>::run(static_cast<const float*>(w) + c0 + lane16 * 8, wv, 8);
+  else Load8<uint16_t>::run(static_cast<const uint16_t*>(w) + c0 + lane16 * 8, wv, 8);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float rs = rstd[m0 + 4 * rsub + u];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[u][k] = raw[u].get(k) * rs * wv[k];
+  }
+  emit_tile<FORMAT>(o, m0, c0, v, sh);
+}
+
+template <typename T>
+bfp8_status quantize_typed(const NormArgs& a, bfp8_code_format format, const CodesOut& o,
+                           hipStream_t stream) {
+  if (o.qt == nullptr) return BFP8_WITH_FORMAT(format, (launch_rows_of<T, F>(a, o, stream)));
+  const bfp8_status st = launch_rows_of<T, kStats>(a, o, stream);
+  if (st != BFP8_OK) return st;
+  const bool added = a.residual != nullptr;
+  const int64_t col_tiles = a.cols / 128, tiles = a.rows / 128 * col_tiles;
+  return BFP8_WITH_FORMAT(
+      format, (launch(norm_tile_kernel<T, F>, dim3(static_cast<unsigned>(tiles)),
+                      dim3(kTileThreads), stream, added ? a.sum : a.x, added ? a.ldsum : a.ldx,
+                      a.rstd, a.w, a.w_f32, static_cast<unsigned>(col_tiles), o)));
+}
+
+// ---- gradient ------------------------------------------------------------------
+
+// Rows in turn, the weight and this workgroup's share of dw in registers; the
+// waves' shares meet in LDS at the end and leave as one row of `partial`.
+template <typename T, int TPR, int NV>
+__global__ __launch_bounds__(block_threads(TPR)) void norm_grad_kernel(NormGradArgs a) {
+  constexpr int kThreads = block_threads(TPR), kRows = kThreads / TPR;
+  __shared__ float parts[2][TPR < 256 ? 1 : TPR / 64];
+  __shared__ __attribute__((aligned(16))) float joined[kRows > 1 ? kRows / 2 * TPR * NV * 8 : 4];
+  const int lane = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+  float w[NV][8], dw[NV][8];
+  load_weight<TPR, NV>(a.w, a.w_f32, lane, a.cols, w);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
+  int turn = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + slot; row < a.rows;
+       row += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
+    Raw8<T> dy[NV], r[NV], ds[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8, n = valid8(c, a.cols);
+      dy[j].load(a.dy, row * a.lddy + c, n);
+      r[j].load(a.r, row * a.ldr + c, n);
+      if (a.dsum != nullptr) ds[j].load(a.dsum, row * a.lddsum + c, n);
+    }
+    const float rstd = a.rstd[row];
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float p = dy[j].get(i) * (r[j].get(i) * rstd);
+        dw[j][i] += p;
+        dot = fmaf(p, w[j][i], dot);
+      }
+    const float mean = row_sum<TPR>(dot, parts[turn]) / static_cast<float>(a.cols);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8, n = valid8(c, a.cols);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = r[j].get(i) * rstd;
+        v[i] = rstd * (dy[j].get(i) * w[j][i] - t * mean);
+        if (a.dsum != nullptr) v[i] += ds[j].get(i);
+      }
+      store8(static_cast<T*>(a.dx) + row * a.lddx + c, v, n);
+    }
+  }
+  // the upper half of the slots gives its sums to the lower half, until one is left
+#pragma unroll
+  for (int half = kRows / 2; half > 0; half /= 2) {
+    if (slot >= half && slot < 2 * half) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          joined[(((slot - half) * NV + j) * 8 + i) * TPR + lane] = dw[j][i];
+    }
+    __syncthreads();
+    if (slot < half) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[j][i] += joined[((slot * NV + j) * 8 + i) * TPR + lane];
+    }
+    __syncthreads();
+  }
+  if (slot == 0) {
+    float* p = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * TPR + lane) * 8, n = valid8(c, a.cols);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) p[c + i] = dw[j][i];
+    }
+  }
+}
+
+// dw [cols] as the sum of `groups` rows of partial sums: 64 columns a
+// workgroup, every 16th row a wave, the waves' sums joined in LDS.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void norm_grad_sum_kernel(const float* partial,
+                                                                       int64_t groups, int cols,
+                                                                       float* dw) {
+  __shared__ float sums[kSumWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float sum = 0.0f;
+  if (c < cols) {
+#pragma unroll 4
+    for (int64_t g = wave; g < groups; g += kSumWaves) sum += partial[g * cols + c];
+  }
+  sums[wave][lane] = sum;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSumWaves; ++k) sum += sums[k][lane];
+    dw[c] = sum;
+  }
+}
+
+template <typename T, int TPR, int NV>
+bfp8_status launch_grad(const NormGradArgs& a, int64_t groups, hipStream_t stream) {
+  return launch(norm_grad_kernel<T, TPR, NV>, dim3(static_cast<unsigned>(groups)),
+                dim3(block_threads(TPR)), stream, a);
+}
+template <typename T>
+bfp8_status launch_grad_of(const NormGradArgs& a, int64_t groups, hipStream_t stream) {
+  return BFP8_WITH_ROW(a.cols, (launch_grad<T, P, V>(a, groups, stream)));
+}
+
+}  // namespace
+
+bfp8_status launch_rmsnorm(const NormArgs& a, bfp8_in_dtype dt, hipStream_t stream) {
+  return dt == BFP8_IN_F32 ? launch_rows_of<float, kValues>(a, CodesOut{}, stream)
+                           : launch_rows_of<uint16_t, kValues>(a, CodesOut{}, stream);
+}
+
+bfp8_status launch_rmsnorm_quantize(const NormArgs& a, bfp8_in_dtype dt, bfp8_code_format format,
+                                    const CodesOut& o, hipStream_t stream) {
+  return dt == BFP8_IN_F32 ? quantize_typed<float>(a, format, o, stream)
+                           : quantize_typed<uint16_t>(a, format, o, stream);
+}
+
+int64_t norm_grad_groups(int64_t rows, int64_t cols) {
+  const int64_t at_once = cols <= 128 ? 16 : cols <= 2048 ? 4 : 1;  // rows of a workgroup
+  return std::min<int64_t>((rows + at_once - 1) / at_once, 1024);
+}
+
+bfp8_status launch_rmsnorm_backward(const NormGradArgs& a, bfp8_in_dtype dt, hipStream_t stream) {
+  const int64_t groups = norm_grad_groups(a.rows, a.cols);
+  if (groups > 0) {
+    const bfp8_status st = dt == BFP8_IN_F32 ? launch_grad_of<float>(a, groups, stream)
+                                             : launch_grad_of<uint16_t>(a, groups, stream);
+    if (st != BFP8_OK) return st;
+  }
+  return launch(norm_grad_sum_kernel, dim3((a.cols + 63) / 64), dim3(64 * kSumWaves), stream,
+                a.partial, groups, a.cols, a.dw);
+}
+
+}  // namespace bfp8

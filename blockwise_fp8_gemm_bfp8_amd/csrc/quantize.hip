@@ -20,68 +20,10 @@
 #include <algorithm>
 #include <atomic>
 
-#include "common.h"
+#include "codes.h"
 
 namespace bfp8 {
 namespace {
-
-// Eight consecutive input elements as float32.  bf16 elements are widened
-// exactly; `nvalid` (0..8) masks a ragged tail to +0.
-template <typename T>
-struct Load8;
-
-template <>
-struct Load8<uint16_t> {
-  static __device__ __forceinline__ void run(const uint16_t* p, float (&v)[8], int nvalid) {
-    if (nvalid >= 8) {
-      uint4 u = *reinterpret_cast<const uint4*>(p);
-      uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-        v[2 * i + 1] = bf16_bits_to_f32(w[i] >> 16);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < nvalid ? bf16_bits_to_f32(p[i]) : 0.0f;
-    }
-  }
-};
-
-template <>
-struct Load8<float> {
-  static __device__ __forceinline__ void run(const float* p, float (&v)[8], int nvalid) {
-    if (nvalid >= 8) {
-      float4 a = reinterpret_cast<const float4*>(p)[0];
-      float4 b = reinterpret_cast<const float4*>(p)[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < nvalid ? p[i] : 0.0f;
-    }
-  }
-};
-
-__device__ __forceinline__ float absmax8(const float (&v)[8]) {
-  float m = fabsf(v[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-  return m;
-}
-
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv) {
-  uint2 r;
-  r.x = encode4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-  r.y = encode4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-  return r;
-}
-
-// Max over the lanes of one group: 16 lanes per 128-group, 4 per 32-group.
-template <int GROUP>
-__device__ __forceinline__ float group_lanes_max(float v) {
-  return GROUP == 128 ? row16_max(v) : quad_max(v);
-}
 
 // ---------------------------------------------------------------------------
 // K1: groups along rows.  16 lanes own one 128-element chunk (8 elements

@@ -1,0 +1,375 @@
+"""Binding of include/bfp8_layer.h: the RMS norm with the residual's addition,
+the gated activation, both with E4M3 codes of their results, their gradients,
+and the norm and clipping of many gradients.
+
+Argument marshalling only, as in the package's other calls: every step runs in
+the HIP kernels of libbfp8.so on the current stream of the tensors' device.
+"""
+
+import ctypes
+
+import torch
+
+from . import DTYPES, GradJob, _check, _padded_empty, _scale_bytes, lib
+from .attention import _pointer, _stream_of
+
+CODE_FORMATS = {"fp32": 0, "mx128": 1, "mx32": 2}  # hotpath's scale formats
+_INVALID = ctypes.c_size_t(-1).value
+
+
+class _on:
+    """Launches go to the current device: makes it the tensors' where it is another."""
+
+    def __new__(cls, device):
+        return _NOTHING if torch.cuda.current_device() == device else torch.cuda.device(device)
+
+
+class _Nothing:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *_):
+        pass
+
+
+_NOTHING = _Nothing()
+
+
+def _matrix(t, name, device=None, shape=None, dtype=None):
+    """Check a matrix of activations; returns its row stride (of no account, and
+    given as one that passes, where there is one row at most)."""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    if device is not None and at != device:
+        raise ValueError(f"{name} must be on device {device}, got {at}")
+    size = t.shape
+    if len(size) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if dtype is None:
+        if t.dtype not in DTYPES:
+            raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    elif t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(size)}")
+    row, one = t.stride()
+    if one != 1 and size[1] > 1:
+        raise ValueError(f"{name} must have unit stride along its last axis")
+    return row if size[0] > 1 else max(-(-size[1] // 16) * 16, 16)
+
+
+def _result(out, like, name, device):
+    """The matrix of a result that has `like`'s shape and dtype, a new one if
+    `out` is None, and its row stride."""
+    if out is None:
+        rows, cols = like.shape
+        out = _padded_empty(rows, cols, like.dtype, like.device, 16 // like.element_size())
+        return out, out.stride(0)
+    return out, _matrix(out, name, device, like.shape, like.dtype)
+
+
+def _vector(t, name, n, device, dtypes=(torch.float32,)):
+    if t.shape != (n,) or t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a dense {' or '.join(str(d) for d in dtypes)} [{n}] on "
+                         f"device {device}")
+
+
+def _codes_out(rows, cols, scales, transposed, given, like, device):
+    """(format, [q, s] or [q, s, qt, st], their arguments) of a rows x cols result;
+    `given`: q, s, qt, st or Nones."""
+    if scales not in CODE_FORMATS:
+        raise ValueError(f"scales must be one of {sorted(CODE_FORMATS)}")
+    q, s, qt, st = given
+    if not transposed and (qt is not None or st is not None):
+        raise ValueError("qt and st are written with transposed=True only")
+    group, f32 = (32 if scales == "mx32" else 128), scales == "fp32"
+
+    def codes(t, name, r, c):
+        if t is None:
+            t = _padded_empty(r, c, torch.uint8, like.device, 16)
+            return t, t.stride(0)
+        return t, _matrix(t, name, device, (r, c), torch.uint8)
+
+    def scale(t, name, r, c):
+        shape = (r, c // 32) if group == 32 else (c // 128, r)
+        if t is None:
+            return (torch.empty(shape, dtype=torch.float32, device=like.device) if f32
+                    else _scale_bytes(*shape, like.device))
+        if (t.shape != shape or t.dtype != (torch.float32 if f32 else torch.uint8)
+                or not t.is_contiguous() or t.get_device() != device):
+            raise ValueError(f"{name} must be a dense {'float32' if f32 else 'uint8'} "
+                             f"[{shape[0]}][{shape[1]}] on device {device}")
+        return t
+
+    q, ldq = codes(q, "q", rows, cols)
+    s = scale(s, "s", rows, cols)
+    if not transposed:
+        return CODE_FORMATS[scales], [q, s], (q.data_ptr(), ldq, s.data_ptr(), None, 0, None)
+    qt, ldqt = codes(qt, "qt", cols, rows)
+    st = scale(st, "st", cols, rows)
+    return CODE_FORMATS[scales], [q, s, qt, st], (q.data_ptr(), ldq, s.data_ptr(), qt.data_ptr(),
+                                                  ldqt, st.data_ptr())
+
+
+# ---- RMS norm -----------------------------------------------------------------
+
+def _norm_inputs(x, weight, residual, sum_out, rstd):
+    device = x.get_device()
+    ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    _vector(weight, "weight", cols, device, tuple(DTYPES))
+    ldr = lds = 0
+    if residual is not None:
+        ldr = _matrix(residual, "residual", device, x.shape, x.dtype)
+        sum_out, lds = _result(sum_out, x, "sum_out", device)
+    elif sum_out is not None:
+        raise ValueError("sum_out is the sum with a residual: there is none")
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    else:
+        _vector(rstd, "rstd", rows, device)
+    head = (x.data_ptr(), ldx, _pointer(residual), ldr, weight.data_ptr(), DTYPES[weight.dtype],
+            DTYPES[x.dtype], rows, cols)
+    return device, head, sum_out, lds, rstd
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor = None,
+            eps: float = 1e-6, out: torch.Tensor = None, sum_out: torch.Tensor = None,
+            rstd: torch.Tensor = None):
+    """r = x + residual (x without one), y = r / sqrt(mean(r^2) + eps) * weight for
+    rows x [rows][cols] (bfloat16 or float32) -> (y, r, rstd float32 [rows]).
+    r and rstd are what the gradient needs; ``sum_out=residual`` adds in place.
+    See bfp8_rmsnorm."""
+    device, head, sum_out, lds, rstd = _norm_inputs(x, weight, residual, sum_out, rstd)
+    out, ldy = _result(out, x, "out", device)
+    with _on(device):
+        _check("bfp8_rmsnorm", lib().bfp8_rmsnorm(
+            *head, eps, _pointer(sum_out), lds, out.data_ptr(), ldy, rstd.data_ptr(),
+            _stream_of(device)))
+    return out, x if residual is None else sum_out, rstd
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor = None,
+                     eps: float = 1e-6, scales: str = "fp32", transposed: bool = False,
+                     q=None, s=None, qt=None, st=None, sum_out: torch.Tensor = None,
+                     rstd: torch.Tensor = None):
+    """rmsnorm with E4M3 codes of y in place of y -> (q, s, r, rstd), or with
+    ``transposed`` (q, s, qt, st, r, rstd): both layouts, for a linear's forward
+    and weight gradient.  ``scales`` is hotpath's format: "fp32" (as
+    quantize_act_dual_kmajor writes them), "mx128" (quantize_mx_act_dual_kmajor)
+    or "mx32" (quantize_mx_act_dual, group 32).  See bfp8_rmsnorm_quantize."""
+    device, head, sum_out, lds, rstd = _norm_inputs(x, weight, residual, sum_out, rstd)
+    fmt, out, args = _codes_out(*x.shape, scales, transposed, (q, s, qt, st), x, device)
+    with _on(device):
+        _check("bfp8_rmsnorm_quantize", lib().bfp8_rmsnorm_quantize(
+            *head, eps, _pointer(sum_out), lds, rstd.data_ptr(), fmt, *args, _stream_of(device)))
+    return (*out, x if residual is None else sum_out, rstd)
+
+
+def rmsnorm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    n = lib().bfp8_rmsnorm_backward_workspace_bytes(rows, cols)
+    if n == _INVALID:
+        raise ValueError("invalid sizes")
+    return n
+
+
+def rmsnorm_backward(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     dsum: torch.Tensor = None, dx: torch.Tensor = None,
+                     dweight: torch.Tensor = None, workspace: torch.Tensor = None):
+    """(dx, dweight float32 [cols]) for the gradient dy of rmsnorm's y, its r and
+    rstd, and the gradient ``dsum`` that arrives at r itself; dx is the gradient
+    of x and of the residual.  See bfp8_rmsnorm_backward."""
+    device = dy.get_device()
+    lddy = _matrix(dy, "dy")
+    rows, cols = dy.shape
+    ldr = _matrix(r, "r", device, dy.shape, dy.dtype)
+    _vector(weight, "weight", cols, device, tuple(DTYPES))
+    _vector(rstd, "rstd", rows, device)
+    lds = _matrix(dsum, "dsum", device, dy.shape, dy.dtype) if dsum is not None else 0
+    dx, lddx = _result(dx, dy, "dx", device)
+    if dweight is None:
+        dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
+    else:
+        _vector(dweight, "dweight", cols, device)
+    if workspace is None:
+        nbytes = lib().bfp8_rmsnorm_backward_workspace_bytes(rows, cols)
+        if nbytes != _INVALID:  # the call itself reports what is wrong with the sizes
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
+    nbytes = _workspace_size(workspace, device)
+    with _on(device):
+        _check("bfp8_rmsnorm_backward", lib().bfp8_rmsnorm_backward(
+            dy.data_ptr(), lddy, r.data_ptr(), ldr, weight.data_ptr(), DTYPES[weight.dtype],
+            rstd.data_ptr(), _pointer(dsum), lds, DTYPES[dy.dtype], rows, cols, dx.data_ptr(), lddx,
+            dweight.data_ptr(), _pointer(workspace), nbytes, _stream_of(device)))
+    return dx, dweight
+
+
+def _workspace_size(t, device):
+    if t is None:
+        return 0
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a dense tensor on device {device}")
+    return t.numel() * t.element_size()
+
+
+# ---- gated activation -----------------------------------------------------------
+
+def _glu_inputs(gate, up, dh=None):
+    device = gate.get_device()
+    ldg = _matrix(gate, "gate")
+    ldu = _matrix(up, "up", device, gate.shape, gate.dtype)
+    head = (gate.data_ptr(), ldg, up.data_ptr(), ldu, DTYPES[gate.dtype], *gate.shape)
+    if dh is not None:
+        head = (dh.data_ptr(), _matrix(dh, "dh", device, gate.shape, gate.dtype), *head)
+    return device, head
+
+
+def swiglu(gate: torch.Tensor, up: torch.Tensor, out: torch.Tensor = None) -> torch.Tensor:
+    """silu(gate) * up for gate, up [rows][cols] (bfloat16 or float32), usually the
+    halves of one projection's rows.  See bfp8_swiglu."""
+    device, head = _glu_inputs(gate, up)
+    out, ldh = _result(out, gate, "out", device)
+    with _on(device):
+        _check("bfp8_swiglu", lib().bfp8_swiglu(*head, out.data_ptr(), ldh, _stream_of(device)))
+    return out
+
+
+def swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, scales: str = "fp32",
+                    transposed: bool = False, q=None, s=None, qt=None, st=None):
+    """swiglu with E4M3 codes of its result in place of it -> (q, s), or with
+    ``transposed`` (q, s, qt, st); ``scales`` as for rmsnorm_quantize.  See
+    bfp8_swiglu_quantize."""
+    device, head = _glu_inputs(gate, up)
+    fmt, out, args = _codes_out(*gate.shape, scales, transposed, (q, s, qt, st), gate, device)
+    with _on(device):
+        _check("bfp8_swiglu_quantize", lib().bfp8_swiglu_quantize(*head, fmt, *args,
+                                                                  _stream_of(device)))
+    return tuple(out)
+
+
+def swiglu_backward(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
+                    dgate: torch.Tensor = None, dup: torch.Tensor = None):
+    """(dgate, dup) for the gradient dh of swiglu(gate, up).  See bfp8_swiglu_backward."""
+    device, head = _glu_inputs(gate, up, dh)
+    dgate, ldg = _result(dgate, gate, "dgate", device)
+    dup, ldu = _result(dup, gate, "dup", device)
+    with _on(device):
+        _check("bfp8_swiglu_backward", lib().bfp8_swiglu_backward(
+            *head, dgate.data_ptr(), ldg, dup.data_ptr(), ldu, _stream_of(device)))
+    return dgate, dup
+
+
+def swiglu_backward_quantize(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
+                             scales: str = "fp32", transposed: bool = False, q=None, s=None,
+                             qt=None, st=None):
+    """E4M3 codes of the rows [dgate | dup] (2 cols wide), the gradient of a
+    projection whose rows are [gate | up] -> (q, s), or with ``transposed``
+    (q, s, qt, st).  See bfp8_swiglu_backward_quantize."""
+    device, head = _glu_inputs(gate, up, dh)
+    rows, cols = gate.shape
+    fmt, out, args = _codes_out(rows, 2 * cols, scales, transposed, (q, s, qt, st), gate, device)
+    with _on(device):
+        _check("bfp8_swiglu_backward_quantize", lib().bfp8_swiglu_backward_quantize(
+            *head, fmt, *args, _stream_of(device)))
+    return tuple(out)
+
+
+# ---- the norm of all gradients, and clipping ----------------------------------------
+
+class GradClip:
+    """The global norm and the clipping of a fixed list of gradients (bfloat16 or
+    float32, dense, or 2-D with rows of unit stride) whose buffers stay: the
+    table of their places is made once.
+
+    out   where the clipped gradients go, tensors of the same shapes and types;
+          None: in place.
+
+    norm() is the square root of the sum of all squares (float32 0-d device
+    tensor); clip(max_norm) scales by max_norm / norm where the norm exceeds
+    max_norm.  Neither synchronises.  A norm over several ranks: sum norm()**2
+    over them and give its root to clip()."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients but {len(self.out)} outputs")
+        if not self.grads:
+            raise ValueError("no gradients")
+        self.device = self.grads[0].get_device()
+        self._jobs = (GradJob * len(self.grads))()
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            rows, cols, ldg = self._place(g, f"grads[{i}]")
+            if o is not g and (o.shape != g.shape or o.dtype != g.dtype):
+                raise ValueError(f"out[{i}] must be {g.dtype} {list(g.shape)}, got {o.dtype} "
+                                 f"{list(o.shape)}")
+            orows, ocols, ldo = self._place(o, f"out[{i}]")
+            if (orows, ocols) != (rows, cols):  # one of the two is dense, the other strided
+                rows, cols = g.shape
+                ldg, ldo = (t.stride(0) if rows > 1 else cols for t in (g, o))
+            self._jobs[i] = GradJob(g.data_ptr(), o.data_ptr(), rows, cols, ldg, ldo,
+                                    DTYPES[g.dtype])
+        n = lib().bfp8_grad_norm_workspace_bytes(self._jobs, len(self._jobs))
+        if n == _INVALID:
+            raise ValueError("invalid gradients")
+        self._bytes = n
+
+    def _place(self, t, name):
+        """(rows, cols, row stride)"""
+        if t.get_device() != self.device or self.device < 0:
+            raise ValueError(f"{name} must be a device tensor, and all on one device")
+        if t.dtype not in DTYPES:
+            raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+        if t.is_contiguous():
+            return 1, t.numel(), t.numel()
+        if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+            return t.shape[0], t.shape[1], t.stride(0)
+        raise ValueError(f"{name} must be dense, or 2-D with rows of unit stride")
+
+    def norm(self, out: torch.Tensor = None, workspace: torch.Tensor = None) -> torch.Tensor:
+        """The norm of the gradients as they are now.  A workspace (of
+        `workspace_bytes`) is allocated when none is given."""
+        if out is None:
+            out = torch.empty((), dtype=torch.float32, device=self.grads[0].device)
+        else:
+            self._check_norm(out, "out")
+        if workspace is None:
+            workspace = torch.empty(self._bytes, dtype=torch.uint8, device=out.device)
+        nbytes = _workspace_size(workspace, self.device)
+        with _on(self.device):
+            _check("bfp8_grad_norm", lib().bfp8_grad_norm(
+                self._jobs, len(self._jobs), out.data_ptr(), workspace.data_ptr(), nbytes,
+                _stream_of(self.device)))
+        return out
+
+    @property
+    def workspace_bytes(self) -> int:
+        return self._bytes
+
+    def _check_norm(self, t, name):
+        if t.dtype != torch.float32 or t.numel() != 1 or t.get_device() != self.device:
+            raise ValueError(f"{name} must be one float32 on device {self.device}")
+
+    def clip(self, max_norm: float, norm: torch.Tensor = None) -> torch.Tensor:
+        """Writes the clipped gradients to `out`; returns the norm they were
+        clipped by: `norm`, or this call's own."""
+        if norm is None:
+            norm = self.norm()
+        else:
+            self._check_norm(norm, "norm")
+        with _on(self.device):
+            _check("bfp8_grad_clip", lib().bfp8_grad_clip(
+                self._jobs, len(self._jobs), norm.data_ptr(), max_norm, _stream_of(self.device)))
+        return norm
+
+
+def grad_norm(grads) -> torch.Tensor:
+    """The global norm of the gradients; see GradClip."""
+    return GradClip(grads).norm()
+
+
+def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
+    """Clips the gradients (in place, or into `out`) to max_norm taken together;
+    returns their norm before.  For gradients whose buffers stay, keep a GradClip."""
+    return GradClip(grads, out).clip(max_norm)
