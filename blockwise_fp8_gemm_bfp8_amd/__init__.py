@@ -188,6 +188,7 @@ _SIGNATURES = {
     "bfp8_grad_norm": [_jobs, _i64, _vp, _vp, _size, _vp],
     "bfp8_grad_norm_workspace_bytes": [_jobs, _i64],
     "bfp8_grad_clip": [_jobs, _i64, _vp, _f32, _vp],
+    "bfp8_grad_norm_clip": [_jobs, _i64, _vp, _f32, _vp, _size, _vp],
     "bfp8_status_str": [_int],
     "bfp8_abi_version": [],
 }

@@ -143,7 +143,7 @@ bfp8_status bfp8_rmsnorm_quantize(const void* x, int64_t ldx, const void* residu
 
 size_t bfp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (check_norm_sizes(BFP8_IN_F32, BFP8_IN_F32, rows, cols) != BFP8_OK) return static_cast<size_t>(-1);
-  return static_cast<size_t>(norm_grad_groups(rows, cols) * cols) * sizeof(float);
+  return static_cast<size_t>(norm_grad_groups(rows, cols) * norm_grad_ld(cols)) * sizeof(float);
 }
 
 bfp8_status bfp8_rmsnorm_backward(const void* dy, int64_t lddy, const void* r, int64_t ldr,
@@ -251,14 +251,20 @@ size_t bfp8_grad_norm_workspace_bytes(const bfp8_grad_job* jobs, int64_t n) {
   return grad_norm_workspace(jobs, n);
 }
 
-bfp8_status bfp8_grad_norm(const bfp8_grad_job* jobs, int64_t n, float* norm, void* workspace,
-                           size_t workspace_bytes, hipStream_t stream) {
-  const bfp8_status st = check_jobs(jobs, n, false);
-  if (st != BFP8_OK) return st;
+// The norm's place and the workspace of its partial sums.
+static bfp8_status check_norm_out(const bfp8_grad_job* jobs, int64_t n, const float* norm,
+                                  const void* workspace, size_t workspace_bytes) {
   if (norm == nullptr) return BFP8_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(norm) & 3u) != 0 || !aligned16(workspace)) return BFP8_ERR_ALIGN;
   const size_t need = grad_norm_workspace(jobs, n);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BFP8_ERR_WORKSPACE;
+  return need > 0 && (workspace == nullptr || workspace_bytes < need) ? BFP8_ERR_WORKSPACE : BFP8_OK;
+}
+
+bfp8_status bfp8_grad_norm(const bfp8_grad_job* jobs, int64_t n, float* norm, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  bfp8_status st = check_jobs(jobs, n, false);
+  if (st == BFP8_OK) st = check_norm_out(jobs, n, norm, workspace, workspace_bytes);
+  if (st != BFP8_OK) return st;
   return launch_grad_norm(jobs, n, norm, static_cast<double*>(workspace), stream);
 }
 
@@ -270,7 +276,16 @@ bfp8_status bfp8_grad_clip(const bfp8_grad_job* jobs, int64_t n, const float* no
   if (n == 0) return BFP8_OK;
   if (norm == nullptr) return BFP8_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(norm) & 3u) != 0) return BFP8_ERR_ALIGN;
-  return launch_grad_clip(jobs, n, norm, max_norm, stream);
+  return launch_grad_clip(jobs, n, const_cast<float*>(norm), max_norm, stream);
+}
+
+bfp8_status bfp8_grad_norm_clip(const bfp8_grad_job* jobs, int64_t n, float* norm, float max_norm,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  bfp8_status st = check_jobs(jobs, n, true);
+  if (st != BFP8_OK) return st;
+  if (!(max_norm >= 0.0f)) return BFP8_ERR_SHAPE;
+  if ((st = check_norm_out(jobs, n, norm, workspace, workspace_bytes)) != BFP8_OK) return st;
+  return launch_grad_norm_clip(jobs, n, norm, max_norm, static_cast<double*>(workspace), stream);
 }
 
 }  // extern "C"

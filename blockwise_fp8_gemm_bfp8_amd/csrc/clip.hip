@@ -10,8 +10,8 @@ namespace bfp8 {
 namespace {
 
 // Tensors of one launch: passed by value, so that no table has to be copied to
-// the device (28 bytes to spare below 4 KiB of arguments).
-constexpr int kJobs = 48;
+// the device (3.9 KB of the 4 KB that arguments may take).
+constexpr int kJobs = 64;
 struct GradBatch {
   const void* g[kJobs];
   void* out[kJobs];
@@ -21,6 +21,7 @@ struct GradBatch {
   int f32;                        // of all jobs of the launch
   int n;
 };
+static_assert(sizeof(GradBatch) + 64 <= 4096, "kernel arguments");
 
 constexpr int kThreads = 256, kUnroll = 8, kChunk = kThreads * kUnroll;  // vectors
 
@@ -30,50 +31,78 @@ constexpr int kThreads = 256, kUnroll = 8, kChunk = kThreads * kUnroll;  // vect
 template <typename T>
 struct Vector {
   static constexpr int N = 16 / sizeof(T);
-  float v[N];
-  __device__ __forceinline__ void load(const T* row, int64_t c, int64_t cols) {
-    if (c >= 0 && c + N <= cols) {
-      if constexpr (N == 8) {
-        Load8<T>::run(row + c, v, 8);
-      } else {
-        const float4 u = *reinterpret_cast<const float4*>(row + c);
-        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-      }
-    } else {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  }
+  __device__ __forceinline__ void load_part(const T* row, int64_t c, int64_t cols) {
+    if (c >= 0 && c + N <= cols) return load(row + c);
+    auto bits = [&](int i) -> uint32_t {
+      if (c + i < 0 || c + i >= cols) return 0u;
+      if constexpr (N == 8) return row[c + i];
+      else return __float_as_uint(row[c + i]);
+    };
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        v[i] = 0.0f;
-        if (c + i >= 0 && c + i < cols) {
-          if constexpr (N == 8) v[i] = bf16_bits_to_f32(row[c + i]);
-          else v[i] = row[c + i];
-        }
-      }
+    for (int i = 0; i < 4; ++i) w[i] = N == 8 ? bits(2 * i) | bits(2 * i + 1) << 16 : bits(i);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (N == 8)
+      return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    else
+      return __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ void scale(float c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (N == 8) w[i] = pack_bf16x2(get(2 * i) * c, get(2 * i + 1) * c);
+      else w[i] = __float_as_uint(get(i) * c);
     }
   }
-  __device__ __forceinline__ void store(T* row, int64_t c, int64_t cols, bool aligned) const {
-    if (aligned && c >= 0 && c + N <= cols) {
-      if constexpr (N == 8) store8(row + c, v, 8);
-      else *reinterpret_cast<float4*>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
+  __device__ __forceinline__ void store(T* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store_part(T* row, int64_t c, int64_t cols) const {
+    if (c >= 0 && c + N <= cols && (reinterpret_cast<uintptr_t>(row + c) & 15) == 0)
+      return store(row + c);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (c + i < 0 || c + i >= cols) continue;
-        if constexpr (N == 8) row[c + i] = static_cast<uint16_t>(pack_bf16x2(v[i], 0.0f));
-        else row[c + i] = v[i];
-      }
+    for (int i = 0; i < N; ++i) {
+      if (c + i < 0 || c + i >= cols) continue;
+      if constexpr (N == 8) row[c + i] = static_cast<T>(w[i >> 1] >> (16 * (i & 1)));
+      else row[c + i] = __uint_as_float(w[i]);
     }
   }
+  __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0; }
 };
 
-// Row and first column of vector `at` of job j.
+template <typename T>
+__device__ __forceinline__ int lead_of(const T* p) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / static_cast<int>(sizeof(T));
+}
+
+// One chunk of a job: the first element of a dense one that has all its vectors
+// (most are), or null.
+template <typename T>
+__device__ __forceinline__ const T* whole_chunk(const GradBatch& b, int j, int64_t base) {
+  const T* p = static_cast<const T*>(b.g[j]);
+  const int64_t c = base * Vector<T>::N - lead_of(p);
+  return b.rows[j] == 1 && c >= 0 && c + kChunk * Vector<T>::N <= b.cols[j] ? p + c : nullptr;
+}
+
+// Row, first column and first element of the row of vector `at` of job j.
 template <typename T>
 __device__ __forceinline__ const T* place(const GradBatch& b, int j, int64_t at, int64_t& row,
                                           int64_t& c) {
   row = b.rows[j] == 1 ? 0 : at / b.per_row[j];
   const T* p = static_cast<const T*>(b.g[j]) + row * b.ldg[j];
-  const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / static_cast<int>(sizeof(T));
-  c = (at - row * b.per_row[j]) * Vector<T>::N - lead;
+  c = (at - row * b.per_row[j]) * Vector<T>::N - lead_of(p);
   return p;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
+  return v;
 }
 
 // The sum of squares of this workgroup's chunks, in float64: a float32 square
@@ -81,80 +110,103 @@ __device__ __forceinline__ const T* place(const GradBatch& b, int j, int64_t at,
 template <typename T>
 __global__ __launch_bounds__(kThreads) void grad_square_kernel(GradBatch b, double* partial) {
   __shared__ double parts[kThreads / 64];
-  double sum = 0.0;
+  constexpr int N = Vector<T>::N;
+  double sum[2] = {0.0, 0.0};
   int j = 0;
   for (unsigned chunk = blockIdx.x; chunk < b.first[b.n]; chunk += gridDim.x) {
     while (chunk >= b.first[j + 1]) ++j;
-    const int64_t base = static_cast<int64_t>(chunk - b.first[j]) * kChunk + threadIdx.x;
-    const int64_t count = b.rows[j] * b.per_row[j], cols = b.cols[j];
+    const int64_t base = static_cast<int64_t>(chunk - b.first[j]) * kChunk;
     Vector<T> v[kUnroll];
+    if (const T* p = whole_chunk<T>(b, j, base)) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t at = base + u * kThreads;
-      int64_t row, c = -Vector<T>::N;  // past the job: no element
-      const T* p = static_cast<const T*>(b.g[j]);
-      if (at < count) p = place<T>(b, j, at, row, c);
-      v[u].load(p, c, cols);
+      for (int u = 0; u < kUnroll; ++u) v[u].load(p + (u * kThreads + threadIdx.x) * N);
+    } else {
+      const int64_t count = b.rows[j] * b.per_row[j];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t at = base + u * kThreads + threadIdx.x;
+        v[u].clear();
+        if (at >= count) continue;
+        int64_t row, c;
+        const T* q = place<T>(b, j, at, row, c);
+        v[u].load_part(q, c, b.cols[j]);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-      for (int i = 0; i < Vector<T>::N; ++i) {
-        const double x = v[u].v[i];
-        sum = fma(x, x, sum);
+      for (int i = 0; i < N; ++i) {
+        const double x = v[u].get(i);
+        sum[i & 1] = fma(x, x, sum[i & 1]);
       }
   }
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
-  if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = sum;
+  const double all = wave_sum(sum[0] + sum[1]);
+  if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = all;
   __syncthreads();
   if (threadIdx.x == 0) partial[blockIdx.x] = (parts[0] + parts[1]) + (parts[2] + parts[3]);
 }
 
-__global__ __launch_bounds__(1024) void grad_norm_kernel(const double* partial, int64_t n, float* norm) {
-  __shared__ double parts[16];
+// The norm from all partial sums, by one workgroup of kThreads; the same order
+// and so the same bits wherever it is done.
+__device__ __forceinline__ float norm_of(const double* partial, int64_t n, double* parts) {
   double sum = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += 1024) sum += partial[i];
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) sum += __shfl_xor(sum, m);
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < n; i += kThreads) sum += partial[i];
+  sum = wave_sum(sum);
   if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    sum = 0.0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) sum += parts[w];
-    norm[0] = static_cast<float>(sqrt(sum));
-  }
+  return static_cast<float>(sqrt((parts[0] + parts[1]) + (parts[2] + parts[3])));
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, const float* norm,
-                                                              float max_norm) {
-  const float n = norm[0];
-  const float c = n > max_norm ? max_norm / n : n <= max_norm ? 1.0f : n;  // NaN stays NaN
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double* partial, int64_t n, float* norm) {
+  __shared__ double parts[kThreads / 64];
+  const float v = norm_of(partial, n, parts);
+  if (threadIdx.x == 0) norm[0] = v;
+}
+
+// Scales by max_norm over the norm: a given one, or (OWN) that of `partial`'s n
+// sums, which every workgroup adds up for itself and the first one writes down.
+template <typename T, bool OWN>
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, float* norm, float max_norm,
+                                                              const double* partial, int64_t n) {
+  __shared__ double parts[kThreads / 64];
+  constexpr int N = Vector<T>::N;
+  float v;
+  if (OWN) {
+    v = norm_of(partial, n, parts);
+    if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = v;
+  } else {
+    v = norm[0];
+  }
+  const float c = v > max_norm ? max_norm / v : v <= max_norm ? 1.0f : v;  // NaN stays NaN
   int j = 0;
   for (unsigned chunk = blockIdx.x; chunk < b.first[b.n]; chunk += gridDim.x) {
     while (chunk >= b.first[j + 1]) ++j;
     if (c == 1.0f && b.out[j] == b.g[j]) continue;  // in place, and nothing to change
-    const int64_t base = static_cast<int64_t>(chunk - b.first[j]) * kChunk + threadIdx.x;
-    const int64_t count = b.rows[j] * b.per_row[j], cols = b.cols[j];
-    Vector<T> v[kUnroll];
-    int64_t rows[kUnroll], at_c[kUnroll];
+    const int64_t base = static_cast<int64_t>(chunk - b.first[j]) * kChunk;
+    Vector<T> x[kUnroll];
+    const T* p = whole_chunk<T>(b, j, base);
+    T* o = static_cast<T*>(b.out[j]);
+    if (p != nullptr) o += p - static_cast<const T*>(b.g[j]);
+    if (p != nullptr && lead_of(o) == 0) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t at = base + u * kThreads;
-      rows[u] = 0, at_c[u] = -Vector<T>::N;
-      const T* p = static_cast<const T*>(b.g[j]);
-      if (at < count) p = place<T>(b, j, at, rows[u], at_c[u]);
-      v[u].load(p, at_c[u], cols);
+      for (int u = 0; u < kUnroll; ++u) x[u].load(p + (u * kThreads + threadIdx.x) * N);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        x[u].scale(c);
+        x[u].store(o + (u * kThreads + threadIdx.x) * N);
+      }
+      continue;
     }
-#pragma unroll
+    const int64_t count = b.rows[j] * b.per_row[j], cols = b.cols[j];
     for (int u = 0; u < kUnroll; ++u) {
-      T* p = static_cast<T*>(b.out[j]) + rows[u] * b.ldo[j];
-#pragma unroll
-      for (int i = 0; i < Vector<T>::N; ++i) v[u].v[i] *= c;
-      const bool aligned = (reinterpret_cast<uintptr_t>(p + at_c[u]) & 15) == 0;
-      v[u].store(p, at_c[u], cols, aligned);
+      const int64_t at = base + u * kThreads + threadIdx.x;
+      if (at >= count) break;
+      int64_t row, col;
+      const T* q = place<T>(b, j, at, row, col);
+      x[0].load_part(q, col, cols);
+      x[0].scale(c);
+      x[0].store_part(static_cast<T*>(b.out[j]) + row * b.ldo[j], col, cols);
     }
   }
 }
@@ -172,6 +224,10 @@ int64_t chunks_of(const bfp8_grad_job& j) {
 }
 
 constexpr unsigned kMaxGroups = 1024;  // workgroups of a norm launch: one partial sum each
+constexpr unsigned kMaxScaleGroups = 1u << 20;
+// Sums that every workgroup of the scaling adds up for itself; more of them (and
+// none) get a launch of their own.
+constexpr int64_t kOwnSums = 2 * kMaxGroups;
 
 // The jobs as launches of up to kJobs tensors of one type and fewer than 2^31
 // chunks: calls f(batch, workgroups), first for bf16 jobs and then for fp32.
@@ -218,24 +274,46 @@ size_t grad_norm_workspace(const bfp8_grad_job* jobs, int64_t n) {
   return groups * sizeof(double);
 }
 
-bfp8_status launch_grad_norm(const bfp8_grad_job* jobs, int64_t n, float* norm, double* partial,
+bfp8_status launch_grad_clip(const bfp8_grad_job* jobs, int64_t n, float* norm, float max_norm,
                              hipStream_t stream) {
-  int64_t at = 0;
-  const bfp8_status st = for_batches(jobs, n, kMaxGroups, [&](const GradBatch& b, unsigned groups) {
-    double* p = partial + at;
-    at += groups;
-    return b.f32 ? launch(grad_square_kernel<float>, dim3(groups), dim3(kThreads), stream, b, p)
-                 : launch(grad_square_kernel<uint16_t>, dim3(groups), dim3(kThreads), stream, b, p);
+  return for_batches(jobs, n, kMaxScaleGroups, [&](const GradBatch& b, unsigned groups) {
+    return launch(b.f32 ? grad_scale_kernel<float, false> : grad_scale_kernel<uint16_t, false>,
+                  dim3(groups), dim3(kThreads), stream, b, norm, max_norm, nullptr, int64_t(0));
   });
-  if (st != BFP8_OK) return st;
-  return launch(grad_norm_kernel, dim3(1), dim3(1024), stream, partial, at, norm);
 }
 
-bfp8_status launch_grad_clip(const bfp8_grad_job* jobs, int64_t n, const float* norm,
-                             float max_norm, hipStream_t stream) {
-  return for_batches(jobs, n, 1u << 20, [&](const GradBatch& b, unsigned groups) {
-    return b.f32 ? launch(grad_scale_kernel<float>, dim3(groups), dim3(kThreads), stream, b, norm, max_norm)
-                 : launch(grad_scale_kernel<uint16_t>, dim3(groups), dim3(kThreads), stream, b, norm, max_norm);
+// The partial sums; n_sums receives their number.
+static bfp8_status launch_squares(const bfp8_grad_job* jobs, int64_t n, double* partial,
+                                  int64_t& n_sums, hipStream_t stream) {
+  n_sums = 0;
+  return for_batches(jobs, n, kMaxGroups, [&](const GradBatch& b, unsigned groups) {
+    double* p = partial + n_sums;
+    n_sums += groups;
+    return launch(b.f32 ? grad_square_kernel<float> : grad_square_kernel<uint16_t>, dim3(groups),
+                  dim3(kThreads), stream, b, p);
+  });
+}
+
+bfp8_status launch_grad_norm(const bfp8_grad_job* jobs, int64_t n, float* norm, double* partial,
+                             hipStream_t stream) {
+  int64_t n_sums;
+  const bfp8_status st = launch_squares(jobs, n, partial, n_sums, stream);
+  if (st != BFP8_OK) return st;
+  return launch(grad_norm_kernel, dim3(1), dim3(kThreads), stream, partial, n_sums, norm);
+}
+
+bfp8_status launch_grad_norm_clip(const bfp8_grad_job* jobs, int64_t n, float* norm, float max_norm,
+                                  double* partial, hipStream_t stream) {
+  int64_t n_sums;
+  bfp8_status st = launch_squares(jobs, n, partial, n_sums, stream);
+  if (st != BFP8_OK) return st;
+  if (n_sums == 0 || n_sums > kOwnSums) {
+    st = launch(grad_norm_kernel, dim3(1), dim3(kThreads), stream, partial, n_sums, norm);
+    return st != BFP8_OK ? st : launch_grad_clip(jobs, n, norm, max_norm, stream);
+  }
+  return for_batches(jobs, n, kMaxScaleGroups, [&](const GradBatch& b, unsigned groups) {
+    return launch(b.f32 ? grad_scale_kernel<float, true> : grad_scale_kernel<uint16_t, true>,
+                  dim3(groups), dim3(kThreads), stream, b, norm, max_norm, partial, n_sums);
   });
 }
 

@@ -82,26 +82,41 @@ template <typename T, int FORMAT, bool GRAD>
 __global__ __launch_bounds__(kTileThreads) void glu_tile_kernel(GluArgs a, unsigned col_tiles,
                                                                 CodesOut o) {
   __shared__ __attribute__((aligned(16))) TileShared sh;
-  const unsigned tm = blockIdx.x / col_tiles, tc = blockIdx.x - tm * col_tiles;
+  const unsigned tile = xcd_run(blockIdx.x, gridDim.x);
+  const unsigned tm = tile / col_tiles, tc = tile - tm * col_tiles;
   const int64_t m0 = static_cast<int64_t>(tm) * 128, c0 = static_cast<int64_t>(tc) * 128;
   const int64_t c = c0 + (threadIdx.x & 15) * 8, m = m0 + (threadIdx.x >> 4) * 4;
   Raw8<T> g[4], u[4], dh[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    g[i].load(a.gate, (m + i) * a.ldg + c, 8);
-    u[i].load(a.up, (m + i) * a.ldu + c, 8);
-    if (GRAD) dh[i].load(a.dh, (m + i) * a.lddh + c, 8);
+    g[i].load_once(a.gate, (m + i) * a.ldg + c);
+    u[i].load_once(a.up, (m + i) * a.ldu + c);
+    if (GRAD) dh[i].load_once(a.dh, (m + i) * a.lddh + c);
   }
-  float x[4][8], y[4][8];
+  float x[4][8];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (GRAD) silu_gate_grad(dh[i].get(k), g[i].get(k), u[i].get(k), x[i][k], y[i][k]);
+      float du;
+      if (GRAD) silu_gate_grad(dh[i].get(k), g[i].get(k), u[i].get(k), x[i][k], du);
       else x[i][k] = silu_gate(g[i].get(k), u[i].get(k));
     }
   emit_tile<FORMAT>(o, m0, c0, x, sh);
-  if (GRAD) emit_tile<FORMAT>(o, m0, a.cols + c0, y, sh);
+  if (!GRAD) return;
+  // dup is computed after dgate has left, from the inputs again: with both kept
+  // a thread needs 156 registers and one workgroup fits a CU (236 -> 218 us)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    g[i].keep_packed();
+    dh[i].keep_packed();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float dg;
+      silu_gate_grad(dh[i].get(k), g[i].get(k), 1.0f, dg, x[i][k]);
+    }
+  }
+  emit_tile<FORMAT>(o, m0, a.cols + c0, x, sh);
 }
 
 template <typename T, bool GRAD>

@@ -43,11 +43,12 @@ struct NormGradArgs {
   void* dx;
   int64_t lddx;
   float* dw;
-  float* partial;  // [norm_grad_groups(rows, cols)][cols]
+  float* partial;  // [norm_grad_groups(rows, cols)][norm_grad_ld(cols)]
   int64_t rows;
   int cols;
 };
 int64_t norm_grad_groups(int64_t rows, int64_t cols);
+__host__ __device__ inline int64_t norm_grad_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 bfp8_status launch_rmsnorm_backward(const NormGradArgs& a, bfp8_in_dtype dt, hipStream_t stream);
 
 struct GluArgs {
@@ -70,8 +71,10 @@ bfp8_status launch_swiglu_quantize(const GluArgs& a, bfp8_in_dtype dt, bfp8_code
 size_t grad_norm_workspace(const bfp8_grad_job* jobs, int64_t n);
 bfp8_status launch_grad_norm(const bfp8_grad_job* jobs, int64_t n, float* norm, double* partial,
                              hipStream_t stream);
-bfp8_status launch_grad_clip(const bfp8_grad_job* jobs, int64_t n, const float* norm,
-                             float max_norm, hipStream_t stream);
+bfp8_status launch_grad_clip(const bfp8_grad_job* jobs, int64_t n, float* norm, float max_norm,
+                             hipStream_t stream);
+bfp8_status launch_grad_norm_clip(const bfp8_grad_job* jobs, int64_t n, float* norm, float max_norm,
+                                  double* partial, hipStream_t stream);
 
 // The format chosen at run time as a template argument F.
 #define BFP8_WITH_FORMAT(format, CALL)                                             \

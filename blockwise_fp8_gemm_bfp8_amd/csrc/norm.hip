@@ -144,7 +144,8 @@ __global__ __launch_bounds__(kTileThreads) void norm_tile_kernel(const void* r, 
                                                                  bool w_f32, unsigned col_tiles,
                                                                  CodesOut o) {
   __shared__ __attribute__((aligned(16))) TileShared sh;
-  const unsigned tm = blockIdx.x / col_tiles, tc = blockIdx.x - tm * col_tiles;
+  const unsigned tile = xcd_run(blockIdx.x, gridDim.x);
+  const unsigned tm = tile / col_tiles, tc = tile - tm * col_tiles;
   const int64_t m0 = static_cast<int64_t>(tm) * 128, c0 = static_cast<int64_t>(tc) * 128;
   const int lane16 = threadIdx.x & 15, rsub = threadIdx.x >> 4;
   Raw8<T> raw[4];
@@ -177,6 +178,11 @@ bfp8_status quantize_typed(const NormArgs& a, bfp8_code_format format, const Cod
 }
 
 // ---- gradient ------------------------------------------------------------------
+
+// Workgroups of the gradient, each with partial sums of dw to write and to be
+// read: as many as run at once (two a CU, by their registers).  At 16384 x 2048
+// 256, 512 and 1024 took 57, 52 and 55 us.
+constexpr int64_t kGradGroups = 512;
 
 // Rows in turn, the weight and this workgroup's share of dw in registers; the
 // waves' shares meet in LDS at the end and leave as one row of `partial`.
@@ -247,39 +253,41 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_grad_kernel(NormGradA
     __syncthreads();
   }
   if (slot == 0) {
-    float* p = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
+    float* p = a.partial + static_cast<int64_t>(blockIdx.x) * norm_grad_ld(a.cols);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * TPR + lane) * 8, n = valid8(c, a.cols);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) p[c + i] = dw[j][i];
+      const int c = (j * TPR + lane) * 8;
+      if (c < a.cols) store8(p + c, dw[j], 8);
     }
   }
 }
 
-// dw [cols] as the sum of `groups` rows of partial sums: 64 columns a
-// workgroup, every 16th row a wave, the waves' sums joined in LDS.
-constexpr int kSumWaves = 16;
-__global__ __launch_bounds__(64 * kSumWaves) void norm_grad_sum_kernel(const float* partial,
-                                                                       int64_t groups, int cols,
-                                                                       float* dw) {
-  __shared__ float sums[kSumWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
-  float sum = 0.0f;
-  if (c < cols) {
+// dw [cols] as the sum of `groups` rows of partial sums: 32 columns a
+// workgroup, four a lane, so that 128 rows are under way at once; their sums
+// meet in LDS.
+constexpr int kSumSlots = 128;
+__global__ __launch_bounds__(8 * kSumSlots) void norm_grad_sum_kernel(const float* partial, int groups,
+                                                                      int cols, float* dw) {
+  __shared__ __attribute__((aligned(16))) float sums[kSumSlots][32];
+  const int lane = threadIdx.x & 7, slot = threadIdx.x >> 3;
+  const int64_t ld = norm_grad_ld(cols);
+  const int c = blockIdx.x * 32 + lane * 4;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < ld) {
 #pragma unroll 4
-    for (int64_t g = wave; g < groups; g += kSumWaves) sum += partial[g * cols + c];
+    for (int g = slot; g < groups; g += kSumSlots) {
+      const float4 p = *reinterpret_cast<const float4*>(partial + g * ld + c);
+      s[0] += p.x, s[1] += p.y, s[2] += p.z, s[3] += p.w;
+    }
   }
-  sums[wave][lane] = sum;
+  *reinterpret_cast<float4*>(&sums[slot][lane * 4]) = make_float4(s[0], s[1], s[2], s[3]);
   __syncthreads();
-  if (wave == 0 && c < cols) {
-    sum = 0.0f;
+  // 32 columns by 32 threads, four slots each; then a row of 32 lanes' tree
+  const int col = threadIdx.x >> 5, part = threadIdx.x & 31;
+  float sum = (sums[part][col] + sums[part + 32][col]) + (sums[part + 64][col] + sums[part + 96][col]);
 #pragma unroll
-    for (int k = 0; k < kSumWaves; ++k) sum += sums[k][lane];
-    dw[c] = sum;
-  }
+  for (int m = 1; m < 32; m *= 2) sum += __shfl_xor(sum, m);
+  if (part == 0 && blockIdx.x * 32 + col < cols) dw[blockIdx.x * 32 + col] = sum;
 }
 
 template <typename T, int TPR, int NV>
@@ -307,7 +315,7 @@ bfp8_status launch_rmsnorm_quantize(const NormArgs& a, bfp8_in_dtype dt, bfp8_co
 
 int64_t norm_grad_groups(int64_t rows, int64_t cols) {
   const int64_t at_once = cols <= 128 ? 16 : cols <= 2048 ? 4 : 1;  // rows of a workgroup
-  return std::min<int64_t>((rows + at_once - 1) / at_once, 1024);
+  return std::min<int64_t>((rows + at_once - 1) / at_once, kGradGroups);
 }
 
 bfp8_status launch_rmsnorm_backward(const NormGradArgs& a, bfp8_in_dtype dt, hipStream_t stream) {
@@ -317,8 +325,8 @@ bfp8_status launch_rmsnorm_backward(const NormGradArgs& a, bfp8_in_dtype dt, hip
                                              : launch_grad_of<uint16_t>(a, groups, stream);
     if (st != BFP8_OK) return st;
   }
-  return launch(norm_grad_sum_kernel, dim3((a.cols + 63) / 64), dim3(64 * kSumWaves), stream,
-                a.partial, groups, a.cols, a.dw);
+  return launch(norm_grad_sum_kernel, dim3((a.cols + 31) / 32), dim3(8 * kSumSlots), stream,
+                a.partial, static_cast<int>(groups), a.cols, a.dw);
 }
 
 }  // namespace bfp8

@@ -10,29 +10,29 @@ import ctypes
 
 import torch
 
-from . import DTYPES, GradJob, _check, _padded_empty, _scale_bytes, lib
+from . import DTYPES, BFP8Error, GradJob, _padded_empty, _scale_bytes, lib
 from .attention import _pointer, _stream_of
 
 CODE_FORMATS = {"fp32": 0, "mx128": 1, "mx32": 2}  # hotpath's scale formats
 _INVALID = ctypes.c_size_t(-1).value
 
 
-class _on:
-    """Launches go to the current device: makes it the tensors' where it is another."""
-
-    def __new__(cls, device):
-        return _NOTHING if torch.cuda.current_device() == device else torch.cuda.device(device)
-
-
-class _Nothing:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *_):
-        pass
+# A generation step's kernels take a few microseconds, so the marshalling is kept
+# short: results without padding are allocated without a view, and the device is
+# changed only where the current one is another.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-_NOTHING = _Nothing()
+def _call(name, device, *args):
+    """The library's call `name` on the current stream of `device`."""
+    fn = getattr(lib(), name)
+    if _current_device() == device:
+        code = fn(*args, _stream_of(device))
+    else:  # launches go to the current device
+        with torch.cuda.device(device):
+            code = fn(*args, _stream_of(device))
+    if code:
+        raise BFP8Error(name, code)
 
 
 def _matrix(t, name, device=None, shape=None, dtype=None):
@@ -59,12 +59,19 @@ def _matrix(t, name, device=None, shape=None, dtype=None):
     return row if size[0] > 1 else max(-(-size[1] // 16) * 16, 16)
 
 
+def _rows_empty(rows, cols, dtype, device, align):
+    """_padded_empty, without its view where there is nothing to pad."""
+    if cols % align == 0 and cols:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    return _padded_empty(rows, cols, dtype, device, align)
+
+
 def _result(out, like, name, device):
     """The matrix of a result that has `like`'s shape and dtype, a new one if
     `out` is None, and its row stride."""
     if out is None:
         rows, cols = like.shape
-        out = _padded_empty(rows, cols, like.dtype, like.device, 16 // like.element_size())
+        out = _rows_empty(rows, cols, like.dtype, like.device, 16 // like.element_size())
         return out, out.stride(0)
     return out, _matrix(out, name, device, like.shape, like.dtype)
 
@@ -75,41 +82,45 @@ def _vector(t, name, n, device, dtypes=(torch.float32,)):
                          f"device {device}")
 
 
+def _codes(t, name, rows, cols, device, place):
+    """The matrix of codes, a new one if `t` is None, and its row stride."""
+    if t is None:
+        t = _rows_empty(rows, cols, torch.uint8, place, 16)
+        return t, t.stride(0)
+    return t, _matrix(t, name, device, (rows, cols), torch.uint8)
+
+
+def _scales(t, name, rows, cols, scales, device, place):
+    """The scales of rows x cols codes in the layout of the format."""
+    shape = (rows, cols // 32) if scales == "mx32" else (cols // 128, rows)
+    if t is None:
+        if scales == "fp32":
+            return torch.empty(shape, dtype=torch.float32, device=place)
+        return _scale_bytes(*shape, place)
+    dtype = torch.float32 if scales == "fp32" else torch.uint8
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a dense {dtype} [{shape[0]}][{shape[1]}] on device {device}")
+    return t
+
+
 def _codes_out(rows, cols, scales, transposed, given, like, device):
-    """(format, [q, s] or [q, s, qt, st], their arguments) of a rows x cols result;
+    """([q, s] or [q, s, qt, st], their arguments) of a rows x cols result;
     `given`: q, s, qt, st or Nones."""
-    if scales not in CODE_FORMATS:
+    fmt = CODE_FORMATS.get(scales)
+    if fmt is None:
         raise ValueError(f"scales must be one of {sorted(CODE_FORMATS)}")
     q, s, qt, st = given
     if not transposed and (qt is not None or st is not None):
         raise ValueError("qt and st are written with transposed=True only")
-    group, f32 = (32 if scales == "mx32" else 128), scales == "fp32"
-
-    def codes(t, name, r, c):
-        if t is None:
-            t = _padded_empty(r, c, torch.uint8, like.device, 16)
-            return t, t.stride(0)
-        return t, _matrix(t, name, device, (r, c), torch.uint8)
-
-    def scale(t, name, r, c):
-        shape = (r, c // 32) if group == 32 else (c // 128, r)
-        if t is None:
-            return (torch.empty(shape, dtype=torch.float32, device=like.device) if f32
-                    else _scale_bytes(*shape, like.device))
-        if (t.shape != shape or t.dtype != (torch.float32 if f32 else torch.uint8)
-                or not t.is_contiguous() or t.get_device() != device):
-            raise ValueError(f"{name} must be a dense {'float32' if f32 else 'uint8'} "
-                             f"[{shape[0]}][{shape[1]}] on device {device}")
-        return t
-
-    q, ldq = codes(q, "q", rows, cols)
-    s = scale(s, "s", rows, cols)
+    place = like.device
+    q, ldq = _codes(q, "q", rows, cols, device, place)
+    s = _scales(s, "s", rows, cols, scales, device, place)
     if not transposed:
-        return CODE_FORMATS[scales], [q, s], (q.data_ptr(), ldq, s.data_ptr(), None, 0, None)
-    qt, ldqt = codes(qt, "qt", cols, rows)
-    st = scale(st, "st", cols, rows)
-    return CODE_FORMATS[scales], [q, s, qt, st], (q.data_ptr(), ldq, s.data_ptr(), qt.data_ptr(),
-                                                  ldqt, st.data_ptr())
+        return [q, s], (fmt, q.data_ptr(), ldq, s.data_ptr(), None, 0, None)
+    qt, ldqt = _codes(qt, "qt", cols, rows, device, place)
+    st = _scales(st, "st", cols, rows, scales, device, place)
+    return [q, s, qt, st], (fmt, q.data_ptr(), ldq, s.data_ptr(), qt.data_ptr(), ldqt,
+                            st.data_ptr())
 
 
 # ---- RMS norm -----------------------------------------------------------------
@@ -143,10 +154,8 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor = None
     See bfp8_rmsnorm."""
     device, head, sum_out, lds, rstd = _norm_inputs(x, weight, residual, sum_out, rstd)
     out, ldy = _result(out, x, "out", device)
-    with _on(device):
-        _check("bfp8_rmsnorm", lib().bfp8_rmsnorm(
-            *head, eps, _pointer(sum_out), lds, out.data_ptr(), ldy, rstd.data_ptr(),
-            _stream_of(device)))
+    _call("bfp8_rmsnorm", device, *head, eps, _pointer(sum_out), lds, out.data_ptr(), ldy,
+          rstd.data_ptr())
     return out, x if residual is None else sum_out, rstd
 
 
@@ -160,10 +169,9 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tens
     quantize_act_dual_kmajor writes them), "mx128" (quantize_mx_act_dual_kmajor)
     or "mx32" (quantize_mx_act_dual, group 32).  See bfp8_rmsnorm_quantize."""
     device, head, sum_out, lds, rstd = _norm_inputs(x, weight, residual, sum_out, rstd)
-    fmt, out, args = _codes_out(*x.shape, scales, transposed, (q, s, qt, st), x, device)
-    with _on(device):
-        _check("bfp8_rmsnorm_quantize", lib().bfp8_rmsnorm_quantize(
-            *head, eps, _pointer(sum_out), lds, rstd.data_ptr(), fmt, *args, _stream_of(device)))
+    out, args = _codes_out(*x.shape, scales, transposed, (q, s, qt, st), x, device)
+    _call("bfp8_rmsnorm_quantize", device, *head, eps, _pointer(sum_out), lds, rstd.data_ptr(),
+          *args)
     return (*out, x if residual is None else sum_out, rstd)
 
 
@@ -197,11 +205,9 @@ def rmsnorm_backward(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rs
         if nbytes != _INVALID:  # the call itself reports what is wrong with the sizes
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
     nbytes = _workspace_size(workspace, device)
-    with _on(device):
-        _check("bfp8_rmsnorm_backward", lib().bfp8_rmsnorm_backward(
-            dy.data_ptr(), lddy, r.data_ptr(), ldr, weight.data_ptr(), DTYPES[weight.dtype],
-            rstd.data_ptr(), _pointer(dsum), lds, DTYPES[dy.dtype], rows, cols, dx.data_ptr(), lddx,
-            dweight.data_ptr(), _pointer(workspace), nbytes, _stream_of(device)))
+    _call("bfp8_rmsnorm_backward", device, dy.data_ptr(), lddy, r.data_ptr(), ldr, weight.data_ptr(),
+          DTYPES[weight.dtype], rstd.data_ptr(), _pointer(dsum), lds, DTYPES[dy.dtype], rows, cols,
+          dx.data_ptr(), lddx, dweight.data_ptr(), _pointer(workspace), nbytes)
     return dx, dweight
 
 
@@ -230,8 +236,7 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, out: torch.Tensor = None) -> to
     halves of one projection's rows.  See bfp8_swiglu."""
     device, head = _glu_inputs(gate, up)
     out, ldh = _result(out, gate, "out", device)
-    with _on(device):
-        _check("bfp8_swiglu", lib().bfp8_swiglu(*head, out.data_ptr(), ldh, _stream_of(device)))
+    _call("bfp8_swiglu", device, *head, out.data_ptr(), ldh)
     return out
 
 
@@ -241,10 +246,8 @@ def swiglu_quantize(gate: torch.Tensor, up: torch.Tensor, scales: str = "fp32",
     ``transposed`` (q, s, qt, st); ``scales`` as for rmsnorm_quantize.  See
     bfp8_swiglu_quantize."""
     device, head = _glu_inputs(gate, up)
-    fmt, out, args = _codes_out(*gate.shape, scales, transposed, (q, s, qt, st), gate, device)
-    with _on(device):
-        _check("bfp8_swiglu_quantize", lib().bfp8_swiglu_quantize(*head, fmt, *args,
-                                                                  _stream_of(device)))
+    out, args = _codes_out(*gate.shape, scales, transposed, (q, s, qt, st), gate, device)
+    _call("bfp8_swiglu_quantize", device, *head, *args)
     return tuple(out)
 
 
@@ -254,9 +257,7 @@ def swiglu_backward(dh: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
     device, head = _glu_inputs(gate, up, dh)
     dgate, ldg = _result(dgate, gate, "dgate", device)
     dup, ldu = _result(dup, gate, "dup", device)
-    with _on(device):
-        _check("bfp8_swiglu_backward", lib().bfp8_swiglu_backward(
-            *head, dgate.data_ptr(), ldg, dup.data_ptr(), ldu, _stream_of(device)))
+    _call("bfp8_swiglu_backward", device, *head, dgate.data_ptr(), ldg, dup.data_ptr(), ldu)
     return dgate, dup
 
 
@@ -268,10 +269,8 @@ def swiglu_backward_quantize(dh: torch.Tensor, gate: torch.Tensor, up: torch.Ten
     (q, s, qt, st).  See bfp8_swiglu_backward_quantize."""
     device, head = _glu_inputs(gate, up, dh)
     rows, cols = gate.shape
-    fmt, out, args = _codes_out(rows, 2 * cols, scales, transposed, (q, s, qt, st), gate, device)
-    with _on(device):
-        _check("bfp8_swiglu_backward_quantize", lib().bfp8_swiglu_backward_quantize(
-            *head, fmt, *args, _stream_of(device)))
+    out, args = _codes_out(rows, 2 * cols, scales, transposed, (q, s, qt, st), gate, device)
+    _call("bfp8_swiglu_backward_quantize", device, *head, *args)
     return tuple(out)
 
 
@@ -297,7 +296,7 @@ class GradClip:
             raise ValueError(f"{len(self.grads)} gradients but {len(self.out)} outputs")
         if not self.grads:
             raise ValueError("no gradients")
-        self.device = self.grads[0].get_device()
+        self.device, self._device = self.grads[0].get_device(), self.grads[0].device
         self._jobs = (GradJob * len(self.grads))()
         for i, (g, o) in enumerate(zip(self.grads, self.out)):
             rows, cols, ldg = self._place(g, f"grads[{i}]")
@@ -327,40 +326,45 @@ class GradClip:
             return t.shape[0], t.shape[1], t.stride(0)
         raise ValueError(f"{name} must be dense, or 2-D with rows of unit stride")
 
-    def norm(self, out: torch.Tensor = None, workspace: torch.Tensor = None) -> torch.Tensor:
-        """The norm of the gradients as they are now.  A workspace (of
-        `workspace_bytes`) is allocated when none is given."""
-        if out is None:
-            out = torch.empty((), dtype=torch.float32, device=self.grads[0].device)
-        else:
-            self._check_norm(out, "out")
-        if workspace is None:
-            workspace = torch.empty(self._bytes, dtype=torch.uint8, device=out.device)
-        nbytes = _workspace_size(workspace, self.device)
-        with _on(self.device):
-            _check("bfp8_grad_norm", lib().bfp8_grad_norm(
-                self._jobs, len(self._jobs), out.data_ptr(), workspace.data_ptr(), nbytes,
-                _stream_of(self.device)))
-        return out
-
     @property
     def workspace_bytes(self) -> int:
         return self._bytes
+
+    def _norm_out(self, out, workspace):
+        """The norm's tensor, the workspace's pointer and its bytes; either is
+        allocated when none is given."""
+        if out is None:
+            out = torch.empty((), dtype=torch.float32, device=self._device)
+        else:
+            self._check_norm(out, "out")
+        if workspace is None:
+            workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self._device)
+            return out, workspace, self._bytes
+        return out, workspace, _workspace_size(workspace, self.device)
+
+    def norm(self, out: torch.Tensor = None, workspace: torch.Tensor = None) -> torch.Tensor:
+        """The norm of the gradients as they are now."""
+        out, workspace, nbytes = self._norm_out(out, workspace)
+        _call("bfp8_grad_norm", self.device, self._jobs, len(self._jobs), out.data_ptr(),
+              workspace.data_ptr(), nbytes)
+        return out
 
     def _check_norm(self, t, name):
         if t.dtype != torch.float32 or t.numel() != 1 or t.get_device() != self.device:
             raise ValueError(f"{name} must be one float32 on device {self.device}")
 
-    def clip(self, max_norm: float, norm: torch.Tensor = None) -> torch.Tensor:
+    def clip(self, max_norm: float, norm: torch.Tensor = None,
+             workspace: torch.Tensor = None) -> torch.Tensor:
         """Writes the clipped gradients to `out`; returns the norm they were
         clipped by: `norm`, or this call's own."""
-        if norm is None:
-            norm = self.norm()
-        else:
+        if norm is not None:
             self._check_norm(norm, "norm")
-        with _on(self.device):
-            _check("bfp8_grad_clip", lib().bfp8_grad_clip(
-                self._jobs, len(self._jobs), norm.data_ptr(), max_norm, _stream_of(self.device)))
+            _call("bfp8_grad_clip", self.device, self._jobs, len(self._jobs), norm.data_ptr(),
+                  max_norm)
+            return norm
+        norm, workspace, nbytes = self._norm_out(None, workspace)
+        _call("bfp8_grad_norm_clip", self.device, self._jobs, len(self._jobs), norm.data_ptr(),
+              max_norm, workspace.data_ptr(), nbytes)
         return norm
 
 

@@ -162,6 +162,11 @@ size_t bfp8_grad_norm_workspace_bytes(const bfp8_grad_job* jobs, int64_t n);
 bfp8_status bfp8_grad_clip(const bfp8_grad_job* jobs, int64_t n, const float* norm, float max_norm,
                            hipStream_t stream);
 
+/* bfp8_grad_norm, then bfp8_grad_clip by that norm: the same bits from a launch
+ * less. */
+bfp8_status bfp8_grad_norm_clip(const bfp8_grad_job* jobs, int64_t n, float* norm, float max_norm,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -41,6 +41,11 @@ def test_clip(sizes, dtypes, max_norm):
     for g, o, b in zip(grads, plan.out, before):
         assert torch.equal(g, o)
     assert torch.equal(norm, bfp8.grad_norm(before))
+    # one call for both, or two: the same bits
+    parts = bfp8.GradClip(before, [torch.empty_like(g) for g in grads])
+    parts.clip(max_norm, norm=parts.norm())
+    for o, p in zip(plan.out, parts.out):
+        assert torch.equal(o, p)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -68,6 +73,19 @@ def test_strided(dtype, rows, cols, ld, ldo):
     rest = base[:, cols:].clone()
     bfp8.clip_grads([g], 1.0)
     assert torch.equal(g, o) and torch.equal(base[:, cols:], rest)
+
+
+def test_more_sums_than_a_workgroup_adds_up():
+    """Three launches of 1024 partial sums each: the norm has a launch of its own."""
+    n = 1024 * 2048 * 4 // 64 + 5
+    grads = [torch.randn(n, device="cuda", generator=generator(i)) for i in range(3 * 64)]
+    plan = bfp8.GradClip(grads, [torch.empty_like(g) for g in grads])
+    assert plan.workspace_bytes > 8 * 2048
+    norm = plan.clip(1.0)
+    want = torch.stack([g.double().square().sum() for g in grads]).sum().sqrt()
+    assert abs(norm.item() - want.item()) <= 1.1 * U * want.item()
+    for g, o in list(zip(grads, plan.out))[::50]:
+        close(o, f64(g) / want.item(), 4 * U * np.abs(f64(g)) / want.item())
 
 
 def test_sizes_that_float32_squares_lose():

@@ -32,7 +32,7 @@ def test_header_and_exports(L):
     assert names == {"bfp8_rmsnorm", "bfp8_rmsnorm_quantize", "bfp8_rmsnorm_backward",
                      "bfp8_rmsnorm_backward_workspace_bytes", "bfp8_swiglu", "bfp8_swiglu_quantize",
                      "bfp8_swiglu_backward", "bfp8_swiglu_backward_quantize", "bfp8_grad_norm",
-                     "bfp8_grad_norm_workspace_bytes", "bfp8_grad_clip"}
+                     "bfp8_grad_norm_workspace_bytes", "bfp8_grad_clip", "bfp8_grad_norm_clip"}
     for name in names:
         assert hasattr(L, name), name
     assert ctypes.sizeof(bfp8.GradJob) == 56
@@ -144,7 +144,8 @@ def test_clip_refusals(L):
         arr = (bfp8.GradJob * max(len(jobs), 1))(*jobs)
         a = L.bfp8_grad_norm(arr, len(jobs), norm, P, 1 << 30, None)
         b = L.bfp8_grad_clip(arr, len(jobs), norm, max_norm, None)
-        assert a == b
+        c = L.bfp8_grad_norm_clip(arr, len(jobs), norm, max_norm, P, 1 << 30, None)
+        assert a == b == c
         return a
     assert both(job(g=None)) == NULL and both(job(), job(g=None)) == NULL
     assert both(job(g=P + 2)) == ALIGN and both(job(g=P + 1, out=P + 1, dt=BF)) == ALIGN
@@ -153,7 +154,11 @@ def test_clip_refusals(L):
     assert both(job(rows=1 << 20, cols=1 << 20, ldg=1 << 20, ldo=1 << 20)) == SHAPE
     assert both(job(), norm=None) == NULL and both(job(), norm=P + 2) == ALIGN
     one = (bfp8.GradJob * 1)(job())
-    clip = lambda j, m=1.0: L.bfp8_grad_clip((bfp8.GradJob * 1)(j), 1, P, m, None)
+
+    def clip(j, m=1.0):
+        a = L.bfp8_grad_clip((bfp8.GradJob * 1)(j), 1, P, m, None)
+        assert a == L.bfp8_grad_norm_clip((bfp8.GradJob * 1)(j), 1, P, m, P, 1 << 30, None)
+        return a
     assert clip(job(out=None)) == NULL and clip(job(out=P + 2)) == ALIGN and clip(job(ldo=99)) == SHAPE
     assert clip(job(ldo=128)) == SHAPE  # in place, with another row stride
     assert clip(job(), -1.0) == SHAPE and clip(job(), NAN) == SHAPE
@@ -164,12 +169,13 @@ def test_clip_refusals(L):
     assert need == 8 and L.bfp8_grad_norm(one, 1, P, P, 7, None) == WS
     assert L.bfp8_grad_norm(one, 1, P, None, 8, None) == WS
     assert L.bfp8_grad_norm(one, 1, P, P + 8, 8, None) == ALIGN
+    assert L.bfp8_grad_norm_clip(one, 1, P, 1.0, P, 7, None) == WS
     empty = (bfp8.GradJob * 1)(job(g=None, out=None, cols=0))
     assert L.bfp8_grad_norm_workspace_bytes(empty, 1) == 0 and L.bfp8_grad_clip(empty, 1, P, 1.0, None) == OK
     assert L.bfp8_grad_norm_workspace_bytes(one, -1) == ctypes.c_size_t(-1).value
-    # 49 tensors are two launches, each with a sum of its own
-    many = (bfp8.GradJob * 49)(*[job()] * 49)
-    assert L.bfp8_grad_norm_workspace_bytes(many, 49) == 49 * 8
+    # 65 tensors are two launches with sums of their own
+    many = (bfp8.GradJob * 65)(*[job()] * 65)
+    assert L.bfp8_grad_norm_workspace_bytes(many, 65) == 65 * 8
 
 
 def test_binding_refuses_host_tensors():
