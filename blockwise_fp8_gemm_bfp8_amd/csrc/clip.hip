@@ -23,7 +23,9 @@ struct GradBatch {
 };
 static_assert(sizeof(GradBatch) + 64 <= 4096, "kernel arguments");
 
-constexpr int kThreads = 256, kUnroll = 8, kChunk = kThreads * kUnroll;  // vectors
+// Vectors of a chunk: 2, 4 and 8 a thread took 186, 188 and 196 us for 101 million
+// float32 values, and 50 to 51 for 50 million in bf16.
+constexpr int kThreads = 256, kUnroll = 4, kChunk = kThreads * kUnroll;
 
 // A vector is 16 bytes at a 16-byte boundary of memory: vector k of a row that
 // starts `lead` elements past one holds columns k N - lead .. + N - 1, those of
@@ -60,7 +62,7 @@ struct Vector {
     }
   }
   __device__ __forceinline__ void store(T* p) const {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    __builtin_nontemporal_store(Words4{w[0], w[1], w[2], w[3]}, reinterpret_cast<Words4*>(p));
   }
   __device__ __forceinline__ void store_part(T* row, int64_t c, int64_t cols) const {
     if (c >= 0 && c + N <= cols && (reinterpret_cast<uintptr_t>(row + c) & 15) == 0)
@@ -179,9 +181,14 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, float
     v = norm[0];
   }
   const float c = v > max_norm ? max_norm / v : v <= max_norm ? 1.0f : v;  // NaN stays NaN
-  int j = 0;
-  for (unsigned chunk = blockIdx.x; chunk < b.first[b.n]; chunk += gridDim.x) {
-    while (chunk >= b.first[j + 1]) ++j;
+  // Last chunks first, which the norm read last, and results past the caches:
+  // what is left of the gradients in the last-level cache is read from there
+  // (225 -> 194 us for 101 million float32 values, 59 -> 50 for 50 million in bf16).
+  int j = b.n - 1;
+  const unsigned last = b.first[b.n] - 1;
+  for (unsigned turn = blockIdx.x; turn <= last; turn += gridDim.x) {
+    const unsigned chunk = last - turn;
+    while (chunk < b.first[j]) --j;
     if (c == 1.0f && b.out[j] == b.g[j]) continue;  // in place, and nothing to change
     const int64_t base = static_cast<int64_t>(chunk - b.first[j]) * kChunk;
     Vector<T> x[kUnroll];

@@ -102,10 +102,6 @@ struct Raw8<uint16_t> {
     const Words4 u = bfp8::load_once(static_cast<const uint16_t*>(base) + at);
     w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
   }
-  // What follows unpacks the words again instead of keeping the values.
-  __device__ __forceinline__ void keep_packed() {
-    asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]));
-  }
   __device__ __forceinline__ float get(int i) const {
     return i & 1 ? __uint_as_float(w[i >> 1] & 0xFFFF0000u) : __uint_as_float(w[i >> 1] << 16);
   }
@@ -117,14 +113,9 @@ struct Raw8<float> {
   __device__ __forceinline__ void load(const void* base, int64_t at, int n) {
     Load8<float>::run(static_cast<const float*>(base) + at, v, n);
   }
-  __device__ __forceinline__ void load_once(const void* base, int64_t at) {
-    const float* p = static_cast<const float*>(base) + at;
-    const Words4 a = bfp8::load_once(p), b = bfp8::load_once(p + 4);
-    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
-  }
-  __device__ __forceinline__ void keep_packed() {}
+  // a lane's two halves share lines with its neighbours' and are loaded apart:
+  // through the caches after all
+  __device__ __forceinline__ void load_once(const void* base, int64_t at) { load(base, at, 8); }
   __device__ __forceinline__ float get(int i) const { return v[i]; }
 };
 
@@ -170,9 +161,10 @@ __device__ __forceinline__ typename ScaleRule<RULE>::type result_scale(float ama
 }
 
 // encode4 without its clamp: |v| <= amax gives |v * inv| <= 448 (1 + 2^-23),
-// which rounds to 448.
+// which rounds to 448.  (The first conversion leaves the upper half of the
+// register as it was, for the second; any dead one will do.)
 __device__ __forceinline__ uint32_t encode4_within(float a, float b, float c, float d) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, __float_as_int(a), false);
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
 }
 __device__ __forceinline__ uint2 encode8_within(const float (&v)[8], float inv) {
@@ -201,15 +193,41 @@ struct CodesOut {
   int64_t rows, cols;
 };
 
+// Largest sizes.  Sizes are not negative, so that their bits order as they do
+// and meet as integers: a maximum with another lane's is one instruction then.
+__device__ __forceinline__ uint32_t size8(const float (&v)[8]) {
+  return __float_as_uint(absmax8(v));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_with_lane(uint32_t v) {
+  const uint32_t w = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, true);
+  return v > w ? v : w;
+}
+// Of every row's sizes the largest in its group's lanes (16, or 4 for groups of 32).
+template <int GROUP, int N>
+__device__ __forceinline__ void group_max(uint32_t (&m)[N]) {
+  // quad_perm [1,0,3,2] and [2,3,0,1], row_half_mirror, row_mirror
+#pragma unroll
+  for (int u = 0; u < N; ++u) m[u] = max_with_lane<0xB1>(m[u]);
+#pragma unroll
+  for (int u = 0; u < N; ++u) m[u] = max_with_lane<0x4E>(m[u]);
+  if (GROUP == 32) return;
+#pragma unroll
+  for (int u = 0; u < N; ++u) m[u] = max_with_lane<0x141>(m[u]);
+#pragma unroll
+  for (int u = 0; u < N; ++u) m[u] = max_with_lane<0x140>(m[u]);
+}
+
 // Row groups from a row of 16 lanes that hold columns c0 + 8 lane .. + 7 of a
 // row (c0 a multiple of 128): codes and scales.
 template <int FORMAT>
 __device__ __forceinline__ void emit_row_chunk(const CodesOut& o, int64_t row, int64_t c0,
                                                int lane16, const float (&v)[8]) {
   typedef Codes<FORMAT> F;
-  const float amax = group_lanes_max<F::kGroupLen>(absmax8(v));
+  uint32_t m[1] = {size8(v)};
+  group_max<F::kGroupLen>(m);
   float inv;
-  const typename F::S sc = result_scale<F::kRule>(amax, inv);
+  const typename F::S sc = result_scale<F::kRule>(__uint_as_float(m[0]), inv);
   *reinterpret_cast<uint2*>(o.q + row * o.ldq + c0 + lane16 * 8) = encode8_within(v, inv);
   typename F::S* s = static_cast<typename F::S*>(o.s);
   if (F::kMajor) {
@@ -219,19 +237,19 @@ __device__ __forceinline__ void emit_row_chunk(const CodesOut& o, int64_t row, i
   }
 }
 
-// max over the two halves (rows of 16) of a wave for two values at once:
+// max over the two halves (rows of 16) of a wave for two sizes at once:
 // lanes of the lower half (of even rows) get a's, the others b's.
-__device__ __forceinline__ float halves_max(float a, float b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+__device__ __forceinline__ uint32_t halves_max(uint32_t a, uint32_t b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return r[0] > r[1] ? r[0] : r[1];
 }
-__device__ __forceinline__ float rows_max(float a, float b) {
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+__device__ __forceinline__ uint32_t rows_max(uint32_t a, uint32_t b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  return r[0] > r[1] ? r[0] : r[1];
 }
 template <int U>
 __device__ __forceinline__ float quad_broadcast(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), U * 0x55, 0xF, 0xF, false));
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), U * 0x55, 0xF, 0xF, true));
 }
 
 // The place of workgroup b of n in an order that gives each XCD (b mod 8) one
@@ -258,7 +276,7 @@ __device__ __forceinline__ unsigned xcd_run(unsigned b, unsigned n) {
 // writes after its own first barrier: tiles can follow each other.
 struct TileShared {
   uint8_t ct[128 * 128];
-  float colmax[8][128];
+  uint32_t colmax[8][128];
   float colinv[4][128];
   float rowscale[128];
 };
@@ -274,13 +292,14 @@ __device__ __forceinline__ void emit_tile(const CodesOut& o, int64_t m0, int64_t
   S* st = static_cast<S*>(o.st);
 
   // row groups
-  float am[4];
+  uint32_t am[4];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) am[u] = group_lanes_max<F::kGroupLen>(absmax8(v[u]));
+  for (int u = 0; u < 4; ++u) am[u] = size8(v[u]);
+  group_max<F::kGroupLen>(am);
   const int mine = tid & 3;
-  const float m01 = mine & 1 ? am[1] : am[0], m23 = mine & 1 ? am[3] : am[2];
+  const uint32_t m01 = mine & 1 ? am[1] : am[0], m23 = mine & 1 ? am[3] : am[2];
   float inv;
-  const S sc = result_scale<F::kRule>(mine & 2 ? m23 : m01, inv);
+  const S sc = result_scale<F::kRule>(__uint_as_float(mine & 2 ? m23 : m01), inv);
   const float invs[4] = {quad_broadcast<0>(inv), quad_broadcast<1>(inv), quad_broadcast<2>(inv),
                          quad_broadcast<3>(inv)};
 #pragma unroll
@@ -294,12 +313,13 @@ __device__ __forceinline__ void emit_tile(const CodesOut& o, int64_t m0, int64_t
   }
 
   // column maxima of the wave's 16 tokens
-  float cm[8];
+  uint32_t cm[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    cm[k] = fmaxf(fmaxf(fabsf(v[0][k]), fabsf(v[1][k])), fmaxf(fabsf(v[2][k]), fabsf(v[3][k])));
-  const float low = rows_max(halves_max(cm[0], cm[1]), halves_max(cm[2], cm[3]));
-  const float high = rows_max(halves_max(cm[4], cm[5]), halves_max(cm[6], cm[7]));
+    cm[k] = __float_as_uint(
+        fmaxf(fmaxf(fmaxf(fabsf(v[0][k]), fabsf(v[1][k])), fabsf(v[2][k])), fabsf(v[3][k])));
+  const uint32_t low = rows_max(halves_max(cm[0], cm[1]), halves_max(cm[2], cm[3]));
+  const uint32_t high = rows_max(halves_max(cm[4], cm[5]), halves_max(cm[6], cm[7]));
   const int kk = ((rsub & 1) << 1) | ((rsub >> 1) & 1);  // the channel this lane's row is left with
   sh.colmax[wave][lane16 * 8 + kk] = low;
   sh.colmax[wave][lane16 * 8 + kk + 4] = high;
@@ -308,13 +328,13 @@ __device__ __forceinline__ void emit_tile(const CodesOut& o, int64_t m0, int64_t
   if (F::kMajor && tid >= 128 && tid < 256) s[c0 / 128 * o.rows + m0 + tid - 128] = rowscale[tid - 128];
   if (F::kGroupLen == 32 || tid < 128) {
     const int c = tid & 127, p = tid >> 7;
-    float amax = fmaxf(sh.colmax[2 * p][c], sh.colmax[2 * p + 1][c]);
+    uint32_t m = max(sh.colmax[2 * p][c], sh.colmax[2 * p + 1][c]);
     if (F::kGroupLen == 128) {
 #pragma unroll
-      for (int w = 2; w < 8; ++w) amax = fmaxf(amax, sh.colmax[w][c]);
+      for (int w = 2; w < 8; ++w) m = max(m, sh.colmax[w][c]);
     }
     float cinv;
-    const S tsc = result_scale<F::kRule>(amax, cinv);
+    const S tsc = result_scale<F::kRule>(__uint_as_float(m), cinv);
     sh.colinv[p][c] = cinv;
     if (F::kMajor) st[m0 / 128 * o.cols + c0 + c] = tsc;
     else st[(c0 + c) * (o.rows / 32) + m0 / 32 + p] = tsc;

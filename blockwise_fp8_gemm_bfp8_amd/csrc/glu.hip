@@ -10,27 +10,23 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// e = exp(-g), at most 2^126 so that e / (1 + e) below stays a number where
-// sigma(g) is already 0 to float32.
-__device__ __forceinline__ float exp_minus(float g) {
-  return __builtin_amdgcn_exp2f(fminf(g * -kLog2e, 126.0f));
+// 1 / (1 + exp(-g)): an exponential that overflows gives 0, one that vanishes 1.
+__device__ __forceinline__ float sigma(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -kLog2e));
 }
 
-__device__ __forceinline__ float silu_gate(float g, float u) {
-  return g * __builtin_amdgcn_rcpf(1.0f + exp_minus(g)) * u;
-}
+__device__ __forceinline__ float silu_gate(float g, float u) { return g * sigma(g) * u; }
 
-// sigma(g) (1 + g (1 - sigma(g))), with 1 - sigma(g) = e sigma(g) free of
-// cancellation.
+// dgate = dh u sigma (1 + g (1 - sigma)).  1 - sigma is off by 2^-24 at most, which
+// g below 17 raises to 2^-20; from there on it is exactly 0.
 __device__ __forceinline__ void silu_gate_grad(float dh, float g, float u, float& dg, float& du) {
-  const float e = exp_minus(g);
-  const float s = __builtin_amdgcn_rcpf(1.0f + e);
-  dg = dh * u * (s * fmaf(g, e * s, 1.0f));
+  const float s = sigma(g);
+  dg = dh * u * (s * fmaf(g, 1.0f - s, 1.0f));
   du = dh * (g * s);
 }
 
-// Vectors of 8 values, one a thread.
-template <typename T, bool GRAD>
+// Vectors of 8 values, one a thread.  ONCE: loads past the caches.
+template <typename T, bool GRAD, bool ONCE>
 __global__ __launch_bounds__(256) void glu_values_kernel(GluArgs a, unsigned per_row, unsigned count) {
   const unsigned item = blockIdx.x * 256u + threadIdx.x;
   if (item >= count) return;
@@ -38,9 +34,15 @@ __global__ __launch_bounds__(256) void glu_values_kernel(GluArgs a, unsigned per
   const int64_t c = static_cast<int64_t>(item - row * per_row) * 8;
   const int n = valid8(c, a.cols);
   Raw8<T> g, u, dh;
-  g.load(a.gate, row * a.ldg + c, n);
-  u.load(a.up, row * a.ldu + c, n);
-  if (GRAD) dh.load(a.dh, row * a.lddh + c, n);
+  if (ONCE && n == 8) {
+    g.load_once(a.gate, row * a.ldg + c);
+    u.load_once(a.up, row * a.ldu + c);
+    if (GRAD) dh.load_once(a.dh, row * a.lddh + c);
+  } else {
+    g.load(a.gate, row * a.ldg + c, n);
+    u.load(a.up, row * a.ldu + c, n);
+    if (GRAD) dh.load(a.dh, row * a.lddh + c, n);
+  }
   float x[8], y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -51,23 +53,22 @@ __global__ __launch_bounds__(256) void glu_values_kernel(GluArgs a, unsigned per
   if (GRAD) store8(static_cast<T*>(a.b) + row * a.ldb + c, y, n);
 }
 
-// Row groups: 16 lanes a chunk of 128 columns.  With K-block-major scales
-// neighbouring chunks are neighbouring rows of one column block, whose scales
-// lie side by side.
+// Row groups: 16 lanes a chunk of 128 columns, 16 rows a workgroup, whose
+// K-block-major scales lie side by side; workgroups along the rows, in runs of
+// an XCD.  (Down the columns, and with loads through the caches, the 16384 x 6144
+// activation took 118 us and its gradient 172; so 87 and 129.)
 template <typename T, int FORMAT, bool GRAD>
-__global__ __launch_bounds__(256) void glu_rows_kernel(GluArgs a, unsigned chunks, unsigned per_row,
-                                                       CodesOut o) {
-  const unsigned chunk = blockIdx.x * 16u + (threadIdx.x >> 4);
-  if (chunk >= chunks) return;
+__global__ __launch_bounds__(256) void glu_rows_kernel(GluArgs a, unsigned per_row, CodesOut o) {
+  const unsigned chunk = xcd_run(blockIdx.x, gridDim.x);
+  const unsigned block = chunk / per_row;
+  const int64_t row = static_cast<int64_t>(block) * 16 + (threadIdx.x >> 4);
+  if (row >= a.rows) return;
   const int lane16 = threadIdx.x & 15;
-  const unsigned rows = static_cast<unsigned>(a.rows);
-  const unsigned block = Codes<FORMAT>::kMajor ? chunk / rows : chunk % per_row;
-  const int64_t row = Codes<FORMAT>::kMajor ? chunk - block * rows : chunk / per_row;
-  const int64_t c0 = static_cast<int64_t>(block) * 128, c = c0 + lane16 * 8;
+  const int64_t c0 = static_cast<int64_t>(chunk - block * per_row) * 128, c = c0 + lane16 * 8;
   Raw8<T> g, u, dh;
-  g.load(a.gate, row * a.ldg + c, 8);
-  u.load(a.up, row * a.ldu + c, 8);
-  if (GRAD) dh.load(a.dh, row * a.lddh + c, 8);
+  g.load_once(a.gate, row * a.ldg + c);
+  u.load_once(a.up, row * a.ldu + c);
+  if (GRAD) dh.load_once(a.dh, row * a.lddh + c);
   float x[8], y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -93,38 +94,41 @@ __global__ __launch_bounds__(kTileThreads) void glu_tile_kernel(GluArgs a, unsig
     u[i].load_once(a.up, (m + i) * a.ldu + c);
     if (GRAD) dh[i].load_once(a.dh, (m + i) * a.lddh + c);
   }
-  float x[4][8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float du;
-      if (GRAD) silu_gate_grad(dh[i].get(k), g[i].get(k), u[i].get(k), x[i][k], du);
-      else x[i][k] = silu_gate(g[i].get(k), u[i].get(k));
-    }
-  emit_tile<FORMAT>(o, m0, c0, x, sh);
-  if (!GRAD) return;
-  // dup is computed after dgate has left, from the inputs again: with both kept
-  // a thread needs 156 registers and one workgroup fits a CU (236 -> 218 us)
+  // Row by row, each one's results pinned before the next: left to itself the
+  // compiler unpacks everything first, 156 registers, and one workgroup fits a
+  // CU (93, two: 236 -> 164 us for the gradient of 16384 x 6144, where computing
+  // dup from the inputs again after dgate has left took 182).
+  float x[4][8], y[4][8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    g[i].keep_packed();
-    dh[i].keep_packed();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float dg;
-      silu_gate_grad(dh[i].get(k), g[i].get(k), 1.0f, dg, x[i][k]);
+      if (GRAD) silu_gate_grad(dh[i].get(k), g[i].get(k), u[i].get(k), x[i][k], y[i][k]);
+      else x[i][k] = silu_gate(g[i].get(k), u[i].get(k));
+    }
+    if (GRAD) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) asm volatile("" : "+v"(x[i][k]), "+v"(y[i][k]));
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
-  emit_tile<FORMAT>(o, m0, a.cols + c0, x, sh);
+  emit_tile<FORMAT>(o, m0, c0, x, sh);
+  if (GRAD) emit_tile<FORMAT>(o, m0, a.cols + c0, y, sh);
 }
+
+// Above this many bytes of gate the loads of bf16 values go past the caches: 201 MB
+// with up took 88 us so and 104 otherwise, where 16 MB with up and dh, read again and
+// again, took 16.8 and 14.3.
+constexpr int64_t kLargeGate = int64_t(64) << 20;
 
 template <typename T, bool GRAD>
 bfp8_status values_typed(const GluArgs& a, hipStream_t stream) {
   const int64_t per_row = (a.cols + 7) / 8, count = a.rows * per_row, blocks = (count + 255) / 256;
   if (!threads_fit(blocks, 256)) return BFP8_ERR_SHAPE;
-  return launch(glu_values_kernel<T, GRAD>, dim3(static_cast<unsigned>(blocks)), dim3(256), stream,
-                a, static_cast<unsigned>(per_row), static_cast<unsigned>(count));
+  const bool once = sizeof(T) == 2 && a.rows * a.cols * 2 > kLargeGate;
+  return launch(once ? glu_values_kernel<T, GRAD, sizeof(T) == 2> : glu_values_kernel<T, GRAD, false>,
+                dim3(static_cast<unsigned>(blocks)), dim3(256), stream, a,
+                static_cast<unsigned>(per_row), static_cast<unsigned>(count));
 }
 
 template <typename T, bool GRAD>
@@ -132,11 +136,11 @@ bfp8_status codes_typed(const GluArgs& a, bfp8_code_format format, const CodesOu
                         hipStream_t stream) {
   const int64_t per_row = a.cols / 128;
   if (o.qt == nullptr) {
-    const int64_t chunks = a.rows * per_row, blocks = (chunks + 15) / 16;
+    const int64_t blocks = (a.rows + 15) / 16 * per_row;
     if (!threads_fit(blocks, 256)) return BFP8_ERR_SHAPE;
     return BFP8_WITH_FORMAT(
         format, (launch(glu_rows_kernel<T, F, GRAD>, dim3(static_cast<unsigned>(blocks)), dim3(256),
-                        stream, a, static_cast<unsigned>(chunks), static_cast<unsigned>(per_row), o)));
+                        stream, a, static_cast<unsigned>(per_row), o)));
   }
   const int64_t tiles = a.rows / 128 * per_row;
   return BFP8_WITH_FORMAT(

@@ -49,7 +49,7 @@ __device__ __forceinline__ void load_weight(const void* w, bool f32, int lane, i
   }
 }
 
-constexpr int block_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+constexpr int block_threads(int tpr) { return tpr <= 64 ? 256 : tpr; }
 
 // What a pass over the rows leaves beside r and rstd.
 constexpr int kStats = -2, kValues = -1;  // otherwise a bfp8_code_format
@@ -59,7 +59,7 @@ constexpr int kStats = -2, kValues = -1;  // otherwise a bfp8_code_format
 // lanes hold a 128-group.
 template <typename T, int TPR, int NV, int OUT>
 __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs a, CodesOut o) {
-  __shared__ float parts[2][TPR < 256 ? 1 : TPR / 64];
+  __shared__ float parts[2][TPR <= 64 ? 1 : TPR / 64];
   constexpr int kRows = block_threads(TPR) / TPR;  // of a workgroup at once
   const int lane = threadIdx.x % TPR;
   float w[NV][8];
@@ -112,15 +112,18 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs 
   }
 }
 
-// The threads and vectors of a row: the fewest that hold it.
-#define BFP8_WITH_ROW(cols, CALL)                                               \
-  ((cols) <= 128     ? [&] { constexpr int P = 16, V = 1; return CALL; }()      \
-   : (cols) <= 512   ? [&] { constexpr int P = 64, V = 1; return CALL; }()      \
-   : (cols) <= 1024  ? [&] { constexpr int P = 64, V = 2; return CALL; }()      \
-   : (cols) <= 2048  ? [&] { constexpr int P = 64, V = 4; return CALL; }()      \
-   : (cols) <= 4096  ? [&] { constexpr int P = 256, V = 2; return CALL; }()     \
-   : (cols) <= 8192  ? [&] { constexpr int P = 256, V = 4; return CALL; }()     \
-                     : [&] { constexpr int P = 1024, V = 2; return CALL; }())
+// The threads P and vectors V of a row; those of 1025 to 2048 columns, where the
+// kernels differ most, as given.  Two vectors a thread read a large matrix as fast
+// as one or four (16384 x 2048 to values 43 us each, 4096 x 8192 44 to 45) and a
+// few rows sooner than four (16 x 8192 3.9 us against 4.5).
+#define BFP8_WITH_ROW(cols, P2048, V2048, CALL)                                   \
+  ((cols) <= 128    ? [&] { constexpr int P = 16, V = 1; return CALL; }()         \
+   : (cols) <= 512  ? [&] { constexpr int P = 64, V = 1; return CALL; }()         \
+   : (cols) <= 1024 ? [&] { constexpr int P = 64, V = 2; return CALL; }()         \
+   : (cols) <= 2048 ? [&] { constexpr int P = P2048, V = V2048; return CALL; }()  \
+   : (cols) <= 4096 ? [&] { constexpr int P = 256, V = 2; return CALL; }()        \
+   : (cols) <= 8192 ? [&] { constexpr int P = 512, V = 2; return CALL; }()        \
+                    : [&] { constexpr int P = 1024, V = 2; return CALL; }())
 
 template <typename T, int TPR, int NV, int OUT>
 bfp8_status launch_rows(const NormArgs& a, const CodesOut& o, hipStream_t stream) {
@@ -131,7 +134,11 @@ bfp8_status launch_rows(const NormArgs& a, const CodesOut& o, hipStream_t stream
 }
 template <typename T, int OUT>
 bfp8_status launch_rows_of(const NormArgs& a, const CodesOut& o, hipStream_t stream) {
-  return BFP8_WITH_ROW(a.cols, (launch_rows<T, P, V, OUT>(a, o, stream)));
+  // one vector a thread is as fast where all is written (43 us), and sooner done
+  // with a few rows (16 x 2048 3.3 us against 3.7) and with odd ones (5003 x 1111
+  // 11.0 against 12.9), but not where r alone is (32.4 against 31.4)
+  return BFP8_WITH_ROW(a.cols, (OUT == kStats ? 128 : 256), (OUT == kStats ? 2 : 1),
+                       (launch_rows<T, P, V, OUT>(a, o, stream)));
 }
 
 // Both layouts' codes of a tile from r and the rows' statistics.  A row's
@@ -179,17 +186,13 @@ bfp8_status quantize_typed(const NormArgs& a, bfp8_code_format format, const Cod
 
 // ---- gradient ------------------------------------------------------------------
 
-// Workgroups of the gradient, each with partial sums of dw to write and to be
-// read: as many as run at once (two a CU, by their registers).  At 16384 x 2048
-// 256, 512 and 1024 took 57, 52 and 55 us.
-constexpr int64_t kGradGroups = 512;
 
 // Rows in turn, the weight and this workgroup's share of dw in registers; the
 // waves' shares meet in LDS at the end and leave as one row of `partial`.
 template <typename T, int TPR, int NV>
 __global__ __launch_bounds__(block_threads(TPR)) void norm_grad_kernel(NormGradArgs a) {
   constexpr int kThreads = block_threads(TPR), kRows = kThreads / TPR;
-  __shared__ float parts[2][TPR < 256 ? 1 : TPR / 64];
+  __shared__ float parts[2][TPR <= 64 ? 1 : TPR / 64];
   __shared__ __attribute__((aligned(16))) float joined[kRows > 1 ? kRows / 2 * TPR * NV * 8 : 4];
   const int lane = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   float w[NV][8], dw[NV][8];
@@ -291,13 +294,24 @@ __global__ __launch_bounds__(8 * kSumSlots) void norm_grad_sum_kernel(const floa
 }
 
 template <typename T, int TPR, int NV>
-bfp8_status launch_grad(const NormGradArgs& a, int64_t groups, hipStream_t stream) {
-  return launch(norm_grad_kernel<T, TPR, NV>, dim3(static_cast<unsigned>(groups)),
-                dim3(block_threads(TPR)), stream, a);
+bfp8_status launch_grad(const NormGradArgs& a, hipStream_t stream) {
+  constexpr int kRows = block_threads(TPR) / TPR;
+  const int64_t groups = std::min((a.rows + kRows - 1) / kRows, norm_grad_groups(a.rows, a.cols));
+  if (groups > 0) {
+    const bfp8_status st = launch(norm_grad_kernel<T, TPR, NV>, dim3(static_cast<unsigned>(groups)),
+                                  dim3(block_threads(TPR)), stream, a);
+    if (st != BFP8_OK) return st;
+  }
+  return launch(norm_grad_sum_kernel, dim3((a.cols + 31) / 32), dim3(8 * kSumSlots), stream,
+                a.partial, static_cast<int>(groups), a.cols, a.dw);
 }
 template <typename T>
-bfp8_status launch_grad_of(const NormGradArgs& a, int64_t groups, hipStream_t stream) {
-  return BFP8_WITH_ROW(a.cols, (launch_grad<T, P, V>(a, groups, stream)));
+bfp8_status launch_grad_of(const NormGradArgs& a, hipStream_t stream) {
+  // bf16 rows of up to 2048 a wave each, so that none waits for another wave (16384
+  // x 2048 43 us against 45); fp32 rows need too many registers for that (8192 x
+  // 2048 58 us, 53 with two waves a row)
+  return BFP8_WITH_ROW(a.cols, (sizeof(T) == 2 ? 64 : 128), (sizeof(T) == 2 ? 4 : 2),
+                       (launch_grad<T, P, V>(a, stream)));
 }
 
 }  // namespace
@@ -313,20 +327,15 @@ bfp8_status launch_rmsnorm_quantize(const NormArgs& a, bfp8_in_dtype dt, bfp8_co
                            : quantize_typed<uint16_t>(a, format, o, stream);
 }
 
+// Workgroups of the gradient at most.  Each has partial sums of dw to write and to
+// be read: as many as run at once, two a CU by their registers, or one of 1024
+// threads.  (The whole call at 16384 x 2048 with 256, 512 and 1024: 57, 52, 55 us.)
 int64_t norm_grad_groups(int64_t rows, int64_t cols) {
-  const int64_t at_once = cols <= 128 ? 16 : cols <= 2048 ? 4 : 1;  // rows of a workgroup
-  return std::min<int64_t>((rows + at_once - 1) / at_once, kGradGroups);
+  return std::min<int64_t>(rows, cols <= 8192 ? 512 : 256);
 }
 
 bfp8_status launch_rmsnorm_backward(const NormGradArgs& a, bfp8_in_dtype dt, hipStream_t stream) {
-  const int64_t groups = norm_grad_groups(a.rows, a.cols);
-  if (groups > 0) {
-    const bfp8_status st = dt == BFP8_IN_F32 ? launch_grad_of<float>(a, groups, stream)
-                                             : launch_grad_of<uint16_t>(a, groups, stream);
-    if (st != BFP8_OK) return st;
-  }
-  return launch(norm_grad_sum_kernel, dim3((a.cols + 31) / 32), dim3(8 * kSumSlots), stream,
-                a.partial, static_cast<int>(groups), a.cols, a.dw);
+  return dt == BFP8_IN_F32 ? launch_grad_of<float>(a, stream) : launch_grad_of<uint16_t>(a, stream);
 }
 
 }  // namespace bfp8
