@@ -8,6 +8,10 @@ sequences, and the FP8 output projection.
              written as rows [dq | dk | dv] -> turn dq and dk back in place
              -> quantise -> QKV dgrad and wgrad -> dx, dw_qkv, dw_o
 
+With a norm's weight the block begins as mlp_block's does: r = x + residual and
+the codes of norm(r) in place of x's, and its backward pass ends in the norm's
+gradient, to which the gradient of r is added.
+
 The linears run as in ``hotpath`` (Puro-2B paper translation, section 3.2: 1x128
 groups and 128x128 weight blocks, both layouts of an activation from one read,
 scales K-block major); attention and the rotation stay in bf16 (Puro-2B
@@ -19,7 +23,8 @@ enqueues kernels on the current stream, so it can be captured into a graph.
 import torch
 
 from . import (attention_backward, attention_forward, attention_workspace_bytes, gemm,
-               gemm_workspace_bytes, quantize_act_dual_kmajor, quantize_weight_batch, rope)
+               gemm_workspace_bytes, quantize_act_dual_kmajor, quantize_weight_batch,
+               rmsnorm_backward, rmsnorm_backward_workspace_bytes, rmsnorm_quantize, rope)
 
 
 class AttentionBlock:
@@ -32,11 +37,13 @@ class AttentionBlock:
     other values in every pass: rows of no sequence (before cu[0], from cu[-1]
     on) count as zeros where attention leaves off, so y and dx are 0 there and
     the weights' gradients take nothing from them, whatever their positions.
-    x and dy must be finite there, as they share a 128-token group's scale.
+    x and dy must be finite there, as they share a 128-token group's scale.  With
+    `w_norm` ([hidden], bfloat16 or float32) that goes for the residual and dr, too,
+    and dx is dr there.
     (BFP8_DEBUG's scan takes a position outside the table for what it gives: NaN.)"""
 
     def __init__(self, w_qkv, w_o, heads: int, kv_heads: int, tokens: int, cu, positions, table,
-                 scale: float = None):
+                 scale: float = None, w_norm=None, eps: float = 1e-6):
         rows, hidden = w_qkv.shape
         if rows % (heads + 2 * kv_heads):
             raise ValueError(f"w_qkv has {rows} rows, not a multiple of {heads + 2 * kv_heads} heads")
@@ -47,7 +54,9 @@ class AttentionBlock:
                         ("heads * head_dim", heads * D)):
             if n % 128:
                 raise ValueError(f"{name} must be a multiple of 128, got {n}")
-        self.w_qkv, self.w_o = w_qkv, w_o
+        if w_norm is not None and tuple(w_norm.shape) != (hidden,):
+            raise ValueError(f"w_norm must be [{hidden}], got {tuple(w_norm.shape)}")
+        self.w_qkv, self.w_o, self.w_norm, self.eps = w_qkv, w_o, w_norm, eps
         self.heads, self.kv_heads, self.head_dim, self.scale = heads, kv_heads, D, scale
         self.cu, self.positions, self.table = cu, positions, table
         self._quantized = self._ran = False  # what the buffers hold
@@ -70,6 +79,10 @@ class AttentionBlock:
         b["lse"] = new((heads, M), f32)
         b["y"], b["dx"] = new((M, hidden), bf), new((M, hidden), bf)
         b["dw_qkv"], b["dw_o"] = new((rows, hidden), bf), new((hidden, E), bf)
+        if w_norm is not None:
+            b["r"], b["rstd"] = new((M, hidden), bf), new((M,), f32)
+            b["dn"], b["dw_norm"] = new((M, hidden), bf), new((hidden,), f32)
+            b["norm_ws"] = new((rmsnorm_backward_workspace_bytes(M, hidden),), u8)
         need = max(gemm_workspace_bytes("NT", "act_km", "act_km", rows, hidden, M),
                    gemm_workspace_bytes("NT", "act_km", "act_km", hidden, E, M), 16)
         b["gemm_ws"] = new((need,), u8)
@@ -99,15 +112,27 @@ class AttentionBlock:
                               [b["wqkv_s"], b["wo_s"]])
         self._quantized = True
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
+    def _check_norm(self, t, name):
+        if (t is None) != (self.w_norm is None):
+            raise ValueError(f"{name} comes with a norm's weight, and only with one")
+        if t is not None:
+            self._check_rows(t, name)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor = None):
         """y [tokens][hidden] of x [tokens][hidden] (bfloat16); the buffers keep
-        what backward needs."""
+        what backward needs.  With a norm: (y, r) of x and the residual stream, r =
+        x + residual, to which y is yet to be added."""
         self._check_rows(x, "x")
+        self._check_norm(residual, "residual")
         if not self._quantized:
             raise RuntimeError("quantize_weights() comes before the first forward")
         b = self.buf
         M = b["y"].shape[0]
-        quantize_act_dual_kmajor(x, b["xq"], b["xs"], b["xqt"], b["xst"])
+        if self.w_norm is None:
+            quantize_act_dual_kmajor(x, b["xq"], b["xs"], b["xqt"], b["xst"])
+        else:
+            rmsnorm_quantize(x, self.w_norm, residual, eps=self.eps, transposed=True, q=b["xq"],
+                             s=b["xs"], qt=b["xqt"], st=b["xst"], sum_out=b["r"], rstd=b["rstd"])
         gemm("NT", b["xq"], b["xs"], b["wqkv_q"], b["wqkv_s"], "act_km", "block",
              out=b["qkv"].view(M, -1), workspace=b["gemm_ws"])
         self._turn(b["qkv"], False)
@@ -115,12 +140,16 @@ class AttentionBlock:
                           lse=b["lse"], workspace=b["attn_ws"], zero_rest=True)
         quantize_act_dual_kmajor(b["a"].view(M, -1), b["aq"], b["as"], b["aqt"], b["ast"])
         self._ran = True
-        return gemm("NT", b["aq"], b["as"], b["wo_q"], b["wo_s"], "act_km", "block", out=b["y"],
-                    workspace=b["gemm_ws"])
+        gemm("NT", b["aq"], b["as"], b["wo_q"], b["wo_s"], "act_km", "block", out=b["y"],
+             workspace=b["gemm_ws"])
+        return b["y"] if self.w_norm is None else (b["y"], b["r"])
 
-    def backward(self, dy: torch.Tensor):
-        """(dx, dw_qkv, dw_o) for the gradient dy of the last forward's y."""
+    def backward(self, dy: torch.Tensor, dr: torch.Tensor = None):
+        """(dx, dw_qkv, dw_o) for the gradient dy of the last forward's y.  With a
+        norm: (dx, dw_qkv, dw_o, dw_norm) for that and the gradient dr of r; dx is
+        the gradient of x and of the residual."""
         self._check_rows(dy, "dy")
+        self._check_norm(dr, "dr")
         if not self._ran:
             raise RuntimeError("forward() comes before backward")
         b = self.buf
@@ -138,7 +167,11 @@ class AttentionBlock:
         quantize_act_dual_kmajor(b["dqkv"].view(M, -1), b["dqkvq"], b["dqkvs"], b["dqkvqt"],
                                  b["dqkvst"])
         gemm("NN", b["dqkvq"], b["dqkvs"], b["wqkv_q"], b["wqkv_s"], "act_km", "block",
-             out=b["dx"], workspace=b["gemm_ws"])
+             out=b["dx" if self.w_norm is None else "dn"], workspace=b["gemm_ws"])
         gemm("NT", b["dqkvqt"], b["dqkvst"], b["xqt"], b["xst"], "act_km", "act_km",
              out=b["dw_qkv"], workspace=b["gemm_ws"])
-        return b["dx"], b["dw_qkv"], b["dw_o"]
+        if self.w_norm is None:
+            return b["dx"], b["dw_qkv"], b["dw_o"]
+        rmsnorm_backward(b["dn"], b["r"], self.w_norm, b["rstd"], dr, dx=b["dx"],
+                         dweight=b["dw_norm"], workspace=b["norm_ws"])
+        return b["dx"], b["dw_qkv"], b["dw_o"], b["dw_norm"]

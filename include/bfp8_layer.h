@@ -46,7 +46,7 @@
  * row); with BFP8_DEBUG (see bfp8.h) these calls scan their inputs for them.
  *
  * Sizes.  rows < 2^31 (rows of a norm's gradient: any such); 2^32 vectors of 8
- * values or more in an activation, or 2^24 tiles of 128 x 128 values in a call
+ * values or more in an activation, or 2^23 tiles of 128 x 128 values in a call
  * that writes qt, are refused with BFP8_ERR_SHAPE.  Empty problems launch
  * nothing, except that the gradient of a norm's weight over no rows is written
  * as zeros.
