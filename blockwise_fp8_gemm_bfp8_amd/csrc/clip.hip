@@ -62,7 +62,7 @@ struct Vector {
     }
   }
   __device__ __forceinline__ void store(T* p) const {
-    __builtin_nontemporal_store(Words4{w[0], w[1], w[2], w[3]}, reinterpret_cast<Words4*>(p));
+    store_once(p, make_uint4(w[0], w[1], w[2], w[3]));
   }
   __device__ __forceinline__ void store_part(T* row, int64_t c, int64_t cols) const {
     if (c >= 0 && c + N <= cols && (reinterpret_cast<uintptr_t>(row + c) & 15) == 0)

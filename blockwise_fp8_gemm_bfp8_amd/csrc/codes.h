@@ -66,15 +66,13 @@ __device__ __forceinline__ float group_lanes_max(float v) {
 }
 
 // Loads and stores of what is read or written once and by nobody else soon:
-// they leave the L2 to data in between (the code tiles below: 126 -> 98 us with
-// such loads and the tiles' order, 16384 x 6144 gated activations).
+// they leave the caches to data in between.
 typedef uint32_t Words4 __attribute__((ext_vector_type(4)));
-typedef uint32_t Words2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ Words4 load_once(const void* p) {
   return __builtin_nontemporal_load(static_cast<const Words4*>(p));
 }
-__device__ __forceinline__ void store_once(void* p, uint2 v) {
-  __builtin_nontemporal_store(Words2{v.x, v.y}, static_cast<Words2*>(p));
+__device__ __forceinline__ void store_once(void* p, uint4 v) {
+  __builtin_nontemporal_store(Words4{v.x, v.y, v.z, v.w}, static_cast<Words4*>(p));
 }
 
 // Eight elements as loaded, `n` (0..8) of them valid, the others zero: loads
@@ -269,9 +267,11 @@ __device__ __forceinline__ unsigned xcd_run(unsigned b, unsigned n) {
 // the waves in LDS, where one thread a group makes the scale.  The codes of a
 // channel's four tokens are one dword of the LDS tile [channel][token], whose
 // 16-byte chunks are permuted by channel / 8 to spread the writes over the
-// banks; its rows leave as 128-byte runs.  (Row codes leave past the L2, which
-// the transposed ones need: of both, either and neither 208, 196, 180 and 181 us
-// for the gradient of 16384 x 6144 gated activations, neither first.)
+// banks; its rows leave as 128-byte runs, past the caches, which are left to the
+// row codes: those are the next GEMM's operand, the transposed ones wait for the
+// backward pass.  (MLPBlock's forward pass over 16384 tokens 719 us so, 740 the
+// other way round; alone the activation's tiles take 97 us either way and 120
+// with both kept, their gradient's 198 and 202.)
 //   The last barrier's reads are of the code tile alone, which the next call
 // writes after its own first barrier: tiles can follow each other.
 struct TileShared {
@@ -304,7 +304,8 @@ __device__ __forceinline__ void emit_tile(const CodesOut& o, int64_t m0, int64_t
                          quad_broadcast<3>(inv)};
 #pragma unroll
   for (int u = 0; u < 4; ++u)
-    store_once(o.q + (m0 + 4 * rsub + u) * o.ldq + c0 + lane16 * 8, encode8_within(v[u], invs[u]));
+    *reinterpret_cast<uint2*>(o.q + (m0 + 4 * rsub + u) * o.ldq + c0 + lane16 * 8) =
+        encode8_within(v[u], invs[u]);
   S* rowscale = reinterpret_cast<S*>(sh.rowscale);
   if (F::kMajor) {
     if (lane16 < 4) rowscale[4 * rsub + lane16] = sc;
@@ -356,7 +357,7 @@ __device__ __forceinline__ void emit_tile(const CodesOut& o, int64_t m0, int64_t
   for (int pass = 0; pass < 2; ++pass) {
     const int c = pass * 64 + (tid >> 3), ch = tid & 7;
     const uint4 w = *reinterpret_cast<const uint4*>(&sh.ct[c * 128 + (ch ^ ((c >> 3) & 7)) * 16]);
-    *reinterpret_cast<uint4*>(o.qt + (c0 + c) * o.ldqt + m0 + ch * 16) = w;
+    store_once(o.qt + (c0 + c) * o.ldqt + m0 + ch * 16, w);
   }
 }
 

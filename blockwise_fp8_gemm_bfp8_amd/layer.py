@@ -13,6 +13,7 @@ import torch
 from . import DTYPES, BFP8Error, GradJob, _padded_empty, _scale_bytes, lib
 from .attention import _pointer, _stream_of
 
+_ANY = tuple(DTYPES)
 CODE_FORMATS = {"fp32": 0, "mx128": 1, "mx32": 2}  # hotpath's scale formats
 _INVALID = ctypes.c_size_t(-1).value
 
@@ -129,7 +130,7 @@ def _norm_inputs(x, weight, residual, sum_out, rstd):
     device = x.get_device()
     ldx = _matrix(x, "x")
     rows, cols = x.shape
-    _vector(weight, "weight", cols, device, tuple(DTYPES))
+    _vector(weight, "weight", cols, device, _ANY)
     ldr = lds = 0
     if residual is not None:
         ldr = _matrix(residual, "residual", device, x.shape, x.dtype)
@@ -192,7 +193,7 @@ def rmsnorm_backward(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rs
     lddy = _matrix(dy, "dy")
     rows, cols = dy.shape
     ldr = _matrix(r, "r", device, dy.shape, dy.dtype)
-    _vector(weight, "weight", cols, device, tuple(DTYPES))
+    _vector(weight, "weight", cols, device, _ANY)
     _vector(rstd, "rstd", rows, device)
     lds = _matrix(dsum, "dsum", device, dy.shape, dy.dtype) if dsum is not None else 0
     dx, lddx = _result(dx, dy, "dx", device)
