@@ -30,6 +30,11 @@ bfp8_status check_matrix(const void* p, int64_t ld, int64_t cols, int64_t size) 
   return ld * size % 16 == 0 ? BFP8_OK : BFP8_ERR_ALIGN;
 }
 
+// An output that is an input itself has to have its rows where the input has them.
+bool shifted(const void* out, int64_t ldo, const void* in, int64_t ldi, int64_t rows) {
+  return out == in && rows > 1 && ldo != ldi;
+}
+
 bfp8_status check_sizes(bfp8_in_dtype dt, int64_t rows, int64_t cols) {
   if (!is_dtype(dt)) return BFP8_ERR_DTYPE;
   if (rows < 0 || rows >= kMaxRows || cols < 0) return BFP8_ERR_SHAPE;
@@ -64,6 +69,9 @@ bfp8_status check_norm(const NormArgs& a, bfp8_in_dtype wdt, bfp8_in_dtype dt) {
   if (st == BFP8_OK && a.residual != nullptr) {
     st = check_matrix(a.residual, a.ldres, a.cols, size);
     if (st == BFP8_OK) st = check_matrix(a.sum, a.ldsum, a.cols, size);
+    if (st == BFP8_OK && (shifted(a.sum, a.ldsum, a.x, a.ldx, a.rows) ||
+                          shifted(a.sum, a.ldsum, a.residual, a.ldres, a.rows)))
+      st = BFP8_ERR_SHAPE;
   }
   if (st != BFP8_OK) return st;
   if (a.w == nullptr || a.rstd == nullptr) return BFP8_ERR_NULL;
@@ -116,6 +124,8 @@ bfp8_status bfp8_rmsnorm(const void* x, int64_t ldx, const void* residual, int64
                    static_cast<int>(cols), eps};
   if ((st = check_norm(a, wdt, dt)) != BFP8_OK) return st;
   if ((st = check_matrix(y, ldy, cols, bytes_of(dt))) != BFP8_OK) return st;
+  if (shifted(y, ldy, x, ldx, rows) || (residual != nullptr && (shifted(y, ldy, residual, ldres, rows) || y == sum)))
+    return BFP8_ERR_SHAPE;
   return launch_rmsnorm(a, dt, stream);
 }
 
@@ -162,6 +172,9 @@ bfp8_status bfp8_rmsnorm_backward(const void* dy, int64_t lddy, const void* r, i
     if ((st = check_matrix(r, ldr, cols, size)) != BFP8_OK) return st;
     if ((st = check_matrix(dx, lddx, cols, size)) != BFP8_OK) return st;
     if (dsum != nullptr && (st = check_matrix(dsum, lddsum, cols, size)) != BFP8_OK) return st;
+    if (shifted(dx, lddx, dy, lddy, rows) || shifted(dx, lddx, r, ldr, rows) ||
+        (dsum != nullptr && shifted(dx, lddx, dsum, lddsum, rows)))
+      return BFP8_ERR_SHAPE;
     if (w == nullptr || rstd == nullptr) return BFP8_ERR_NULL;
     if (!aligned16(w) || !aligned16(rstd) || !aligned16(workspace)) return BFP8_ERR_ALIGN;
     if (workspace == nullptr || workspace_bytes < bfp8_rmsnorm_backward_workspace_bytes(rows, cols))
@@ -181,6 +194,7 @@ bfp8_status bfp8_swiglu(const void* gate, int64_t ldg, const void* up, int64_t l
   if ((st = check_matrix(gate, ldg, cols, size)) != BFP8_OK) return st;
   if ((st = check_matrix(up, ldu, cols, size)) != BFP8_OK) return st;
   if ((st = check_matrix(h, ldh, cols, size)) != BFP8_OK) return st;
+  if (shifted(h, ldh, gate, ldg, rows) || shifted(h, ldh, up, ldu, rows)) return BFP8_ERR_SHAPE;
   const GluArgs a{gate, ldg, up, ldu, nullptr, 0, h, ldh, nullptr, 0, rows, cols};
   return launch_swiglu(a, dt, stream);
 }
@@ -197,6 +211,10 @@ bfp8_status bfp8_swiglu_backward(const void* dh, int64_t lddh, const void* gate,
   if ((st = check_matrix(up, ldu, cols, size)) != BFP8_OK) return st;
   if ((st = check_matrix(dgate, lddg, cols, size)) != BFP8_OK) return st;
   if ((st = check_matrix(dup, lddu, cols, size)) != BFP8_OK) return st;
+  if (dgate == dup) return BFP8_ERR_SHAPE;
+  for (const auto& in : {std::pair{dh, lddh}, std::pair{gate, ldg}, std::pair{up, ldu}})
+    if (shifted(dgate, lddg, in.first, in.second, rows) || shifted(dup, lddu, in.first, in.second, rows))
+      return BFP8_ERR_SHAPE;
   const GluArgs a{gate, ldg, up, ldu, dh, lddh, dgate, lddg, dup, lddu, rows, cols};
   return launch_swiglu(a, dt, stream);
 }

@@ -151,8 +151,8 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor = None
             rstd: torch.Tensor = None):
     """r = x + residual (x without one), y = r / sqrt(mean(r^2) + eps) * weight for
     rows x [rows][cols] (bfloat16 or float32) -> (y, r, rstd float32 [rows]).
-    r and rstd are what the gradient needs; ``sum_out=residual`` adds in place.
-    See bfp8_rmsnorm."""
+    r and rstd are what the gradient needs; ``sum_out=residual`` adds in place (and
+    ``out=x`` without a residual gives r up).  See bfp8_rmsnorm."""
     device, head, sum_out, lds, rstd = _norm_inputs(x, weight, residual, sum_out, rstd)
     out, ldy = _result(out, x, "out", device)
     _call("bfp8_rmsnorm", device, *head, eps, _pointer(sum_out), lds, out.data_ptr(), ldy,
@@ -283,7 +283,8 @@ class GradClip:
     table of their places is made once.
 
     out   where the clipped gradients go, tensors of the same shapes and types;
-          None: in place.
+          None: in place.  A place written twice, or another gradient's, is
+          refused, so a gradient is listed once.
 
     norm() is the square root of the sum of all squares (float32 0-d device
     tensor); clip(max_norm) scales by max_norm / norm where the norm exceeds
@@ -310,6 +311,13 @@ class GradClip:
                 ldg, ldo = (t.stride(0) if rows > 1 else cols for t in (g, o))
             self._jobs[i] = GradJob(g.data_ptr(), o.data_ptr(), rows, cols, ldg, ldo,
                                     DTYPES[g.dtype])
+        source = {g.data_ptr(): i for i, g in enumerate(self.grads) if g.numel()}
+        written = set()
+        for i, o in enumerate(self.out):
+            at = o.data_ptr()
+            if o.numel() and (at in written or source.get(at, i) != i):
+                raise ValueError(f"out[{i}] is written twice, or another gradient's place")
+            written.add(at)
         n = lib().bfp8_grad_norm_workspace_bytes(self._jobs, len(self._jobs))
         if n == _INVALID:
             raise ValueError("invalid gradients")

@@ -20,9 +20,9 @@
  * times the element's size a multiple of 16), ld >= cols.  All arithmetic is
  * float32; a value is rounded to dt, or to E4M3, once, where it is stored.
  * Only the cols values of a row are written, never its padding.  An output may
- * be one of the call's dt inputs itself (same pointer and ld), but outputs never
- * overlap each other, and no other overlap is allowed; codes and scales overlap
- * nothing.
+ * be one of the call's dt inputs itself (same pointer and ld; BFP8_ERR_SHAPE with
+ * another ld), but outputs never overlap each other, and no other overlap is
+ * allowed; codes and scales overlap nothing.
  *
  * Codes.  The calls named ..._quantize write their result as the quantisers of
  * bfp8.h would write the unrounded float32 result: q [rows][ldq] with scales s
@@ -41,12 +41,12 @@
  * cols is a multiple of 128, and so is rows where qt is given.  One case is
  * defined that those quantisers leave open, as a result's size is not the
  * caller's to choose: a BFP8_CODES_F32 group of 0 < amax < 2^-117 counts as
- * zeros, with s = 1.  Inf or NaN in a group make its codes and scale
- * unspecified (no fault; nothing else is affected but, for the norm, its whole
- * row); with BFP8_DEBUG (see bfp8.h) these calls scan their inputs for them.
+ * zeros, with s = 1.  Inf or NaN make the codes and scales of the groups that
+ * hold them unspecified, and nothing else (no fault); a norm's row with one is
+ * such a value in all its columns.  With BFP8_DEBUG (see bfp8.h) these calls scan
+ * their inputs for them.
  *
- * Sizes.  rows < 2^31 (rows of a norm's gradient: any such); 2^32 vectors of 8
- * values or more in an activation, or 2^23 tiles of 128 x 128 values in a call
+ * Sizes.  rows < 2^31; 2^32 vectors of 8 values or more in an activation, or 2^23 tiles of 128 x 128 values in a call
  * that writes qt, are refused with BFP8_ERR_SHAPE.  Empty problems launch
  * nothing, except that the gradient of a norm's weight over no rows is written
  * as zeros.
@@ -139,7 +139,8 @@ bfp8_status bfp8_swiglu_backward_quantize(const void* dh, int64_t lddh, const vo
  * values go: out, which may be g itself (same pointer and ld).  Pointers need
  * their elements' alignment only; data that is 16-byte aligned is read faster.
  * Every job is validated before anything is launched; jobs without elements may
- * have NULL pointers.  rows * cols < 2^40.
+ * have NULL pointers.  rows * cols < 2^40.  Outputs must not overlap each other
+ * or another job's g; a tensor in two jobs counts twice in the norm.
  */
 typedef struct {
   const void* g;

@@ -67,6 +67,12 @@ def test_norm_refusals(L, quantize):
     assert call(rows=0, x=None, w=None, rstd=None) == OK
     # rows that no 32-bit count of their vectors holds
     assert call(rows=(1 << 31) - 128, cols=256) == SHAPE
+    # a result over an input whose rows lie elsewhere
+    Q = P + 0x10000
+    assert call(residual=Q, ldres=256, sum=Q, ldsum=264) == SHAPE
+    assert call(residual=Q, ldres=256, sum=P, ldsum=264) == SHAPE
+    if not quantize:
+        assert call(ldy=264) == SHAPE and call(residual=Q, ldres=256, sum=P, ldsum=256) == SHAPE
 
 
 def codes_refusals(call, cols):
@@ -113,6 +119,11 @@ def test_glu_refusals(L, grad, quantize):
     for name, ld in tensors:
         assert call(**{name: None}) == NULL and call(**{name: P + 2}) == ALIGN, name
         assert call(**{ld: 248}) == SHAPE and call(**{ld: 260}) == ALIGN, ld
+    if not quantize:  # two results in one place, or over an input whose rows lie elsewhere
+        Q = P + 0x10000
+        assert call(ldg=264) == SHAPE and call(ldu=264) == SHAPE
+        if grad:
+            assert call() == SHAPE and call(dup=Q, lddh=264) == SHAPE and call(dup=Q, ldg=264) == SHAPE
     assert call(dt=9) == DTYPE and call(rows=-1) == SHAPE and call(cols=-1) == SHAPE
     assert call(rows=1 << 31) == SHAPE and call(rows=(1 << 31) - 128) == SHAPE
     assert call(rows=0, gate=None, up=None) == OK
@@ -127,6 +138,8 @@ def test_norm_gradient_refusals(L):
     assert call(dsum=P + 4) == ALIGN and call(ws=P + 4) == ALIGN
     for ld in ("lddy", "ldr", "lddsum", "lddx"):
         assert call(**{ld: 248}) == SHAPE and call(**{ld: 260}) == ALIGN, ld
+    for ld in ("lddy", "ldr", "lddsum"):  # dx over an input whose rows lie elsewhere
+        assert call(**{ld: 264}) == SHAPE
     need = L.bfp8_rmsnorm_backward_workspace_bytes(128, 256)
     assert need > 0 and need % (256 * 4) == 0
     assert call(ws=None) == WS and call(nbytes=need - 1) == WS

@@ -182,3 +182,32 @@ def test_many_rows_of_few_channels():
     y, _, _ = bfp8.rmsnorm(x, w)
     for at in (slice(0, 300), slice(1 << 20, (1 << 20) + 300), slice(rows - 300, rows)):
         assert torch.equal(y[at], bfp8.rmsnorm(x[at], w)[0])
+
+
+def test_more_rows_than_workgroups():
+    """Rows of several waves, in turn: each turn's sums are its own."""
+    rows = (1 << 16) + 4000
+    x = torch.randn((rows, 1104), device="cuda", generator=generator(13)).to(BF)
+    x[1 << 16:] *= 100  # a sum taken from another turn's row would show
+    w = torch.ones(1104, device="cuda")
+    y, _, rstd = bfp8.rmsnorm(x, w)
+    for at in (slice(0, 4000), slice(1 << 16, rows)):
+        part = bfp8.rmsnorm(x[at], w)
+        assert torch.equal(y[at], part[0]) and torch.equal(rstd[at], part[2])
+
+
+@pytest.mark.parametrize("scales", ["fp32", "mx32"])
+def test_codes_into_given_buffers(scales):
+    """Codes in rows of a larger buffer: the same bytes, and nothing beside them."""
+    x, residual, w, _ = inputs(256, 384, BF, 14, True)
+    *want, r, rstd = bfp8.rmsnorm_quantize(x, w, residual, scales=scales, transposed=True)
+    room = [torch.full((256, 512), 9, dtype=torch.uint8, device="cuda"),
+            torch.full((384, 304), 9, dtype=torch.uint8, device="cuda")]
+    s, st = (torch.empty_like(t) for t in (want[1], want[3]))
+    total, stat = torch.empty_like(residual), torch.empty_like(rstd)
+    out = bfp8.rmsnorm_quantize(x, w, residual, scales=scales, transposed=True, q=room[0][:, 64:448], s=s,
+                                qt=room[1][:, 32:288], st=st, sum_out=total, rstd=stat)
+    for a, b in zip(out, (*want, r, rstd)):
+        assert torch.equal(a, b)
+    assert torch.all(room[0][:, :64] == 9) and torch.all(room[0][:, 448:] == 9)
+    assert torch.all(room[1][:, :32] == 9) and torch.all(room[1][:, 288:] == 9)

@@ -77,7 +77,8 @@ def test_refusals_of_the_binding():
                  lambda: bfp8.rmsnorm_backward(x, x, w, torch.ones(64, device="cuda")),
                  lambda: bfp8.swiglu(x, x[:, :128]), lambda: bfp8.swiglu(x, x.float()),
                  lambda: bfp8.GradClip([x.half()]), lambda: bfp8.GradClip([x.t()]),
-                 lambda: bfp8.GradClip([x], [x.float()]), lambda: bfp8.GradClip([x], []),
+                 lambda: bfp8.GradClip([x], [x.float()]), lambda: bfp8.GradClip([x, w, x]),
+                 lambda: bfp8.GradClip([x, x.clone()], [x.clone(), x]), lambda: bfp8.GradClip([x], []),
                  lambda: bfp8.GradClip([x]).clip(1.0, norm=torch.ones(1)),
                  lambda: bfp8.GradClip([x]).norm(out=torch.ones(2, device="cuda"))):
         with pytest.raises(ValueError):
