@@ -25,6 +25,7 @@ struct NormArgs {
   int64_t rows;
   int cols;
   float eps;
+  bool large;  // set by the launch: the rows are read past the caches
 };
 bfp8_status launch_rmsnorm(const NormArgs& a, bfp8_in_dtype dt, hipStream_t stream);
 bfp8_status launch_rmsnorm_quantize(const NormArgs& a, bfp8_in_dtype dt, bfp8_code_format format,

@@ -65,14 +65,20 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs 
   float w[NV][8];
   if (OUT != kStats) load_weight<TPR, NV>(a.w, a.w_f32, lane, a.cols, w);
   int turn = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR; row < a.rows;
+  const int64_t place = a.large ? xcd_run(blockIdx.x, gridDim.x) : blockIdx.x;
+  for (int64_t row = place * kRows + threadIdx.x / TPR; row < a.rows;
        row += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
     Raw8<T> x[NV], y[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TPR + lane) * 8, n = valid8(c, a.cols);
-      x[j].load(a.x, row * a.ldx + c, n);
-      if (a.residual != nullptr) y[j].load(a.residual, row * a.ldres + c, n);
+      if (a.large && n == 8) {
+        x[j].load_once(a.x, row * a.ldx + c);
+        if (a.residual != nullptr) y[j].load_once(a.residual, row * a.ldres + c);
+      } else {
+        x[j].load(a.x, row * a.ldx + c, n);
+        if (a.residual != nullptr) y[j].load(a.residual, row * a.ldres + c, n);
+      }
     }
     float r[NV][8], square = 0.0f;
 #pragma unroll
@@ -125,8 +131,15 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs 
    : (cols) <= 8192 ? [&] { constexpr int P = 512, V = 2; return CALL; }()        \
                     : [&] { constexpr int P = 1024, V = 2; return CALL; }())
 
+// Above this many bytes of x bf16 rows are read past the caches, in runs of an XCD: 67
+// MB and as much of residual to values took 43 us so and 47 otherwise (54 in runs
+// through the caches), with both codes inside MLPBlock's forward pass 706 and 724,
+// where 17 MB made that pass 207 and 206.
+constexpr int64_t kLargeRows = int64_t(32) << 20;
+
 template <typename T, int TPR, int NV, int OUT>
-bfp8_status launch_rows(const NormArgs& a, const CodesOut& o, hipStream_t stream) {
+bfp8_status launch_rows(NormArgs a, const CodesOut& o, hipStream_t stream) {
+  a.large = sizeof(T) == 2 && a.rows * a.cols * 2 > kLargeRows;
   constexpr int kRows = block_threads(TPR) / TPR;
   const int64_t blocks = std::min<int64_t>((a.rows + kRows - 1) / kRows, 1 << 16);
   return launch(norm_rows_kernel<T, TPR, NV, OUT>, dim3(static_cast<unsigned>(blocks)),
@@ -186,9 +199,9 @@ bfp8_status quantize_typed(const NormArgs& a, bfp8_code_format format, const Cod
 
 // ---- gradient ------------------------------------------------------------------
 
-
 // Rows in turn, the weight and this workgroup's share of dw in registers; the
-// waves' shares meet in LDS at the end and leave as one row of `partial`.
+// waves' shares meet in LDS at the end and leave as one row of `partial`.  The
+// rows are read past the caches (16384 x 2048 51 us, and 55 through them).
 template <typename T, int TPR, int NV>
 __global__ __launch_bounds__(block_threads(TPR)) void norm_grad_kernel(NormGradArgs a) {
   constexpr int kThreads = block_threads(TPR), kRows = kThreads / TPR;
@@ -208,9 +221,15 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_grad_kernel(NormGradA
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TPR + lane) * 8, n = valid8(c, a.cols);
-      dy[j].load(a.dy, row * a.lddy + c, n);
-      r[j].load(a.r, row * a.ldr + c, n);
-      if (a.dsum != nullptr) ds[j].load(a.dsum, row * a.lddsum + c, n);
+      if (n == 8) {
+        dy[j].load_once(a.dy, row * a.lddy + c);
+        r[j].load_once(a.r, row * a.ldr + c);
+        if (a.dsum != nullptr) ds[j].load_once(a.dsum, row * a.lddsum + c);
+      } else {
+        dy[j].load(a.dy, row * a.lddy + c, n);
+        r[j].load(a.r, row * a.ldr + c, n);
+        if (a.dsum != nullptr) ds[j].load(a.dsum, row * a.lddsum + c, n);
+      }
     }
     const float rstd = a.rstd[row];
     float dot = 0.0f;
@@ -271,7 +290,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_grad_kernel(NormGradA
 constexpr int kSumSlots = 128;
 __global__ __launch_bounds__(8 * kSumSlots) void norm_grad_sum_kernel(const float* partial, int groups,
                                                                       int cols, float* dw) {
-  __shared__ __attribute__((aligned(16))) float sums[kSumSlots][32];
+  __shared__ __attribute__((aligned(16))) float sums[kSumSlots][36];  // 32, and 4 to spread a column
   const int lane = threadIdx.x & 7, slot = threadIdx.x >> 3;
   const int64_t ld = norm_grad_ld(cols);
   const int c = blockIdx.x * 32 + lane * 4;

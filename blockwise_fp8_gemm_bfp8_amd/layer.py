@@ -63,7 +63,7 @@ def _matrix(t, name, device=None, shape=None, dtype=None):
 def _rows_empty(rows, cols, dtype, device, align):
     """_padded_empty, without its view where there is nothing to pad."""
     if cols % align == 0 and cols:
-        return torch.empty((rows, cols), dtype=dtype, device=device)
+        return torch.empty(rows, cols, dtype=dtype, device=device)  # sooner parsed than a tuple
     return _padded_empty(rows, cols, dtype, device, align)
 
 
@@ -96,7 +96,7 @@ def _scales(t, name, rows, cols, scales, device, place):
     shape = (rows, cols // 32) if scales == "mx32" else (cols // 128, rows)
     if t is None:
         if scales == "fp32":
-            return torch.empty(shape, dtype=torch.float32, device=place)
+            return torch.empty(*shape, dtype=torch.float32, device=place)
         return _scale_bytes(*shape, place)
     dtype = torch.float32 if scales == "fp32" else torch.uint8
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != device:
