@@ -282,7 +282,8 @@ struct TileShared {
 };
 constexpr int kTileThreads = 512;
 
-template <int FORMAT>
+// ROWS false: the transposed codes alone.
+template <int FORMAT, bool ROWS>
 __device__ __forceinline__ void emit_tile(const CodesOut& o, int64_t m0, int64_t c0,
                                           const float (&v)[4][8], TileShared& sh) {
   typedef Codes<FORMAT> F;
@@ -291,26 +292,27 @@ __device__ __forceinline__ void emit_tile(const CodesOut& o, int64_t m0, int64_t
   S* s = static_cast<S*>(o.s);
   S* st = static_cast<S*>(o.st);
 
-  // row groups
-  uint32_t am[4];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) am[u] = size8(v[u]);
-  group_max<F::kGroupLen>(am);
-  const int mine = tid & 3;
-  const uint32_t m01 = mine & 1 ? am[1] : am[0], m23 = mine & 1 ? am[3] : am[2];
-  float inv;
-  const S sc = result_scale<F::kRule>(__uint_as_float(mine & 2 ? m23 : m01), inv);
-  const float invs[4] = {quad_broadcast<0>(inv), quad_broadcast<1>(inv), quad_broadcast<2>(inv),
-                         quad_broadcast<3>(inv)};
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    *reinterpret_cast<uint2*>(o.q + (m0 + 4 * rsub + u) * o.ldq + c0 + lane16 * 8) =
-        encode8_within(v[u], invs[u]);
   S* rowscale = reinterpret_cast<S*>(sh.rowscale);
-  if (F::kMajor) {
-    if (lane16 < 4) rowscale[4 * rsub + lane16] = sc;
-  } else {
-    s[(m0 + 4 * rsub + mine) * (o.cols / 32) + c0 / 32 + lane16 / 4] = sc;
+  if constexpr (ROWS) {
+    uint32_t am[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) am[u] = size8(v[u]);
+    group_max<F::kGroupLen>(am);
+    const int mine = tid & 3;
+    const uint32_t m01 = mine & 1 ? am[1] : am[0], m23 = mine & 1 ? am[3] : am[2];
+    float inv;
+    const S sc = result_scale<F::kRule>(__uint_as_float(mine & 2 ? m23 : m01), inv);
+    const float invs[4] = {quad_broadcast<0>(inv), quad_broadcast<1>(inv), quad_broadcast<2>(inv),
+                           quad_broadcast<3>(inv)};
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<uint2*>(o.q + (m0 + 4 * rsub + u) * o.ldq + c0 + lane16 * 8) =
+          encode8_within(v[u], invs[u]);
+    if (F::kMajor) {
+      if (lane16 < 4) rowscale[4 * rsub + lane16] = sc;
+    } else {
+      s[(m0 + 4 * rsub + mine) * (o.cols / 32) + c0 / 32 + lane16 / 4] = sc;
+    }
   }
 
   // column maxima of the wave's 16 tokens
@@ -326,7 +328,8 @@ __device__ __forceinline__ void emit_tile(const CodesOut& o, int64_t m0, int64_t
   sh.colmax[wave][lane16 * 8 + kk + 4] = high;
   __syncthreads();
 
-  if (F::kMajor && tid >= 128 && tid < 256) s[c0 / 128 * o.rows + m0 + tid - 128] = rowscale[tid - 128];
+  if (ROWS && F::kMajor && tid >= 128 && tid < 256)
+    s[c0 / 128 * o.rows + m0 + tid - 128] = rowscale[tid - 128];
   if (F::kGroupLen == 32 || tid < 128) {
     const int c = tid & 127, p = tid >> 7;
     uint32_t m = max(sh.colmax[2 * p][c], sh.colmax[2 * p + 1][c]);

@@ -112,8 +112,8 @@ __global__ __launch_bounds__(kTileThreads) void glu_tile_kernel(GluArgs a, unsig
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  emit_tile<FORMAT>(o, m0, c0, x, sh);
-  if (GRAD) emit_tile<FORMAT>(o, m0, a.cols + c0, y, sh);
+  emit_tile<FORMAT, true>(o, m0, c0, x, sh);
+  if (GRAD) emit_tile<FORMAT, true>(o, m0, a.cols + c0, y, sh);
 }
 
 // Above this many bytes of gate the loads of bf16 values go past the caches: 201 MB

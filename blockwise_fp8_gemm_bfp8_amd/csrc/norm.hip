@@ -51,8 +51,9 @@ __device__ __forceinline__ void load_weight(const void* w, bool f32, int lane, i
 
 constexpr int block_threads(int tpr) { return tpr <= 64 ? 256 : tpr; }
 
-// What a pass over the rows leaves beside r and rstd.
-constexpr int kStats = -2, kValues = -1;  // otherwise a bfp8_code_format
+// What a pass over the rows leaves beside r and rstd: values, or else the row codes
+// of a bfp8_code_format.
+constexpr int kValues = -1;
 
 // TPR threads a row, NV vectors of 8 values a thread: vector j of a thread
 // holds columns 8 (j TPR + lane), so that a wave's loads are contiguous and 16
@@ -63,7 +64,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs 
   constexpr int kRows = block_threads(TPR) / TPR;  // of a workgroup at once
   const int lane = threadIdx.x % TPR;
   float w[NV][8];
-  if (OUT != kStats) load_weight<TPR, NV>(a.w, a.w_f32, lane, a.cols, w);
+  load_weight<TPR, NV>(a.w, a.w_f32, lane, a.cols, w);
   int turn = 0;
   const int64_t place = a.large ? xcd_run(blockIdx.x, gridDim.x) : blockIdx.x;
   for (int64_t row = place * kRows + threadIdx.x / TPR; row < a.rows;
@@ -105,7 +106,6 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs 
     square = row_sum<TPR>(square, parts[turn]);
     const float rstd = 1.0f / sqrtf(square / static_cast<float>(a.cols) + a.eps);
     if (lane == 0) a.rstd[row] = rstd;
-    if (OUT == kStats) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * TPR + lane) * 8, n = valid8(c, a.cols);
@@ -147,17 +147,17 @@ bfp8_status launch_rows(NormArgs a, const CodesOut& o, hipStream_t stream) {
 }
 template <typename T, int OUT>
 bfp8_status launch_rows_of(const NormArgs& a, const CodesOut& o, hipStream_t stream) {
-  // one vector a thread is as fast where all is written (43 us), and sooner done
-  // with a few rows (16 x 2048 3.3 us against 3.7) and with odd ones (5003 x 1111
-  // 11.0 against 12.9), but not where r alone is (32.4 against 31.4)
-  return BFP8_WITH_ROW(a.cols, (OUT == kStats ? 128 : 256), (OUT == kStats ? 2 : 1),
-                       (launch_rows<T, P, V, OUT>(a, o, stream)));
+  // one vector a thread is as fast with many rows (16384 x 2048 to values 43 us), and
+  // sooner done with a few (16 x 2048 3.3 us against 3.7) and with odd ones (5003 x
+  // 1111 11.0 against 12.9)
+  return BFP8_WITH_ROW(a.cols, 256, 1, (launch_rows<T, P, V, OUT>(a, o, stream)));
 }
 
-// Both layouts' codes of a tile from r and the rows' statistics.  A row's
-// statistics need the whole row and a token group needs 128 rows, which no
-// workgroup holds at once: so r is read a second time, from the last-level
-// cache where it fits.
+// The transposed codes of a tile from r and the rows' statistics.  Statistics need
+// the whole row and a token group needs 128 rows, which no workgroup holds at once:
+// so r is read a second time, from the last-level cache where it fits.  (The row
+// codes leave with the statistics, in whole rows: 16384 x 2048 55 us, and 57 with
+// them in these tiles.)
 template <typename T, int FORMAT>
 __global__ __launch_bounds__(kTileThreads) void norm_tile_kernel(const void* r, int64_t ldr,
                                                                  const float* rstd, const void* w,
@@ -180,15 +180,14 @@ __global__ __launch_bounds__(kTileThreads) void norm_tile_kernel(const void* r, 
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[u][k] = raw[u].get(k) * rs * wv[k];
   }
-  emit_tile<FORMAT>(o, m0, c0, v, sh);
+  emit_tile<FORMAT, false>(o, m0, c0, v, sh);
 }
 
 template <typename T>
 bfp8_status quantize_typed(const NormArgs& a, bfp8_code_format format, const CodesOut& o,
                            hipStream_t stream) {
-  if (o.qt == nullptr) return BFP8_WITH_FORMAT(format, (launch_rows_of<T, F>(a, o, stream)));
-  const bfp8_status st = launch_rows_of<T, kStats>(a, o, stream);
-  if (st != BFP8_OK) return st;
+  const bfp8_status st = BFP8_WITH_FORMAT(format, (launch_rows_of<T, F>(a, o, stream)));
+  if (st != BFP8_OK || o.qt == nullptr) return st;
   const bool added = a.residual != nullptr;
   const int64_t col_tiles = a.cols / 128, tiles = a.rows / 128 * col_tiles;
   return BFP8_WITH_FORMAT(

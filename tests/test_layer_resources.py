@@ -10,7 +10,7 @@ import pytest
 from blockwise_fp8_gemm_bfp8_amd import build as bfp8_build
 
 
-@pytest.mark.parametrize("source,least", [("norm.hip", 80), ("glu.hip", 20), ("clip.hip", 5)])
+@pytest.mark.parametrize("source,least", [("norm.hip", 70), ("glu.hip", 20), ("clip.hip", 5)])
 def test_kernels_do_not_spill(source, least, tmp_path):
     if shutil.which("hipcc") is None and not os.path.exists("/opt/rocm/bin/hipcc"):
         pytest.skip("hipcc not available")
