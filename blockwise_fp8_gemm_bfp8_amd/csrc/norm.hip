@@ -104,7 +104,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs 
       for (int i = 0; i < 8; ++i) square = fmaf(r[j][i], r[j][i], square);
     }
     square = row_sum<TPR>(square, parts[turn]);
-    const float rstd = 1.0f / sqrtf(square / static_cast<float>(a.cols) + a.eps);
+    const float rstd = __builtin_amdgcn_rsqf(fmaf(square, a.per_col, a.eps));  // within 2^-23
     if (lane == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -118,17 +118,17 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs 
   }
 }
 
-// The threads P and vectors V of a row; those of 1025 to 2048 columns, where the
-// kernels differ most, as given.  Two vectors a thread read a large matrix as fast
-// as one or four (16384 x 2048 to values 43 us each, 4096 x 8192 44 to 45) and a
-// few rows sooner than four (16 x 8192 3.9 us against 4.5).
-#define BFP8_WITH_ROW(cols, P2048, V2048, CALL)                                   \
-  ((cols) <= 128    ? [&] { constexpr int P = 16, V = 1; return CALL; }()         \
-   : (cols) <= 512  ? [&] { constexpr int P = 64, V = 1; return CALL; }()         \
-   : (cols) <= 1024 ? [&] { constexpr int P = 64, V = 2; return CALL; }()         \
-   : (cols) <= 2048 ? [&] { constexpr int P = P2048, V = V2048; return CALL; }()  \
-   : (cols) <= 4096 ? [&] { constexpr int P = 256, V = 2; return CALL; }()        \
-   : (cols) <= 8192 ? [&] { constexpr int P = 512, V = 2; return CALL; }()        \
+// The threads P and vectors V of a row: one vector a thread as far as a workgroup
+// goes.  (Two or four were as fast only before large rows went past the caches: 16384 x
+// 2048 with both codes 55 us, 57 and 61; 32768 x 1024 53 and, with two, 58; 8192 x 4096
+// 56 and 59.  A few rows are done sooner, too: 16 x 2048 3.3 us against 3.7 and 4.1.)
+#define BFP8_WITH_ROW(cols, CALL)                                             \
+  ((cols) <= 128    ? [&] { constexpr int P = 16, V = 1; return CALL; }()     \
+   : (cols) <= 512  ? [&] { constexpr int P = 64, V = 1; return CALL; }()     \
+   : (cols) <= 1024 ? [&] { constexpr int P = 128, V = 1; return CALL; }()    \
+   : (cols) <= 2048 ? [&] { constexpr int P = 256, V = 1; return CALL; }()    \
+   : (cols) <= 4096 ? [&] { constexpr int P = 512, V = 1; return CALL; }()    \
+   : (cols) <= 8192 ? [&] { constexpr int P = 1024, V = 1; return CALL; }()   \
                     : [&] { constexpr int P = 1024, V = 2; return CALL; }())
 
 // Above this many bytes of x bf16 rows are read past the caches, in runs of an XCD: 67
@@ -139,6 +139,7 @@ constexpr int64_t kLargeRows = int64_t(32) << 20;
 
 template <typename T, int TPR, int NV, int OUT>
 bfp8_status launch_rows(NormArgs a, const CodesOut& o, hipStream_t stream) {
+  a.per_col = 1.0f / static_cast<float>(a.cols);
   a.large = sizeof(T) == 2 && a.rows * a.cols * 2 > kLargeRows;
   constexpr int kRows = block_threads(TPR) / TPR;
   const int64_t blocks = std::min<int64_t>((a.rows + kRows - 1) / kRows, 1 << 16);
@@ -147,10 +148,7 @@ bfp8_status launch_rows(NormArgs a, const CodesOut& o, hipStream_t stream) {
 }
 template <typename T, int OUT>
 bfp8_status launch_rows_of(const NormArgs& a, const CodesOut& o, hipStream_t stream) {
-  // one vector a thread is as fast with many rows (16384 x 2048 to values 43 us), and
-  // sooner done with a few (16 x 2048 3.3 us against 3.7) and with odd ones (5003 x
-  // 1111 11.0 against 12.9)
-  return BFP8_WITH_ROW(a.cols, 256, 1, (launch_rows<T, P, V, OUT>(a, o, stream)));
+  return BFP8_WITH_ROW(a.cols, (launch_rows<T, P, V, OUT>(a, o, stream)));
 }
 
 // The transposed codes of a tile from r and the rows' statistics.  Statistics need
@@ -323,13 +321,20 @@ bfp8_status launch_grad(const NormGradArgs& a, hipStream_t stream) {
   return launch(norm_grad_sum_kernel, dim3((a.cols + 31) / 32), dim3(8 * kSumSlots), stream,
                 a.partial, static_cast<int>(groups), a.cols, a.dw);
 }
+// Two vectors a thread, whose sums of dw stay in registers (one: 32768 x 1024 49 to 85
+// us, 42 with two).  bf16 rows of up to 2048 a wave each, so that none waits for another
+// wave (16384 x 2048 43 us against 45); fp32 rows need too many registers for that (8192
+// x 2048 58 us, 53 with two waves a row).
 template <typename T>
 bfp8_status launch_grad_of(const NormGradArgs& a, hipStream_t stream) {
-  // bf16 rows of up to 2048 a wave each, so that none waits for another wave (16384
-  // x 2048 43 us against 45); fp32 rows need too many registers for that (8192 x
-  // 2048 58 us, 53 with two waves a row)
-  return BFP8_WITH_ROW(a.cols, (sizeof(T) == 2 ? 64 : 128), (sizeof(T) == 2 ? 4 : 2),
-                       (launch_grad<T, P, V>(a, stream)));
+  constexpr bool kBf16 = sizeof(T) == 2;
+  return a.cols <= 128    ? launch_grad<T, 16, 1>(a, stream)
+         : a.cols <= 512  ? launch_grad<T, 64, 1>(a, stream)
+         : a.cols <= 1024 ? launch_grad<T, 64, 2>(a, stream)
+         : a.cols <= 2048 ? launch_grad<T, kBf16 ? 64 : 128, kBf16 ? 4 : 2>(a, stream)
+         : a.cols <= 4096 ? launch_grad<T, 256, 2>(a, stream)
+         : a.cols <= 8192 ? launch_grad<T, 512, 2>(a, stream)
+                          : launch_grad<T, 1024, 2>(a, stream);
 }
 
 }  // namespace
