@@ -10,18 +10,23 @@ namespace bfp8 {
 namespace {
 
 // Tensors of one launch: passed by value, so that no table has to be copied to
-// the device (3.9 KB of the 4 KB that arguments may take).
-constexpr int kJobs = 64;
-struct GradBatch {
-  const void* g[kJobs];
-  void* out[kJobs];
-  int64_t rows[kJobs], cols[kJobs], ldg[kJobs], ldo[kJobs];
-  int64_t per_row[kJobs];         // vectors that cover a row wherever it starts
-  unsigned first[kJobs + 1];      // first chunk of each job
-  int f32;                        // of all jobs of the launch
-  int n;
+// the device.  Arguments lie in host memory, where each cache line that a kernel
+// touches first costs it a trip: the chunks' bounds are together, and what belongs to a
+// job is one line.
+struct BatchJob {
+  const void* g;
+  void* out;
+  int64_t rows, cols, ldg, ldo;
+  int64_t per_row;  // vectors that cover a row wherever it starts
+  int64_t fill;  // up to the line
 };
-static_assert(sizeof(GradBatch) + 64 <= 4096, "kernel arguments");
+constexpr int kJobs = 58;
+struct GradBatch {
+  int n;
+  unsigned first[kJobs + 1];  // first chunk of each job
+  BatchJob job[kJobs];
+};
+static_assert(sizeof(BatchJob) == 64 && sizeof(GradBatch) + 64 <= 4096, "kernel arguments");
 
 // Vectors of a chunk: 2, 4 and 8 a thread took 186, 188 and 196 us for 101 million
 // float32 values, and 50 to 51 for 50 million in bf16.
@@ -86,18 +91,18 @@ __device__ __forceinline__ int lead_of(const T* p) {
 // (most are), or null.
 template <typename T>
 __device__ __forceinline__ const T* whole_chunk(const GradBatch& b, int j, int64_t base) {
-  const T* p = static_cast<const T*>(b.g[j]);
+  const T* p = static_cast<const T*>(b.job[j].g);
   const int64_t c = base * Vector<T>::N - lead_of(p);
-  return b.rows[j] == 1 && c >= 0 && c + kChunk * Vector<T>::N <= b.cols[j] ? p + c : nullptr;
+  return b.job[j].rows == 1 && c >= 0 && c + kChunk * Vector<T>::N <= b.job[j].cols ? p + c : nullptr;
 }
 
 // Row, first column and first element of the row of vector `at` of job j.
 template <typename T>
 __device__ __forceinline__ const T* place(const GradBatch& b, int j, int64_t at, int64_t& row,
                                           int64_t& c) {
-  row = b.rows[j] == 1 ? 0 : at / b.per_row[j];
-  const T* p = static_cast<const T*>(b.g[j]) + row * b.ldg[j];
-  c = (at - row * b.per_row[j]) * Vector<T>::N - lead_of(p);
+  row = b.job[j].rows == 1 ? 0 : at / b.job[j].per_row;
+  const T* p = static_cast<const T*>(b.job[j].g) + row * b.job[j].ldg;
+  c = (at - row * b.job[j].per_row) * Vector<T>::N - lead_of(p);
   return p;
 }
 
@@ -123,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void grad_square_kernel(GradBatch b, doub
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) v[u].load(p + (u * kThreads + threadIdx.x) * N);
     } else {
-      const int64_t count = b.rows[j] * b.per_row[j];
+      const int64_t count = b.job[j].rows * b.job[j].per_row;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int64_t at = base + u * kThreads + threadIdx.x;
@@ -131,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void grad_square_kernel(GradBatch b, doub
         if (at >= count) continue;
         int64_t row, c;
         const T* q = place<T>(b, j, at, row, c);
-        v[u].load_part(q, c, b.cols[j]);
+        v[u].load_part(q, c, b.job[j].cols);
       }
     }
 #pragma unroll
@@ -166,6 +171,10 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const double* parti
   if (threadIdx.x == 0) norm[0] = v;
 }
 
+__device__ __forceinline__ float factor_of(float norm, float max_norm) {
+  return norm > max_norm ? max_norm / norm : norm <= max_norm ? 1.0f : norm;  // NaN stays NaN
+}
+
 // Scales by max_norm over the norm: a given one, or (OWN) that of `partial`'s n
 // sums, which every workgroup adds up for itself and the first one writes down.
 template <typename T, bool OWN>
@@ -180,7 +189,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, float
   } else {
     v = norm[0];
   }
-  const float c = v > max_norm ? max_norm / v : v <= max_norm ? 1.0f : v;  // NaN stays NaN
+  const float c = factor_of(v, max_norm);
   // Last chunks first, which the norm read last, and results past the caches:
   // what is left of the gradients in the last-level cache is read from there
   // (225 -> 194 us for 101 million float32 values, 59 -> 50 for 50 million in bf16).
@@ -189,12 +198,12 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, float
   for (unsigned turn = blockIdx.x; turn <= last; turn += gridDim.x) {
     const unsigned chunk = last - turn;
     while (chunk < b.first[j]) --j;
-    if (c == 1.0f && b.out[j] == b.g[j]) continue;  // in place, and nothing to change
+    if (c == 1.0f && b.job[j].out == b.job[j].g) continue;  // in place, and nothing to change
     const int64_t base = static_cast<int64_t>(chunk - b.first[j]) * kChunk;
     Vector<T> x[kUnroll];
     const T* p = whole_chunk<T>(b, j, base);
-    T* o = static_cast<T*>(b.out[j]);
-    if (p != nullptr) o += p - static_cast<const T*>(b.g[j]);
+    T* o = static_cast<T*>(b.job[j].out);
+    if (p != nullptr) o += p - static_cast<const T*>(b.job[j].g);
     if (p != nullptr && lead_of(o) == 0) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) x[u].load(p + (u * kThreads + threadIdx.x) * N);
@@ -205,7 +214,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, float
       }
       continue;
     }
-    const int64_t count = b.rows[j] * b.per_row[j], cols = b.cols[j];
+    const int64_t count = b.job[j].rows * b.job[j].per_row, cols = b.job[j].cols;
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t at = base + u * kThreads + threadIdx.x;
       if (at >= count) break;
@@ -213,7 +222,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(GradBatch b, float
       const T* q = place<T>(b, j, at, row, col);
       x[0].load_part(q, col, cols);
       x[0].scale(c);
-      x[0].store_part(static_cast<T*>(b.out[j]) + row * b.ldo[j], col, cols);
+      x[0].store_part(static_cast<T*>(b.job[j].out) + row * b.job[j].ldo, col, cols);
     }
   }
 }
@@ -236,35 +245,34 @@ constexpr unsigned kMaxScaleGroups = 1u << 20;
 // none) get a launch of their own.
 constexpr int64_t kOwnSums = 2 * kMaxGroups;
 
+void add_job(GradBatch& b, const bfp8_grad_job& j, int64_t chunks) {
+  b.job[b.n] = BatchJob{j.g, j.out, j.rows, j.cols, j.ldg, j.ldo, vectors_per_row(j), 0};
+  b.first[b.n + 1] = b.first[b.n] + static_cast<unsigned>(chunks);
+  ++b.n;
+}
+
+void clear(GradBatch& b) {
+  b.n = 0;
+  b.first[0] = 0;
+}
+
 // The jobs as launches of up to kJobs tensors of one type and fewer than 2^31
-// chunks: calls f(batch, workgroups), first for bf16 jobs and then for fp32.
+// chunks: calls f(batch, its type, workgroups), first for bf16 jobs, then for fp32.
 template <typename F>
 bfp8_status for_batches(const bfp8_grad_job* jobs, int64_t n, unsigned most, F&& f) {
   for (int f32 = 0; f32 < 2; ++f32) {
     GradBatch b;
-    b.n = 0;
-    b.f32 = f32;
-    b.first[0] = 0;
+    clear(b);
     for (int64_t i = 0; i <= n; ++i) {
       const bool mine = i < n && (jobs[i].dt == BFP8_IN_F32) == (f32 == 1);
       const int64_t chunks = mine ? chunks_of(jobs[i]) : 0;
-      const bool full = b.n == kJobs || (mine && b.first[b.n] + chunks >= (int64_t(1) << 31));
+      const bool full = b.n == kJobs || b.first[b.n] + chunks >= (int64_t(1) << 31);
       if (b.n > 0 && (full || i == n)) {
-        const bfp8_status st = f(b, std::min(b.first[b.n], most));
+        const bfp8_status st = f(b, f32 == 1, std::min(b.first[b.n], most));
         if (st != BFP8_OK) return st;
-        b.n = 0;
+        clear(b);
       }
-      if (chunks == 0) continue;
-      const bfp8_grad_job& j = jobs[i];
-      b.g[b.n] = j.g;
-      b.out[b.n] = j.out;
-      b.rows[b.n] = j.rows;
-      b.cols[b.n] = j.cols;
-      b.ldg[b.n] = j.ldg;
-      b.ldo[b.n] = j.ldo;
-      b.per_row[b.n] = vectors_per_row(j);
-      b.first[b.n + 1] = b.first[b.n] + static_cast<unsigned>(chunks);
-      ++b.n;
+      if (chunks > 0) add_job(b, jobs[i], chunks);
     }
   }
   return BFP8_OK;
@@ -274,7 +282,7 @@ bfp8_status for_batches(const bfp8_grad_job* jobs, int64_t n, unsigned most, F&&
 
 size_t grad_norm_workspace(const bfp8_grad_job* jobs, int64_t n) {
   size_t groups = 0;
-  for_batches(jobs, n, kMaxGroups, [&](const GradBatch&, unsigned g) {
+  for_batches(jobs, n, kMaxGroups, [&](const GradBatch&, bool, unsigned g) {
     groups += g;
     return BFP8_OK;
   });
@@ -283,8 +291,8 @@ size_t grad_norm_workspace(const bfp8_grad_job* jobs, int64_t n) {
 
 bfp8_status launch_grad_clip(const bfp8_grad_job* jobs, int64_t n, float* norm, float max_norm,
                              hipStream_t stream) {
-  return for_batches(jobs, n, kMaxScaleGroups, [&](const GradBatch& b, unsigned groups) {
-    return launch(b.f32 ? grad_scale_kernel<float, false> : grad_scale_kernel<uint16_t, false>,
+  return for_batches(jobs, n, kMaxScaleGroups, [&](const GradBatch& b, bool f32, unsigned groups) {
+    return launch(f32 ? grad_scale_kernel<float, false> : grad_scale_kernel<uint16_t, false>,
                   dim3(groups), dim3(kThreads), stream, b, norm, max_norm, nullptr, int64_t(0));
   });
 }
@@ -293,10 +301,10 @@ bfp8_status launch_grad_clip(const bfp8_grad_job* jobs, int64_t n, float* norm, 
 static bfp8_status launch_squares(const bfp8_grad_job* jobs, int64_t n, double* partial,
                                   int64_t& n_sums, hipStream_t stream) {
   n_sums = 0;
-  return for_batches(jobs, n, kMaxGroups, [&](const GradBatch& b, unsigned groups) {
+  return for_batches(jobs, n, kMaxGroups, [&](const GradBatch& b, bool f32, unsigned groups) {
     double* p = partial + n_sums;
     n_sums += groups;
-    return launch(b.f32 ? grad_square_kernel<float> : grad_square_kernel<uint16_t>, dim3(groups),
+    return launch(f32 ? grad_square_kernel<float> : grad_square_kernel<uint16_t>, dim3(groups),
                   dim3(kThreads), stream, b, p);
   });
 }
@@ -318,8 +326,8 @@ bfp8_status launch_grad_norm_clip(const bfp8_grad_job* jobs, int64_t n, float* n
     st = launch(grad_norm_kernel, dim3(1), dim3(kThreads), stream, partial, n_sums, norm);
     return st != BFP8_OK ? st : launch_grad_clip(jobs, n, norm, max_norm, stream);
   }
-  return for_batches(jobs, n, kMaxScaleGroups, [&](const GradBatch& b, unsigned groups) {
-    return launch(b.f32 ? grad_scale_kernel<float, true> : grad_scale_kernel<uint16_t, true>,
+  return for_batches(jobs, n, kMaxScaleGroups, [&](const GradBatch& b, bool f32, unsigned groups) {
+    return launch(f32 ? grad_scale_kernel<float, true> : grad_scale_kernel<uint16_t, true>,
                   dim3(groups), dim3(kThreads), stream, b, norm, max_norm, partial, n_sums);
   });
 }

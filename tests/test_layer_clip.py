@@ -48,35 +48,42 @@ def test_clip(sizes, dtypes, max_norm):
         assert torch.equal(o, p)
 
 
+@pytest.mark.parametrize("others", [False, True])  # one workgroup does it all, or many
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("lead,out_lead", [(0, 0), (1, 1), (3, 3), (1, 0), (0, 5), (2, 7)])
-def test_any_alignment(dtype, lead, out_lead):
+def test_any_alignment(dtype, lead, out_lead, others):
     n = 5003
+    large = [torch.randn(300000, device="cuda", generator=generator(77)).to(dtype)] if others else []
     base = torch.randn(n + 16, device="cuda", generator=generator(lead)).to(dtype)
     room = torch.full((n + 16,), 9.0, dtype=dtype, device="cuda")
     g, o = base[lead:lead + n], room[out_lead:out_lead + n]
-    norm = bfp8.clip_grads([g], 1.0, out=[o])
-    check([g], [o], norm, 1.0)
+    clipped = [torch.empty_like(t) for t in large]
+    norm = bfp8.clip_grads([g] + large, 1.0, out=[o] + clipped)
+    check([g] + large, [o] + clipped, norm, 1.0)
     assert torch.all(room[:out_lead] == 9) and torch.all(room[out_lead + n:] == 9)
 
 
+@pytest.mark.parametrize("others", [False, True])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows,cols,ld,ldo", [(37, 100, 104, 104), (37, 100, 101, 128), (5, 2047, 2048, 2051),
                                               (300, 1, 3, 1), (1, 65, 200, 65), (64, 64, 64, 72)])
-def test_strided(dtype, rows, cols, ld, ldo):
+def test_strided(dtype, rows, cols, ld, ldo, others):
+    large = [torch.randn(300000, device="cuda", generator=generator(78)).to(dtype)] if others else []
     base = torch.randn((rows, ld), device="cuda", generator=generator(ld)).to(dtype)
     room = torch.full((rows, ldo), 9.0, dtype=dtype, device="cuda")
     g, o = base[:, :cols], room[:, :cols]
-    norm = bfp8.clip_grads([g], 1.0, out=[o])
-    check([g], [o], norm, 1.0)
+    clipped = [torch.empty_like(t) for t in large]
+    norm = bfp8.clip_grads([g] + large, 1.0, out=[o] + clipped)
+    check([g] + large, [o] + clipped, norm, 1.0)
     assert torch.all(room[:, cols:] == 9)
     rest = base[:, cols:].clone()
-    bfp8.clip_grads([g], 1.0)
+    bfp8.clip_grads([g] + large, 1.0)
     assert torch.equal(g, o) and torch.equal(base[:, cols:], rest)
 
 
 def test_more_sums_than_a_workgroup_adds_up():
-    """Three launches of 1024 partial sums each: the norm has a launch of its own."""
+    """Launches of up to 1024 partial sums each, more than 2048 in all: the norm has a
+    launch of its own."""
     n = 1024 * 2048 * 4 // 64 + 5
     grads = [torch.randn(n, device="cuda", generator=generator(i)) for i in range(3 * 64)]
     plan = bfp8.GradClip(grads, [torch.empty_like(g) for g in grads])
@@ -89,8 +96,8 @@ def test_more_sums_than_a_workgroup_adds_up():
 
 
 def test_sizes_that_float32_squares_lose():
-    for scale in (1e30, 1e-30):
-        g = torch.randn(5000, device="cuda", generator=generator(1)) * scale
+    for scale, n in ((1e30, 5000), (1e-30, 5000), (1e30, 500000), (1e-30, 500000)):
+        g = torch.randn(n, device="cuda", generator=generator(1)) * scale
         check([g], [g], bfp8.grad_norm([g]), float("inf"))
     g = torch.full((70000,), 1e-4, device="cuda")
     g[0] = 1e30
@@ -98,8 +105,9 @@ def test_sizes_that_float32_squares_lose():
 
 
 def test_infinities_and_nan():
-    for bad, norm_is in ((float("inf"), torch.isinf), (float("nan"), torch.isnan)):
-        g = torch.ones(100, device="cuda")
+    for bad, norm_is, n in ((float("inf"), torch.isinf, 100), (float("nan"), torch.isnan, 100),
+                            (float("inf"), torch.isinf, 200000), (float("nan"), torch.isnan, 200000)):
+        g = torch.ones(n, device="cuda")
         g[3] = bad
         norm = bfp8.clip_grads([g], 1.0)
         assert norm_is(norm)
