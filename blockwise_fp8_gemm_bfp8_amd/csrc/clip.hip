@@ -18,7 +18,7 @@ struct BatchJob {
   void* out;
   int64_t rows, cols, ldg, ldo;
   int64_t per_row;  // vectors that cover a row wherever it starts
-  int64_t fill;  // up to the line
+  int64_t fill;     // up to the line
 };
 constexpr int kJobs = 58;
 struct GradBatch {

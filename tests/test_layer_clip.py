@@ -48,7 +48,7 @@ def test_clip(sizes, dtypes, max_norm):
         assert torch.equal(o, p)
 
 
-@pytest.mark.parametrize("others", [False, True])  # one workgroup does it all, or many
+@pytest.mark.parametrize("others", [False, True])  # a large tensor beside it or none
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("lead,out_lead", [(0, 0), (1, 1), (3, 3), (1, 0), (0, 5), (2, 7)])
 def test_any_alignment(dtype, lead, out_lead, others):
