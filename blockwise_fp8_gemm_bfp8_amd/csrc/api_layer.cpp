@@ -2,6 +2,7 @@
 // points of include/bfp8_layer.h.  As in api.cpp, every argument is checked on
 // the host before the first HIP call.
 
+#include <float.h>
 #include <math.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -84,7 +85,8 @@ bfp8_status check_norm_sizes(bfp8_in_dtype wdt, bfp8_in_dtype dt, int64_t rows, 
   return st == BFP8_OK && cols > kMaxNormCols ? BFP8_ERR_SHAPE : st;
 }
 
-bool valid_eps(float eps) { return eps > 0.0f && !isinf(eps); }
+// From the smallest normal number on: the reciprocal root takes what is less for 0.
+bool valid_eps(float eps) { return eps >= FLT_MIN && !isinf(eps); }
 
 bfp8_status check_jobs(const bfp8_grad_job* jobs, int64_t n, bool outputs) {
   if (n < 0) return BFP8_ERR_SHAPE;

@@ -70,7 +70,7 @@ typedef enum { BFP8_CODES_F32 = 0, BFP8_CODES_E8M0 = 1, BFP8_CODES_E8M0_32 = 2 }
  * The norm is of r as stored, so that the gradient, which reads r, is that of
  * what was computed.  sum [rows][ldsum] receives r (the residual stream that
  * goes on), rstd [rows] float32 the statistics.
- * cols <= 16384; eps > 0 and finite.  Rows whose mean square passes float32's
+ * cols <= 16384; eps a positive normal number (2^-126 or more).  Rows whose mean square passes float32's
  * range (values near 1e19) are outside the contract.  Rows of zeros give zeros.
  */
 bfp8_status bfp8_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldres,

@@ -62,8 +62,9 @@ def test_norm_refusals(L, quantize):
     assert call(dt=2) == DTYPE and call(wdt=7) == DTYPE
     assert call(rows=-1) == SHAPE and call(cols=-1) == SHAPE and call(rows=1 << 31) == SHAPE
     assert call(cols=16512, ldx=16512) == SHAPE
-    for eps in (0.0, -1.0, NAN, INF):
+    for eps in (0.0, -1.0, NAN, INF, 2.0 ** -127, 2.0 ** -149):
         assert call(eps=eps) == SHAPE, eps
+    assert call(eps=2.0 ** -126, rows=0) == OK
     assert call(rows=0, x=None, w=None, rstd=None) == OK
     # rows that no 32-bit count of their vectors holds
     assert call(rows=(1 << 31) - 128, cols=256) == SHAPE

@@ -76,6 +76,22 @@ def test_rows_of_zeros_and_one_value():
     assert torch.all(q[0] == 0) and torch.all(s[:, 0] == 1) and torch.all(s[1] == 1)
 
 
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e30])
+def test_smallest_and_large_eps(eps):
+    """Rows of zeros under the smallest eps, whose root is 2^63, and rows whose squares
+    vanish beside it or outweigh it."""
+    x = torch.zeros((4, 300), device="cuda")
+    x[1:] = torch.randn((3, 300), device="cuda", generator=generator(8))
+    x[2] *= 1e-17
+    x[3] *= 1e15
+    w = torch.ones(300, device="cuda")
+    y, r, rstd = bfp8.rmsnorm(x, w, eps=eps)
+    want, stat = layer.rmsnorm(f64(x), f64(w), eps)
+    close(rstd, stat, NORM * stat)
+    close(y, want, NORM * np.abs(want) + 2.0 ** -126)  # results below that may vanish
+    assert torch.all(y[0] == 0)
+
+
 @pytest.mark.parametrize("scales", ["fp32", "mx128", "mx32"])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows,cols,transposed", [(1, 128, False), (7, 512, False), (33, 2048, False),
