@@ -126,7 +126,8 @@ bfp8_status bfp8_rmsnorm(const void* x, int64_t ldx, const void* residual, int64
                    static_cast<int>(cols), eps, 0.0f, false};
   if ((st = check_norm(a, wdt, dt)) != BFP8_OK) return st;
   if ((st = check_matrix(y, ldy, cols, bytes_of(dt))) != BFP8_OK) return st;
-  if (shifted(y, ldy, x, ldx, rows) || (residual != nullptr && (shifted(y, ldy, residual, ldres, rows) || y == sum)))
+  if (shifted(y, ldy, x, ldx, rows) ||
+      (residual != nullptr && (shifted(y, ldy, residual, ldres, rows) || y == sum)))
     return BFP8_ERR_SHAPE;
   return launch_rmsnorm(a, dt, stream);
 }

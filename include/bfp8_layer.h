@@ -46,10 +46,10 @@
  * such a value in all its columns.  With BFP8_DEBUG (see bfp8.h) these calls scan
  * their inputs for them.
  *
- * Sizes.  rows < 2^31; 2^32 vectors of 8 values or more in an activation, or 2^23 tiles of 128 x 128 values in a call
- * that writes qt, are refused with BFP8_ERR_SHAPE.  Empty problems launch
- * nothing, except that the gradient of a norm's weight over no rows is written
- * as zeros.
+ * Sizes.  rows < 2^31; 2^32 vectors of 8 values or more in an activation, or
+ * 2^23 tiles of 128 x 128 values in a call that writes qt, are refused with
+ * BFP8_ERR_SHAPE.  Empty problems launch nothing, except that the gradient of a
+ * norm's weight over no rows is written as zeros.
  */
 #ifndef BFP8_LAYER_H_
 #define BFP8_LAYER_H_
