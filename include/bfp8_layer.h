@@ -106,6 +106,9 @@ size_t bfp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  * element by element for gate, up, h [rows][cols]; gate and up are usually the
  * halves of the rows of one projection.  Gradients:
  *   dgate = dh up sigma(gate) (1 + gate (1 - sigma(gate))),  dup = dh silu(gate).
+ * float32 values of silu are within 2^-20 of themselves for gates down to -88.7;
+ * below, where exp(-gate) passes float32's range, silu and its gradient are 0.
+ * The results of bf16 inputs are those of the same values in float32, rounded.
  */
 bfp8_status bfp8_swiglu(const void* gate, int64_t ldg, const void* up, int64_t ldu,
                         bfp8_in_dtype dt, int64_t rows, int64_t cols, void* h, int64_t ldh,
