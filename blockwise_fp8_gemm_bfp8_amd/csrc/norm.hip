@@ -3,6 +3,8 @@
 // value, so a row is read once, kept in registers between its sum of squares
 // and its use, and nothing but outputs is written.
 
+#include <float.h>
+
 #include <algorithm>
 
 #include "layer.h"
@@ -21,7 +23,7 @@ __device__ __forceinline__ float row16_sum(float v) {
 
 // Sum over the TPR threads of a row, in every one of them.  Rows of more than
 // a wave are a workgroup's, and its `parts` in LDS are free again only after
-// the next barrier: two are used in turn.
+// the next barrier: two are used in turn (and a third between two of those).
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* parts) {
   v = row16_sum(v);
@@ -60,7 +62,7 @@ constexpr int kValues = -1;
 // lanes hold a 128-group.
 template <typename T, int TPR, int NV, int OUT>
 __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs a, CodesOut o) {
-  __shared__ float parts[2][TPR <= 64 ? 1 : TPR / 64];
+  __shared__ float parts[3][TPR <= 64 ? 1 : TPR / 64];
   constexpr int kRows = block_threads(TPR) / TPR;  // of a workgroup at once
   const int lane = threadIdx.x % TPR;
   float w[NV][8];
@@ -104,7 +106,22 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs 
       for (int i = 0; i < 8; ++i) square = fmaf(r[j][i], r[j][i], square);
     }
     square = row_sum<TPR>(square, parts[turn]);
-    const float rstd = __builtin_amdgcn_rsqf(fmaf(square, a.per_col, a.eps));  // within 2^-23
+    // The sum of a row whose mean is within float32's range may be past it: again with
+    // values 2^-72 of their size, of which all that matter to such a sum are normal.  (The
+    // condition is the same in all of the row's threads.)
+    float unit = 1.0f, eps = a.eps;
+    if (__builtin_expect(square > FLT_MAX, 0)) {
+      unit = 0x1p-72f;
+      eps = eps * unit * unit;
+      square = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) square = fmaf(r[j][i] * unit, r[j][i] * unit, square);
+      square = row_sum<TPR>(square, parts[2]);
+    }
+    const float rstd =
+        __builtin_amdgcn_rsqf(fmaf(square, a.per_col, eps)) * unit;  // within 2^-23
     if (lane == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
