@@ -123,7 +123,7 @@ bfp8_status bfp8_rmsnorm(const void* x, int64_t ldx, const void* residual, int64
   if (!valid_eps(eps)) return BFP8_ERR_SHAPE;
   if (rows == 0 || cols == 0) return BFP8_OK;
   const NormArgs a{x, ldx, residual, ldres, w, wdt == BFP8_IN_F32, sum, ldsum, y, ldy, rstd, rows,
-                   static_cast<int>(cols), eps, 0.0f, false};
+                   static_cast<int>(cols), eps, 0.0f, 0.0f, false};
   if ((st = check_norm(a, wdt, dt)) != BFP8_OK) return st;
   if ((st = check_matrix(y, ldy, cols, bytes_of(dt))) != BFP8_OK) return st;
   if (shifted(y, ldy, x, ldx, rows) ||
@@ -144,7 +144,7 @@ bfp8_status bfp8_rmsnorm_quantize(const void* x, int64_t ldx, const void* residu
   if ((st = check_codes(o, format)) != BFP8_OK) return st;
   if (rows == 0 || cols == 0) return BFP8_OK;
   const NormArgs a{x, ldx, residual, ldres, w, wdt == BFP8_IN_F32, sum, ldsum, nullptr, 0, rstd,
-                   rows, static_cast<int>(cols), eps, 0.0f, false};
+                   rows, static_cast<int>(cols), eps, 0.0f, 0.0f, false};
   if ((st = check_norm(a, wdt, dt)) != BFP8_OK) return st;
   if (debug_checks_enabled()) {
     if ((st = scan(x, ldx, dt, rows, cols, stream)) != BFP8_OK) return st;

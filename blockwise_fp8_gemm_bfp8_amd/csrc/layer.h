@@ -25,8 +25,9 @@ struct NormArgs {
   int64_t rows;
   int cols;
   float eps;
-  float per_col;  // set by the launch: 1 / cols,
-  bool large;     // and whether the rows are read past the caches
+  // set by the launch: 1 / cols as a sum of two, and whether the rows are read past the caches
+  float per_col, per_col_low;
+  bool large;
 };
 bfp8_status launch_rmsnorm(const NormArgs& a, bfp8_in_dtype dt, hipStream_t stream);
 bfp8_status launch_rmsnorm_quantize(const NormArgs& a, bfp8_in_dtype dt, bfp8_code_format format,

@@ -1,5 +1,5 @@
 """The norm's statistics: rows whose squares' sum passes float32 although their mean does
-not."""
+not, and how exact the reciprocal root is.  U = 2^-24."""
 import numpy as np
 import pytest
 import torch
@@ -85,3 +85,21 @@ def test_infinity_and_nan_stay_in_their_rows():
     keep = [0, 2, 3, 5]
     assert torch.equal(y[keep], clean[0][keep]) and torch.equal(rstd[keep], clean[2][keep])
     assert torch.isnan(y[1, 3]) and torch.all(torch.isnan(y[4]))
+
+
+@pytest.mark.parametrize("cols", [1020, 2048, 8160, 16372, 16380])
+def test_the_reciprocal_root_of_an_exact_sum(cols):
+    """Integers whose squares add up exactly: what is left is one rounding of mean + eps
+    (half of U in the root), one of its product with the estimate (half of U again), and the
+    last one: 2 U.  (The estimate's own 2 U are squared away.)"""
+    rows = 20000
+    gen = generator(6)
+    x = torch.randint(-4, 5, (rows, cols), device="cuda", generator=gen).float()
+    x[:, 0] = torch.arange(rows, device="cuda") % 1000
+    exact = x.double().square().sum(1)
+    assert torch.all(exact < 2 ** 24)
+    _, _, rstd = bfp8.rmsnorm(x, torch.ones(cols, device="cuda"), eps=EPS)
+    want = (exact / cols + float(np.float32(EPS))).rsqrt()
+    worst = ((rstd.double() - want).abs() / want).max().item() / U
+    print(f"[norm] {cols}: {worst:.2f}", flush=True)
+    assert worst <= 2.0, worst
