@@ -277,21 +277,63 @@ def swiglu_backward_quantize(dh: torch.Tensor, gate: torch.Tensor, up: torch.Ten
 
 # ---- the norm of all gradients, and clipping ----------------------------------------
 
+def _span(at, rows, cols, ld, size, *_):
+    """(first byte, rows, bytes a row, bytes from row to row) of a matrix."""
+    if rows == 1 or ld == cols:
+        rows, cols, ld = 1, rows * cols, rows * cols
+    return at, rows, cols * size, ld * size
+
+
+def _meet(a, b):
+    """Whether two such places share a byte."""
+    if a[1] > b[1]:
+        a, b = b, a
+    (start, rows, width, ld), (other, other_rows, other_width, other_ld) = a, b
+
+    def row_meets(at, low, high):
+        # rows m of `low` to `high`, at m ld, of the other place: one around byte `at`?
+        first = (at - other_width - other) // other_ld + 1
+        last = -((other - at - width) // other_ld) - 1
+        return max(first, low) <= min(last, high)
+
+    if ld == other_ld:  # only the difference of two rows' numbers counts
+        return row_meets(start, 1 - rows, other_rows - 1)
+    return any(row_meets(start + i * ld, 0, other_rows - 1) for i in range(rows))
+
+
+def _refuse_overlaps(places):
+    """What a job writes is its own: neither another's nor a shifted part of its own
+    gradient.  places: (first byte, rows, cols, row stride, bytes a value, number, "grads"
+    or "out")."""
+    reach, end = [], 0  # the places since the last gap, and where they end
+    for place in sorted(places):
+        at, rows, cols, ld, size, i, kind = place
+        if at >= end:
+            reach.clear()
+        for p in reach:
+            if (kind == "out" or p[6] == "out") and _meet(_span(*p), _span(*place)):
+                raise ValueError(f"{p[6]}[{p[5]}] and {kind}[{i}] share memory: one writes what the other "
+                                 "holds")
+        reach.append(place)
+        end = max(end, at + ((rows - 1) * ld + cols) * size)
+
+
 class GradClip:
     """The global norm and the clipping of a fixed list of gradients (bfloat16 or
     float32, dense, or 2-D with rows of unit stride) whose buffers stay: the
     table of their places is made once.
 
     out   where the clipped gradients go, tensors of the same shapes and types;
-          None: in place.  A place written twice, or another gradient's, is
-          refused, so a gradient is listed once.
+          None: in place.  Memory that is written twice, or that is another
+          gradient's or a shifted part of the same one, is refused: a gradient
+          is listed once.  (grad_norm writes nothing and counts it twice.)
 
     norm() is the square root of the sum of all squares (float32 0-d device
     tensor); clip(max_norm) scales by max_norm / norm where the norm exceeds
     max_norm.  Neither synchronises.  A norm over several ranks: sum norm()**2
     over them and give its root to clip()."""
 
-    def __init__(self, grads, out=None):
+    def __init__(self, grads, out=None, _clips=True):
         self.grads = list(grads)
         self.out = self.grads if out is None else list(out)
         if len(self.out) != len(self.grads):
@@ -299,25 +341,28 @@ class GradClip:
         if not self.grads:
             raise ValueError("no gradients")
         self.device, self._device = self.grads[0].get_device(), self.grads[0].device
-        self._jobs = (GradJob * len(self.grads))()
+        self._jobs, places = (GradJob * len(self.grads))(), []
         for i, (g, o) in enumerate(zip(self.grads, self.out)):
             rows, cols, ldg = self._place(g, f"grads[{i}]")
             if o is not g and (o.shape != g.shape or o.dtype != g.dtype):
                 raise ValueError(f"out[{i}] must be {g.dtype} {list(g.shape)}, got {o.dtype} "
                                  f"{list(o.shape)}")
-            orows, ocols, ldo = self._place(o, f"out[{i}]")
-            if (orows, ocols) != (rows, cols):  # one of the two is dense, the other strided
-                rows, cols = g.shape
-                ldg, ldo = (t.stride(0) if rows > 1 else cols for t in (g, o))
-            self._jobs[i] = GradJob(g.data_ptr(), o.data_ptr(), rows, cols, ldg, ldo,
-                                    DTYPES[g.dtype])
-        source = {g.data_ptr(): i for i, g in enumerate(self.grads) if g.numel()}
-        written = set()
-        for i, o in enumerate(self.out):
-            at = o.data_ptr()
-            if o.numel() and (at in written or source.get(at, i) != i):
-                raise ValueError(f"out[{i}] is written twice, or another gradient's place")
-            written.add(at)
+            at, size, dtype = g.data_ptr(), g.element_size(), DTYPES[g.dtype]
+            if o is g:
+                out, ldo = at, ldg
+            else:
+                out = o.data_ptr()
+                orows, ocols, ldo = self._place(o, f"out[{i}]")
+                if (orows, ocols) != (rows, cols):  # one of the two is dense, the other strided
+                    rows, cols = g.shape
+                    ldg, ldo = (t.stride(0) if rows > 1 else cols for t in (g, o))
+            self._jobs[i] = GradJob(at, out, rows, cols, ldg, ldo, dtype)
+            if rows and cols:
+                places.append((out, rows, cols, ldo, size, i, "out"))
+                if out != at or ldo != ldg:
+                    places.append((at, rows, cols, ldg, size, i, "grads"))
+        if _clips:
+            _refuse_overlaps(places)
         n = lib().bfp8_grad_norm_workspace_bytes(self._jobs, len(self._jobs))
         if n == _INVALID:
             raise ValueError("invalid gradients")
@@ -379,7 +424,7 @@ class GradClip:
 
 def grad_norm(grads) -> torch.Tensor:
     """The global norm of the gradients; see GradClip."""
-    return GradClip(grads).norm()
+    return GradClip(grads, _clips=False).norm()
 
 
 def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
