@@ -83,8 +83,10 @@ class AttentionBlock:
             b["r"], b["rstd"] = new((M, hidden), bf), new((M,), f32)
             b["dn"], b["dw_norm"] = new((M, hidden), bf), new((hidden,), f32)
             b["norm_ws"] = new((rmsnorm_backward_workspace_bytes(M, hidden),), u8)
-        need = max(gemm_workspace_bytes("NT", "act_km", "act_km", rows, hidden, M),
-                   gemm_workspace_bytes("NT", "act_km", "act_km", hidden, E, M), 16)
+        gemms = [("NT", "act_km", "block", M, rows, hidden), ("NT", "act_km", "block", M, hidden, E),
+                 ("NN", "act_km", "block", M, E, hidden), ("NN", "act_km", "block", M, hidden, rows),
+                 ("NT", "act_km", "act_km", rows, hidden, M), ("NT", "act_km", "act_km", hidden, E, M)]
+        need = max(*(gemm_workspace_bytes(*g) for g in gemms), 16)
         b["gemm_ws"] = new((need,), u8)
         q, k, v = self._heads(b["qkv"])
         need = max(attention_workspace_bytes(q, k, v, cu, cu, backward=back) for back in (False, True))

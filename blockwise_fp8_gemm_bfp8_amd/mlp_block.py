@@ -60,8 +60,10 @@ class MLPBlock:
         b["dh"], b["dn"], b["dx"] = new((M, ffn), bf), new((M, hidden), bf), new((M, hidden), bf)
         b["dw_gate_up"], b["dw_down"] = new((2 * ffn, hidden), bf), new((hidden, ffn), bf)
         b["dw_norm"] = new((hidden,), f32)
-        need = max(gemm_workspace_bytes("NT", "act_km", "act_km", 2 * ffn, hidden, M),
-                   gemm_workspace_bytes("NT", "act_km", "act_km", hidden, ffn, M),
+        gemms = [("NT", "act_km", "block", M, 2 * ffn, hidden), ("NT", "act_km", "block", M, hidden, ffn),
+                 ("NN", "act_km", "block", M, ffn, hidden), ("NN", "act_km", "block", M, hidden, 2 * ffn),
+                 ("NT", "act_km", "act_km", 2 * ffn, hidden, M), ("NT", "act_km", "act_km", hidden, ffn, M)]
+        need = max(*(gemm_workspace_bytes(*g) for g in gemms),
                    rmsnorm_backward_workspace_bytes(M, hidden), 16)
         b["ws"] = new((need,), u8)
 
