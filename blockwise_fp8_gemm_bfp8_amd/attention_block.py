@@ -117,8 +117,12 @@ class AttentionBlock:
     def _check_norm(self, t, name):
         if (t is None) != (self.w_norm is None):
             raise ValueError(f"{name} comes with a norm's weight, and only with one")
-        if t is not None:
-            self._check_rows(t, name)
+        if t is None:
+            return
+        self._check_rows(t, name)
+        if t.dtype != torch.bfloat16 or t.stride(1) != 1:  # dr is read last: not in mid-pass
+            raise ValueError(f"{name} must be bfloat16 rows of unit stride, got {t.dtype} with strides "
+                             f"{t.stride()}")
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor = None):
         """y [tokens][hidden] of x [tokens][hidden] (bfloat16); the buffers keep

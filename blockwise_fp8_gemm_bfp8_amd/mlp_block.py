@@ -73,6 +73,8 @@ class MLPBlock:
         if t.shape != y.shape or t.device != y.device or t.dtype != y.dtype:
             raise ValueError(f"{name} must be {y.dtype} {list(y.shape)} on {y.device}, got {t.dtype} "
                              f"{list(t.shape)} on {t.device}")
+        if t.stride(1) != 1:  # dr is read last: not in mid-pass
+            raise ValueError(f"{name} must have rows of unit stride, got strides {t.stride()}")
 
     def quantize_weights(self):
         """Codes of both weights, once per optimizer step (and before the first forward)."""
