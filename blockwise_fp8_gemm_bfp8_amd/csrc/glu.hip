@@ -74,8 +74,8 @@ __global__ __launch_bounds__(256) void glu_values_kernel(GluArgs a, unsigned per
 
 // Row groups: 16 lanes a chunk of 128 columns, 16 rows a workgroup, whose
 // K-block-major scales lie side by side; workgroups along the rows, in runs of
-// an XCD.  (Down the columns, and with loads through the caches, the 16384 x 6144
-// activation took 118 us and its gradient 172; so 87 and 129.)
+// an XCD.  (The 16384 x 6144 activation 89 us and its gradient 145; down the columns with
+// loads through the caches 119 and 178, along the rows with such loads 94 and 144.)
 template <typename T, int FORMAT, bool GRAD>
 __global__ __launch_bounds__(256) void glu_rows_kernel(GluArgs a, unsigned per_row, CodesOut o) {
   const unsigned chunk = xcd_run(blockIdx.x, gridDim.x);
@@ -115,8 +115,7 @@ __global__ __launch_bounds__(kTileThreads) void glu_tile_kernel(GluArgs a, unsig
   }
   // Row by row, each one's results pinned before the next: left to itself the
   // compiler unpacks everything first, 156 registers, and one workgroup fits a
-  // CU (93, two: 236 -> 164 us for the gradient of 16384 x 6144, where computing
-  // dup from the inputs again after dgate has left took 182).
+  // CU (93, two: 238 -> 199 us for the gradient of 16384 x 6144, 60 -> 47 for 4096 x 6144).
   float x[4][8], y[4][8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -136,8 +135,8 @@ __global__ __launch_bounds__(kTileThreads) void glu_tile_kernel(GluArgs a, unsig
 }
 
 // Above this many bytes of gate the loads of bf16 values go past the caches: 201 MB
-// with up took 88 us so and 104 otherwise, where 16 MB with up and dh, read again and
-// again, took 16.8 and 14.3.
+// with as much of up took 99 us so and 107 otherwise (the gradient 174 and 179), where 17
+// MB with up and dh took 15.5 and 14.6.
 constexpr int64_t kLargeGate = int64_t(64) << 20;
 
 template <typename T, bool GRAD>

@@ -142,7 +142,10 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs 
 // The threads P and vectors V of a row: one vector a thread as far as a workgroup
 // goes.  (Two or four were as fast only before large rows went past the caches: 16384 x
 // 2048 with both codes 55 us, 57 and 61; 32768 x 1024 53 and, with two, 58; 8192 x 4096
-// 56 and 59.  A few rows are done sooner, too: 16 x 2048 3.3 us against 3.7 and 4.1.)
+// 56 and 59.  A few rows are done sooner, too: 16 x 2048 3.3 us against 3.7 and 4.1.)  Up
+// to 128 channels 16 lanes, up to 512 a wave: 131072 x 64 11 us, and 33 with a wave a row;
+// 65536 x 512 25, and 36 with two.  (Half of the 16 lanes idle at 64 channels, half of the
+// wave at 256.)
 #define BFP8_WITH_ROW(cols, CALL)                                             \
   ((cols) <= 128    ? [&] { constexpr int P = 16, V = 1; return CALL; }()     \
    : (cols) <= 512  ? [&] { constexpr int P = 64, V = 1; return CALL; }()     \
@@ -153,9 +156,10 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_rows_kernel(NormArgs 
                     : [&] { constexpr int P = 1024, V = 2; return CALL; }())
 
 // Above this many bytes of x bf16 rows are read past the caches, in runs of an XCD: 67
-// MB and as much of residual to values took 43 us so and 47 otherwise (54 in runs
-// through the caches), with both codes inside MLPBlock's forward pass 706 and 724,
-// where 17 MB made that pass 207 and 206.
+// MB and as much of residual to values took 44 us so and 47 otherwise (54 in runs
+// through the caches), to row codes 39 and 44, to both 56 and 61 (without a residual to
+// values 26 and 24); MLPBlock's forward pass over 16384 tokens 706 and 724, over 4096,
+// where x has 17 MB, 207 and 206.
 constexpr int64_t kLargeRows = int64_t(32) << 20;
 
 template <typename T, int TPR, int NV, int OUT>
@@ -343,10 +347,12 @@ bfp8_status launch_grad(const NormGradArgs& a, hipStream_t stream) {
   return launch(norm_grad_sum_kernel, dim3((a.cols + 31) / 32), dim3(8 * kSumSlots), stream,
                 a.partial, static_cast<int>(groups), a.cols, a.dw);
 }
-// Two vectors a thread, whose sums of dw stay in registers (one: 32768 x 1024 49 to 85
-// us, 42 with two).  bf16 rows of up to 2048 a wave each, so that none waits for another
-// wave (16384 x 2048 43 us against 45); fp32 rows need too many registers for that (8192
-// x 2048 58 us, 53 with two waves a row).
+// Two vectors a thread, whose sums of dw stay in registers (32768 x 1024 with dsum 50 us, 80
+// with one in twice the threads).  bf16 rows of up to 2048 a wave each, so that none waits
+// for another wave (16384 x 2048 with dsum 52 us, 76 with two waves a row); fp32 rows need
+// too many registers for that (8192 x 2048 61 us, 54 with two waves).  Few channels as in
+// the forward pass (262144 x 128 with dsum 48 us, 184 with a wave a row; 65536 x 512 48,
+// 147 with two waves).
 template <typename T>
 bfp8_status launch_grad_of(const NormGradArgs& a, hipStream_t stream) {
   constexpr bool kBf16 = sizeof(T) == 2;
