@@ -11,9 +11,10 @@ namespace {
 // 1 / (1 + exp(-g)) with exp(-g) = 2^y e^rho: y = -g H rounded, H the 16 leading bits of
 // log2(e); rho, what H leaves of log2(e) and the rounding leaves of y, is under 5e-4 and
 // goes in as 1 + rho.  A rounded -g log2(e) alone was off by |g| 2^-24, 65 U at g = -87 (U
-// = 2^-24); silu is within 6 U now, and 3.5 U for bf16 gates, whose product with H is
-// exact: there rho takes one instruction, and the bits are the same (16384 x 6144 with row
-// codes 89 us, and 87 without rho; every other call, float32 ones too, within 1 %).
+// = 2^-24); silu is within 6 U now (9 from -87.3 to -88.7, where sigma is subnormal), and
+// 3.5 U for bf16 gates, whose product with H is exact: there rho takes one instruction, and
+// the bits are the same.  (16384 x 6144 with row codes 89 us, and 87 without rho; no call,
+// float32 ones too, lost more than 2 %.)
 //   All of it at 2^-24 of its size, so that the reciprocal stays a normal number until
 // exp(-g) overflows (g = -88.72); from there on the result is 0.
 template <bool F32>
